@@ -72,6 +72,8 @@ enum { PKV_QUANT_NONE = 0x00, PKV_QUANT_PER_TENSOR = 0x01, PKV_QUANT_PER_CHANNEL
 #define PKV_ERRBIT_CSR_PHYS     0x10 /* unpack: physical page id >= num_pages */
 #define PKV_ERRBIT_SPAN         0x20 /* slot mapping: cu_new disagrees with [start, end) */
 #define PKV_ERRBIT_TIMEOUT      0x40 /* an internal pipeline wait gave up (never expected) */
+#define PKV_ERRBIT_NO_BLOCKS    0x80 /* grow: too few free blocks for a sequence */
+#define PKV_ERRBIT_REF_COUNT    0x100 /* shrink: a released block was not referenced */
 
 /* Text of the last error returned on this thread ("" after success). */
 PKV_API const char *pkv_last_error_string(void);
@@ -116,6 +118,62 @@ PKV_API pkv_status pkv_compute_slot_mapping(const int32_t *block_tables, int32_t
                                     int32_t block_size, int32_t num_blocks,
                                     int32_t *slot_mapping, int64_t num_new_tokens,
                                     int32_t *err_flag, void *stream);
+
+/*
+ * pkv_grow_block_tables / pkv_shrink_block_tables -- block tables and slot maps
+ * on the device, from request lengths: what the host allocator does ("Walk the
+ * Shapes First": a sequence takes a block exactly when a position p has
+ * p % block_size == 0; lowest-numbered free block first), without a host round
+ * trip, so that a serving step can be enqueued or captured whole.
+ *
+ * The state is the tables and ref_counts[num_blocks], the number of table
+ * entries that list each block; 0 means free.  A caller that shares a prefix
+ * (whole blocks only) copies the entries and raises their counts itself.
+ *
+ * grow: sequence b goes from starts[b] to ends[b] positions.  It needs
+ *   ceil(ends[b] / block_size) - ceil(starts[b] / block_size) blocks.  Sequences
+ *   are served in order: b gets its blocks if the needs of sequences 0 .. b
+ *   together do not exceed the free blocks (or it needs none).  A served
+ *   sequence's new table entries are written and their counts set to 1.
+ *     block_tables    device int32 [num_seqs, max_blocks_per_seq] (in / out);
+ *                     entries outside a sequence's new range are left as they are
+ *     starts, ends    device int32 [num_seqs], 0 <= starts[b] <= ends[b]
+ *     ref_counts      device int32 [num_blocks] (in / out)
+ *     cu_new          device int32 [num_seqs + 1] (output): running count of new
+ *                     positions, cu_new[0] = 0 (the cu_q of the step's prefill)
+ *     slot_mapping    device int32 [num_new_tokens] (output): the slots of
+ *                     sequence b's new positions from cu_new[b] on, and -1 past
+ *                     cu_new[num_seqs] (the store skips those), so that
+ *                     num_new_tokens may be an upper bound
+ *     workspace       pkv_grow_block_tables_workspace_size bytes, 256-byte
+ *                     aligned; calls that may overlap need one each
+ *   Device errors: a sequence that gets no blocks keeps its counts, its new
+ *   table entries and slots are -1, PKV_ERRBIT_NO_BLOCKS; lengths that are
+ *   negative, decreasing or longer than the table row: slots -1, table as it
+ *   was, PKV_ERRBIT_CONTEXT; a bad entry for the partly filled block that a
+ *   sequence continues in: those slots -1, PKV_ERRBIT_BLOCK_RANGE; more new
+ *   positions than num_new_tokens: the rest is not written, PKV_ERRBIT_SPAN.
+ *
+ * shrink: sequence b goes back from lens[b] to keeps[b] positions (0 releases
+ *   it).  The entries of blocks ceil(keeps[b] / block_size) .. ceil(lens[b] /
+ *   block_size) - 1 become -1 and their counts fall by one; entries that are -1
+ *   already (a sequence that grow did not serve) are skipped.  Device errors:
+ *   bad lengths leave the sequence as it is, PKV_ERRBIT_CONTEXT; an entry
+ *   outside [0, num_blocks) becomes -1, PKV_ERRBIT_BLOCK_RANGE; a count that is
+ *   not positive stays, PKV_ERRBIT_REF_COUNT.
+ *
+ * num_blocks * block_size < 2^31, at most 65535 sequences per call.
+ */
+PKV_API size_t pkv_grow_block_tables_workspace_size(int32_t num_seqs, int32_t num_blocks);
+PKV_API pkv_status pkv_grow_block_tables(int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *starts,
+                                         const int32_t *ends, int32_t num_seqs, int32_t block_size,
+                                         int32_t *ref_counts, int32_t num_blocks, int32_t *cu_new,
+                                         int32_t *slot_mapping, int64_t num_new_tokens, void *workspace,
+                                         size_t workspace_bytes, int32_t *err_flag, void *stream);
+PKV_API pkv_status pkv_shrink_block_tables(int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *keeps,
+                                           const int32_t *lens, int32_t num_seqs, int32_t block_size,
+                                           int32_t *ref_counts, int32_t num_blocks, int32_t *err_flag,
+                                           void *stream);
 
 /*
  * pkv_store_kvcache -- "Step 1: slot_mapping and store_kvcache": with the caches

@@ -33,7 +33,8 @@ PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA, PKV_ERR_OUT_OF_R
 PKV_F32, PKV_F16, PKV_BF16 = 0, 1, 2
 PKV_U32, PKV_U64 = 0, 1
 ERRBIT_SLOT_RANGE, ERRBIT_BLOCK_RANGE, ERRBIT_CONTEXT, ERRBIT_CSR_PAGE, ERRBIT_CSR_PHYS, \
-    ERRBIT_SPAN, ERRBIT_TIMEOUT = 0x01, 0x02, 0x04, 0x08, 0x10, 0x20, 0x40
+    ERRBIT_SPAN, ERRBIT_TIMEOUT, ERRBIT_NO_BLOCKS, ERRBIT_REF_COUNT = \
+    0x01, 0x02, 0x04, 0x08, 0x10, 0x20, 0x40, 0x80, 0x100
 _DTYPE = {torch.float32: PKV_F32, torch.float16: PKV_F16, torch.bfloat16: PKV_BF16}
 
 _vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -77,6 +78,10 @@ _SIGS = {
     "pkv_paged_attention_decode_append_int8": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32,
                                                 _i32, _i32, _i32, _i32, _i32, _f32, ctypes.c_int, _vp, _sz, _vp, _vp],
                                                ctypes.c_int),
+    "pkv_grow_block_tables_workspace_size": ([_i32, _i32], _sz),
+    "pkv_grow_block_tables": ([_vp, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _i64, _vp, _sz, _vp, _vp],
+                              ctypes.c_int),
+    "pkv_shrink_block_tables": ([_vp, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp], ctypes.c_int),
     "pkv_selftest_wait_timeout": ([_vp, ctypes.c_uint32, _vp], ctypes.c_int),
     "pkv_allocator_create": ([_i32, _i32, _vp], ctypes.c_int),
     "pkv_allocator_destroy": ([_vp], None),
@@ -157,6 +162,54 @@ def pkv_compute_slot_mapping(block_tables, starts, ends, cu_new, block_size: int
                                              _ptr(cu_new), B, block_size, num_blocks, _ptr(out), out.numel(),
                                              _ptr(err_flag), _stream(dev, stream)))
     return out
+
+
+def _table_args(block_tables, a, b, ref_counts, names):
+    for t, n in ((block_tables, "block_tables"), (a, names[0]), (b, names[1]), (ref_counts, "ref_counts")):
+        _want(t, torch.int32, n)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    if a.numel() != block_tables.shape[0] or b.numel() != block_tables.shape[0]:
+        raise ValueError(f"{names[0]} and {names[1]} need num_seqs entries")
+    return block_tables.shape
+
+
+def pkv_grow_block_tables(block_tables, starts, ends, ref_counts, block_size: int, *, num_new_tokens: int, cu_new=None,
+                          out=None, workspace=None, err_flag=None, stream=None):
+    """Sequence b grows from starts[b] to ends[b] positions: its new blocks (the
+    lowest free ones, sequences in order) go into block_tables and ref_counts in
+    place.  Returns (cu_new [num_seqs + 1], slot_mapping [num_new_tokens]);
+    num_new_tokens may be an upper bound (slots past the last position are -1)."""
+    dev = _dev(block_tables, starts, ends, ref_counts, cu_new, out, workspace, err_flag)
+    B, max_blocks = _table_args(block_tables, starts, ends, ref_counts, ("starts", "ends"))
+    nb = ref_counts.numel()
+    if cu_new is None:
+        cu_new = (torch.empty if B else torch.zeros)(B + 1, dtype=torch.int32, device=dev)
+    if out is None:
+        out = torch.empty(num_new_tokens, dtype=torch.int32, device=dev)
+    _want(cu_new, torch.int32, "cu_new")
+    _want(out, torch.int32, "out")
+    if cu_new.numel() != B + 1 or out.numel() != num_new_tokens:
+        raise ValueError("cu_new needs num_seqs + 1 entries and out num_new_tokens")
+    if workspace is None:
+        workspace = torch.empty(_lib.pkv_grow_block_tables_workspace_size(B, nb), dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(_lib.pkv_grow_block_tables(_ptr(block_tables), max_blocks, _ptr(starts), _ptr(ends), B, block_size,
+                                          _ptr(ref_counts), nb, _ptr(cu_new), _ptr(out), num_new_tokens,
+                                          _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                          _ptr(err_flag), _stream(dev, stream)))
+    return cu_new, out
+
+
+def pkv_shrink_block_tables(block_tables, keeps, lens, ref_counts, block_size: int, *, err_flag=None, stream=None):
+    """Sequence b goes back from lens[b] to keeps[b] positions: the table entries
+    past the kept blocks become -1 and their blocks' counts fall (in place)."""
+    dev = _dev(block_tables, keeps, lens, ref_counts, err_flag)
+    B, max_blocks = _table_args(block_tables, keeps, lens, ref_counts, ("keeps", "lens"))
+    with torch.cuda.device(dev):
+        _check(_lib.pkv_shrink_block_tables(_ptr(block_tables), max_blocks, _ptr(keeps), _ptr(lens), B, block_size,
+                                            _ptr(ref_counts), ref_counts.numel(), _ptr(err_flag),
+                                            _stream(dev, stream)))
 
 
 def pkv_store_kvcache(key, value, k_cache, v_cache, slot_mapping, *, err_flag=None, stream=None):

@@ -56,6 +56,7 @@
 #include <type_traits>
 
 #include "pkv_internal.h"
+#include "pkv_pack.cuh"
 #include "pkv_pdl.cuh"
 #include "pkv_tc.cuh"
 #include "pkv_tma.cuh"
@@ -69,44 +70,6 @@ constexpr int kQTileBytes = 2 * kQHalf;        // 32 KB
 constexpr uint64_t kPreDeadlineNs = 2000000000ull;
 constexpr float kPreLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.f;  // log2 units: P stays <= 2^8 between rescales
-
-// acc + the low 16-bit value of w (lo) and acc2 + the high one, in f32: the
-// mixed-precision adds take the 16-bit operand as it is (exact widening).
-template <typename T> __device__ __forceinline__ void pair_acc(uint32_t w, float &acc, float &acc2);
-template <> __device__ __forceinline__ void pair_acc<__nv_bfloat16>(uint32_t w, float &acc, float &acc2) {
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-        "add.rn.f32.bf16 %0, lo, %0;\n\tadd.rn.f32.bf16 %1, hi, %1;\n\t}"
-        : "+f"(acc), "+f"(acc2)
-        : "r"(w));
-}
-template <> __device__ __forceinline__ void pair_acc<__half>(uint32_t w, float &acc, float &acc2) {
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-        "add.rn.f32.f16 %0, lo, %0;\n\tadd.rn.f32.f16 %1, hi, %1;\n\t}"
-        : "+f"(acc), "+f"(acc2)
-        : "r"(w));
-}
-
-// max(a, b, c) in one instruction (three-input max; NaN operands are ignored
-// as by fmaxf).
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
-// (x0, x1) * s + c per lane, both fused and rounded once (one packed f32x2 FMA);
-// s2 / c2 hold the same value in both halves.
-__device__ __forceinline__ void fma_x2(float x0, float x1, uint64_t s2, uint64_t c2, float &e0, float &e1) {
-    asm("{\n\t.reg .b64 a, d;\n\tmov.b64 a, {%2, %3};\n\t"
-        "fma.rn.f32x2 d, a, %4, %5;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(e0), "=f"(e1)
-        : "f"(x0), "f"(x1), "l"(s2), "l"(c2));
-}
-
-__device__ __forceinline__ uint64_t splat2(float v) {
-    const uint64_t u = __float_as_uint(v);
-    return u | u << 32;
-}
 
 // Per block size (KEYS keys per block, the S MMA's N), ring depth and query
 // tiles per CTA: the K/V tiles, the shared-memory layout, TMEM columns and
