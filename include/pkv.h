@@ -61,6 +61,34 @@ typedef enum pkv_dtype { PKV_F32 = 0, PKV_F16 = 1, PKV_BF16 = 2 } pkv_dtype;
 /* Width of the CSR index buffers ("BlockTableIndexType" U32 / U64). */
 typedef enum pkv_index_type { PKV_U32 = 0, PKV_U64 = 1 } pkv_index_type;
 
+/* What a cache pool holds: values of the call's pkv_dtype, or 8-bit codes with one
+ * float32 scale per (block, KV head) (see the fp8 and int8 caches below). */
+typedef enum pkv_cache_format { PKV_CACHE_DTYPE = 0, PKV_CACHE_E4M3 = 1, PKV_CACHE_INT8 = 2 } pkv_cache_format;
+
+/*
+ * Score rules of the _mod attention calls.  For the query at position p and key t,
+ * with s = scale * q . K_t, in this order:
+ *   softcap > 0      s = softcap * tanh(s / softcap); 0: none.  Finite, not negative.
+ *   alibi_slopes     device float32 [num_q_heads] or NULL: s -= slope_h * |p - t|
+ *   key_starts       device int32, one per query (prefill: in the order of q's rows;
+ *                    decode: one per sequence) or NULL: keys t < key_starts are not
+ *                    visible.  The start of the query's document, or of its window
+ *                    (p - width + 1); negative counts as 0.
+ *   prefix_lens      device int32 [num_seqs] or NULL (prefill): keys t <
+ *                    prefix_lens[b] are visible to every query of sequence b, beside
+ *                    those up to its own position; keys past the stored span are
+ *                    not.  A decode query stands behind its whole context, so decode
+ *                    ignores it.
+ * A query that sees no key has a zero output row.  A zeroed struct, or NULL, is plain
+ * causal attention.
+ */
+typedef struct pkv_score_mod {
+    float softcap;
+    const float *alibi_slopes;
+    const int32_t *key_starts;
+    const int32_t *prefix_lens;
+} pkv_score_mod;
+
 /* Quantization scheme tags ("Block-Paged KV Cache", Quantization compatibility). */
 enum { PKV_QUANT_NONE = 0x00, PKV_QUANT_PER_TENSOR = 0x01, PKV_QUANT_PER_CHANNEL = 0x02, PKV_QUANT_PER_BLOCK = 0x03 };
 
@@ -460,6 +488,42 @@ PKV_API pkv_status pkv_paged_attention_prefill(void *out, const void *q, const v
                                                int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
                                                int32_t head_dim, int32_t block_size, int32_t num_blocks,
                                                float scale, pkv_dtype dtype, int32_t *err_flag, void *stream);
+
+/*
+ * pkv_paged_attention_prefill_mod -- pkv_paged_attention_prefill with score rules
+ * (`mod`, may be NULL) and over any cache format: chunked prefill of a model with
+ * capped scores, a distance bias, packed documents, local windows or a bidirectional
+ * prefix, and over 8-bit caches.
+ *
+ *   k_scale, v_scale  device float32 [num_blocks, num_kv_heads] for PKV_CACHE_E4M3
+ *                     and PKV_CACHE_INT8 pools, not negative, V scales at
+ *                     most 2^90 (NULL for PKV_CACHE_DTYPE)
+ *   max_q_len         host bound on n_b; the exact maximum gives the best schedule
+ *   workspace         pkv_paged_attention_prefill_mod_workspace_size bytes (may be
+ *                     0), 256-byte aligned, needed during the call only; calls that
+ *                     may overlap need one each
+ *   other arguments as pkv_paged_attention_prefill.
+ * f32 scores, softmax and accumulators.  P enters its product rounded to dtype (f16
+ * over 8-bit caches, whose codes are widened exactly; bf16 queries become f16 under
+ * one power of two per row).  Shapes and alignment as pkv_paged_attention_prefill.  K and V of masked keys may hold
+ * anything in rows of other sequences, past the span, or in front of every visible
+ * key; a non-finite V value that one query of a 256-row tile pair sees may reach
+ * queries of that pair that do not.
+ * Device errors: starts[b] < 0 or a span needing more than max_blocks_per_seq blocks
+ * gives zero rows and PKV_ERRBIT_CONTEXT; n_b < 0 or n_b > max_q_len leaves the
+ * sequence's rows as they were and sets PKV_ERRBIT_CONTEXT; a used block id outside
+ * [0, num_blocks) drops that block's tokens and sets PKV_ERRBIT_BLOCK_RANGE.
+ */
+PKV_API size_t pkv_paged_attention_prefill_mod_workspace_size(int32_t num_seqs, int32_t num_q_heads,
+                                                              int32_t num_kv_heads, int32_t head_dim,
+                                                              int32_t block_size, int32_t max_q_len,
+                                                              int32_t max_blocks_per_seq);
+PKV_API pkv_status pkv_paged_attention_prefill_mod(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
+    pkv_cache_format format, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *starts,
+    const int32_t *cu_q, int32_t num_seqs, int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale, const pkv_score_mod *mod, pkv_dtype dtype,
+    void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream);
 
 /*
  * fp8 (E4M3) paged caches -- "Block-Paged KV Cache", Quantization

@@ -32,6 +32,7 @@ PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA, PKV_ERR_OUT_OF_R
     PKV_ERR_WORKSPACE = range(6)
 PKV_F32, PKV_F16, PKV_BF16 = 0, 1, 2
 PKV_U32, PKV_U64 = 0, 1
+PKV_CACHE_DTYPE, PKV_CACHE_E4M3, PKV_CACHE_INT8 = 0, 1, 2
 ERRBIT_SLOT_RANGE, ERRBIT_BLOCK_RANGE, ERRBIT_CONTEXT, ERRBIT_CSR_PAGE, ERRBIT_CSR_PHYS, \
     ERRBIT_SPAN, ERRBIT_TIMEOUT, ERRBIT_NO_BLOCKS, ERRBIT_REF_COUNT = \
     0x01, 0x02, 0x04, 0x08, 0x10, 0x20, 0x40, 0x80, 0x100
@@ -62,6 +63,10 @@ _SIGS = {
                                         _i64, _vp], ctypes.c_int),
     "pkv_paged_attention_prefill": ([_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
                                      _i32, _f32, ctypes.c_int, _vp, _vp], ctypes.c_int),
+    "pkv_paged_attention_prefill_mod_workspace_size": ([_i32] * 7, _sz),
+    "pkv_paged_attention_prefill_mod": ([_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _vp, _i32, _vp, _vp, _i32, _i32,
+                                         _i32, _i32, _i32, _i32, _i32, _f32, _vp, ctypes.c_int, _vp, _sz, _vp, _vp],
+                                        ctypes.c_int),
     "pkv_quantize_kvcache_fp8": ([_vp, _vp, _vp, _i32, _i32, _i32, _i32, ctypes.c_int, _vp], ctypes.c_int),
     "pkv_store_kvcache_fp8": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i64, _i32, ctypes.c_int, _vp,
                                _vp], ctypes.c_int),
@@ -97,6 +102,12 @@ for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(_lib, _name)
     _fn.argtypes = _args
     _fn.restype = _res
+
+
+class _ScoreMod(ctypes.Structure):
+    """pkv_score_mod"""
+
+    _fields_ = [("softcap", _f32), ("alibi_slopes", _vp), ("key_starts", _vp), ("prefix_lens", _vp)]
 
 
 class PkvError(RuntimeError):
@@ -405,6 +416,82 @@ def pkv_paged_attention_prefill(q, k_cache, v_cache, block_tables, starts, cu_q,
                                                 block_tables.shape[1], _ptr(starts), _ptr(cu_q), B, max_q_len, Hq,
                                                 Hkv, d, bs, nb, float(scale), _DTYPE[q.dtype], _ptr(err_flag),
                                                 _stream(dev, stream)))
+    return out
+
+
+# ----------------------------------------------------------------------------- score rules, any cache format
+_FORMAT = {torch.uint8: PKV_CACHE_E4M3, torch.int8: PKV_CACHE_INT8}
+
+
+def _cache_format(q, k_cache, v_cache, k_scale, v_scale):
+    """The caches' pkv_cache_format, with their scales checked."""
+    if q.dtype not in _DTYPE or k_cache.dtype != v_cache.dtype:
+        raise TypeError("q must be float32/float16/bfloat16 and both caches of one type")
+    if q.dim() != 3 or k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[3] != q.shape[2]:
+        raise ValueError("q [rows, Hq, d], caches [num_blocks, bs, Hkv, d]")
+    fmt = _FORMAT.get(k_cache.dtype, PKV_CACHE_DTYPE)
+    if fmt == PKV_CACHE_DTYPE:
+        if k_cache.dtype != q.dtype:
+            raise TypeError("caches must have the type of q, uint8 (E4M3 codes) or int8")
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("scales belong to 8-bit caches")
+    else:
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is None:
+                raise ValueError(f"{name} is required for an 8-bit cache")
+            _want(t, torch.float32, name)
+            if t.shape != (k_cache.shape[0], k_cache.shape[2]):
+                raise ValueError(f"{name} must be [num_blocks, num_kv_heads]")
+    return fmt
+
+
+def _score_mod(softcap, alibi_slopes, key_starts, prefix_lens, Hq, rows, B):
+    for t, dtype, n, name in ((alibi_slopes, torch.float32, Hq, "alibi_slopes"),
+                              (key_starts, torch.int32, rows, "key_starts"),
+                              (prefix_lens, torch.int32, B, "prefix_lens")):
+        if t is not None:
+            _want(t, dtype, name)
+            if t.numel() != n:
+                raise ValueError(f"{name} needs {n} entries")
+    return _ScoreMod(softcap, *(None if t is None else t.data_ptr() for t in (alibi_slopes, key_starts, prefix_lens)))
+
+
+def pkv_paged_attention_prefill_mod_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                   max_q_len, max_blocks_per_seq) -> int:
+    return int(_lib.pkv_paged_attention_prefill_mod_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                                   block_size, max_q_len, max_blocks_per_seq))
+
+
+def pkv_paged_attention_prefill_mod(q, k_cache, v_cache, block_tables, starts, cu_q, scale: float, max_q_len: int, *,
+                                    softcap: float = 0.0, alibi_slopes=None, key_starts=None, prefix_lens=None,
+                                    k_scale=None, v_scale=None, out=None, workspace=None, err_flag=None, stream=None):
+    """Prefill attention with score rules, over caches of q's type or of 8-bit codes
+    (uint8 E4M3 or int8, with k_scale / v_scale): softcap * tanh(s / softcap), minus
+    alibi_slopes[h] * |p - t|; query row i sees keys key_starts[i] <= t <= p, and
+    those below prefix_lens[b]."""
+    dev = _dev(q, k_cache, v_cache, k_scale, v_scale, block_tables, starts, cu_q, alibi_slopes, key_starts,
+               prefix_lens, out, workspace, err_flag)
+    fmt = _cache_format(q, k_cache, v_cache, k_scale, v_scale)
+    _want(block_tables, torch.int32, "block_tables")
+    _want(starts, torch.int32, "starts")
+    _want(cu_q, torch.int32, "cu_q")
+    rows, Hq, d = q.shape
+    nb, bs, Hkv, _ = k_cache.shape
+    B = starts.numel()
+    if cu_q.numel() != B + 1 or block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("inconsistent shapes")
+    mod = _score_mod(softcap, alibi_slopes, key_starts, prefix_lens, Hq, rows, B)
+    if out is None:
+        out = torch.empty_like(q)
+    ws = _lib.pkv_paged_attention_prefill_mod_workspace_size(B, Hq, Hkv, d, bs, max_q_len, block_tables.shape[1])
+    if ws and workspace is None:
+        workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(_lib.pkv_paged_attention_prefill_mod(
+            _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), fmt, _ptr(block_tables),
+            block_tables.shape[1], _ptr(starts), _ptr(cu_q), B, max_q_len, Hq, Hkv, d, bs, nb, float(scale),
+            ctypes.byref(mod), _DTYPE[q.dtype], _ptr(workspace) if ws else None,
+            workspace.numel() * workspace.element_size() if ws else 0, _ptr(err_flag), _stream(dev, stream)))
     return out
 
 

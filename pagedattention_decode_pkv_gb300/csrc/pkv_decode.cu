@@ -1621,23 +1621,6 @@ append_kv_kernel(const char *__restrict__ key, const char *__restrict__ value, c
 }
 
 // ----------------------------------------------------------------------------- host side
-// 8-bit code pool [num_slots, Hkv, 128] of bytes viewed as (128 codes,
-// num_slots, Hkv heads): one 128-byte row per (token, head), HPC heads per box.
-pkv_status make_kv_map_8bit(CUtensorMap *map, const void *pool, int64_t num_slots, int Hkv, int hpc) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return set_error(PKV_ERR_CUDA, "decode: cuTensorMapEncodeTiled entry point unavailable");
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kFastHeadDim), static_cast<cuuint64_t>(num_slots),
-                                static_cast<cuuint64_t>(Hkv)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(Hkv) * kFastHeadDim, kFastHeadDim};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kFastHeadDim), kStageTokens, static_cast<cuuint32_t>(hpc)};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(pool), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return set_error(PKV_ERR_CUDA, "decode: cuTensorMapEncodeTiled failed (%d)", (int)r);
-    return PKV_OK;
-}
-
 // cudaFuncSetAttribute once per (kernel, device); `done` is the caller's
 // per-kernel bitmask of devices already configured.
 template <typename K>
@@ -1762,10 +1745,10 @@ pkv_status launch_stream(const DecodeArgs &a, const Plan &p) {
     using L = StreamSmem<HPC, STAGES, FMT != kCode16>;
     CUtensorMap mk, mv;
     const int64_t slots = static_cast<int64_t>(a.num_blocks) * a.bs;
-    pkv_status st = FMT != kCode16 ? make_kv_map_8bit(&mk, a.k_cache, slots, a.Hkv, HPC)
+    pkv_status st = FMT != kCode16 ? make_kv_map_8bit(&mk, a.k_cache, slots, a.Hkv, kStageTokens, HPC)
                         : make_kv_map(&mk, a.k_cache, Half16<T>::kTmaType, slots, a.Hkv, HPC);
     if (st != PKV_OK) return st;
-    st = FMT != kCode16 ? make_kv_map_8bit(&mv, a.v_cache, slots, a.Hkv, HPC)
+    st = FMT != kCode16 ? make_kv_map_8bit(&mv, a.v_cache, slots, a.Hkv, kStageTokens, HPC)
              : make_kv_map(&mv, a.v_cache, Half16<T>::kTmaType, slots, a.Hkv, HPC);
     if (st != PKV_OK) return st;
     const int C = StreamLaunch<T, HPC, STAGES, FMT>::grid();

@@ -1,0 +1,897 @@
+// Causal varlen / chunked prefill attention over the paged cache with score
+// rules and over 8-bit caches.
+//
+// Query i of sequence b sits at position p = starts[b] + i.  Its score for key t
+// (query head h reading KV head h / G) is
+//     s = scale q . K_t,   s <- c tanh(s / c) (softcap c > 0),
+//     s <- s - slope_h |p - t| (alibi slopes),
+// over the visible keys  lo <= t < hi,  lo = key_starts[row] (0 without),
+// hi = min(total, max(p + 1, prefix_lens[b])): one interval per row, so a document
+// mask, a window and a prefix cost two comparisons, and only in the blocks that
+// hold a boundary; blocks that no row of the CTA sees are never loaded.  Then the
+// softmax and the sum over V_t; a row that sees nothing is zero.
+//
+// tanh comes from one exponential and one reciprocal, c tanh(u) = c - 2 c / (1 +
+// e^{2u}): its absolute error is a few 2^-23 c (both units are good to about
+// 2^-22), far below the rounding of P, where the one-instruction tanh
+// approximation (relative 2^-11) would cost more than that rounding.
+//
+// 8-bit caches: K_t = ks code, V_t = vs code, one scale per (block, KV head).  Both
+// code formats are exact in f16, so K and V codes are widened to f16 tiles by
+// converter warps and never rounded; ks multiplies the score, in f32.  P enters
+// its product as f16(p vs), and the row's reference maximum follows s + log2 vs,
+// which keeps p vs in f16's range whatever the scales; the row sum adds p itself.
+// bf16 queries become f16 under a power of two per row (exact; undone in the
+// score's factor), so no bf16 magnitude overflows.
+//
+// The CTA.  Two tiles of 128 query rows (128 / G positions x G heads) of one KV
+// head, keys by blocks of 128, accumulators in tensor memory: 12 warps, of which
+// eight softmax warps hold one query row per thread, one producer copies pages by
+// TMA, one issues the tcgen05.mma, two widen codes.  K_j and V_j go through one
+// ring of 32 KB tiles in order K_0 V_0 K_1 V_1 ..  Per tile and block: S = Q K^T,
+// softmax, P (16 bit, over S's columns), O += P V.  P is handed over in two halves
+// of 64 keys, so that PV of the first runs while the second is computed.
+// Registers: the launch gives 168 per thread; the four service warps fall to 88
+// and the softmax warps rise to 208 (their row of 128 scores then stays in
+// registers), 256 x 208 + 128 x 88 = 384 x 168.
+//
+// Few rows over a long context (a small chunk, few sequences) leave most SMs idle,
+// so the blocks of a tile pair are cut into up to nsplit runs, one CTA each, whose
+// (O, m, l) a second kernel joins.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "pkv_internal.h"
+#include "pkv_mod.h"
+#include "pkv_pack.cuh"
+#include "pkv_pdl.cuh"
+#include "pkv_tc.cuh"
+#include "pkv_tma.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kModRows = 128;   // query rows per tile (MMA M, TMEM lanes)
+constexpr int kModKeys = 128;   // keys per block
+constexpr int kModThreads = 384;
+constexpr int kModLaunchRegs = 168, kModSoftRegs = 208, kModServiceRegs = 88;
+static_assert(256 * kModSoftRegs + 128 * kModServiceRegs <= kModThreads * kModLaunchRegs,
+              "the register split draws on what the block was launched with");
+constexpr int kModTile = 32768;       // a 128 x 128 tile of 16-bit values: two 64-column halves
+constexpr int kModHalf = kModTile / 2;
+constexpr int kModCodeTile = 16384;   // the same tile in codes
+constexpr uint64_t kModDeadlineNs = 2000000000ull;
+constexpr float kModRescale = 8.f;    // log2 units a block may exceed the reference maximum by before O is rescaled
+constexpr int kMinSplitBlocks = 2;    // blocks of a split at least
+
+// Scores of a block of keys as every consumer needs them.
+struct ModInfo {
+    int32_t miss;  // bit g: the page of keys 16 g .. 16 g + 15 is out of range
+    int32_t fix;   // some V rows of the block hold nothing valid and must read as zero
+    int32_t neg;   // a K scale is negative or NaN
+    int32_t pad;
+    float ks[8], vs[8], lv[8];  // scales of each 16 keys, and log2 of the V scale (at least -100)
+};
+static_assert(sizeof(ModInfo) <= 128, "info slot");
+
+template <bool C8>
+struct ModLayout {
+    static constexpr int kRing = C8 ? 3 : 4;    // 32 KB tiles
+    static constexpr int kStage = C8 ? 4 : 0;   // 16 KB code tiles
+    static constexpr int kQ = 0;
+    static constexpr int kRingOff = 2 * kModTile;
+    static constexpr int kStageOff = kRingOff + kRing * kModTile;
+    static constexpr int kInfoOff = kStageOff + kStage * kModCodeTile;
+    static constexpr int kRangeOff = kInfoOff + 4 * 128;
+    static constexpr int kBarOff = kRangeOff + 32;
+    static constexpr int kTmemSlot = kBarOff + 256;
+    static constexpr int kBytes = kTmemSlot + 16;
+    static constexpr int kAlloc = kBytes + 1024;
+    static_assert(kAlloc <= 227 * 1024, "shared memory per CTA");
+    // mbarriers
+    static constexpr int kFull = 0;                     // [kRing] tile landed (copy bytes) or widened (two warps)
+    static constexpr int kEmpty = kFull + kRing;        // [kRing] MMA commit: both query tiles are done with it
+    static constexpr int kStFull = kEmpty + kRing;      // [kStage] codes landed
+    static constexpr int kStEmpty = kStFull + kStage;   // [kStage] codes read by both converter warps
+    static constexpr int kInfo = kStEmpty + kStage;     // [4] the block's ModInfo is written
+    static constexpr int kSFull = kInfo + 4;            // [2] S ready, and with it every earlier MMA done
+    static constexpr int kPFull = kSFull + 2;           // [2][2] a half of P written by the tile's 128 threads
+    static constexpr int kQFull = kPFull + 4;           // [2] Q rows written
+    static constexpr int kOLast = kQFull + 2;           // [2] the tile's last PV is done
+    static constexpr int kFinal = kOLast + 2;           // every MMA of the CTA is done
+    static constexpr int kNumBars = kFinal + 1;
+    static_assert(kNumBars * 8 <= 256, "mbarriers");
+};
+
+struct ModArgs {
+    void *out;
+    const void *q;
+    const int32_t *block_tables, *starts, *cu_q;
+    const float *k_scale, *v_scale;
+    const float *slopes;
+    const int32_t *key_starts, *prefix_lens;
+    int32_t max_blocks, Hq, Hkv, G, bs, num_blocks, box_lg, max_q_len, pairs, nsplit;
+    float sl;     // scale log2 e: raw score -> log2 units
+    float su;     // softcap: raw score -> 2 log2 e scale / c
+    float capl2;  // softcap in log2 units
+    float *o_part;
+    float2 *ml_part;
+    int32_t *split_used;  // [B * pairs]
+    int32_t *err_flag;
+};
+
+__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kModSoftRegs)); }
+__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kModServiceRegs)); }
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+template <typename T, int FMT, bool CAP, bool ALIBI>
+__global__ void __launch_bounds__(kModThreads, 1)
+prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ ModArgs A) {
+    constexpr bool C8 = FMT != kCode16;
+    constexpr bool RAW = !CAP && !ALIBI;  // the score's factor goes into the exponent's FMA
+    using L = ModLayout<C8>;
+    using M16 = typename std::conditional<C8, __half, T>::type;  // operand type of the products
+    using H = Half16<M16>;
+    constexpr bool kBf16 = std::is_same<M16, __nv_bfloat16>::value;
+    constexpr int kRing = L::kRing;
+    const int b = blockIdx.z, kh = blockIdx.y;
+    const int pair = blockIdx.x / A.nsplit, split = blockIdx.x - pair * A.nsplit;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = A.G, Hq = A.Hq, bs = A.bs;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    int32_t *range = reinterpret_cast<int32_t *>(smem + L::kRangeOff);  // [tile]{lowest key seen, highest + 1}
+    auto info = [&](int jj) { return reinterpret_cast<ModInfo *>(smem + L::kInfoOff + (jj & 3) * 128); };
+    const uint32_t bar0 = smem_u32(smem + L::kBarOff);
+    auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+    const uint32_t sQ = smem_u32(smem + L::kQ), sRing = smem_u32(smem + L::kRingOff);
+    const uint32_t sStage = smem_u32(smem + L::kStageOff);
+    if (warp == 8 && lane == 0) {
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(bar(L::kFull + i), C8 ? 2 : 1);
+            mbar_init(bar(L::kEmpty + i), 1);
+        }
+        for (int i = 0; i < L::kStage; ++i) {
+            mbar_init(bar(L::kStFull + i), 1);
+            mbar_init(bar(L::kStEmpty + i), 2);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(L::kInfo + i), 1);
+            mbar_init(bar(L::kPFull + i), kModRows);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(bar(L::kSFull + t), 1);
+            mbar_init(bar(L::kQFull + t), kModRows);
+            mbar_init(bar(L::kOLast + t), 1);
+            range[2 * t] = INT32_MAX;
+            range[2 * t + 1] = 0;
+        }
+        mbar_init(bar(L::kFinal), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+    }
+    pdl_wait();
+    pdl_trigger();
+    const int q_begin = A.cu_q[b], n = A.cu_q[b + 1] - q_begin, start = A.starts[b];
+    const bool first = pair == 0 && split == 0 && kh == 0;  // the CTA that reports the sequence's errors
+    if (n <= 0 || n > A.max_q_len) {  // nothing to do, or not what was declared: the rows stay as they are
+        if (n != 0 && first && threadIdx.x == 0 && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_CONTEXT);
+        return;
+    }
+    const int positions = kModRows / G;
+    const int tile0 = (n + positions - 1) / positions - 1 - 2 * pair;  // the CTA's tiles: tile0, tile0 - 1
+    if (tile0 < 0) return;
+    const int64_t total64 = static_cast<int64_t>(start) + n;
+    T *out = static_cast<T *>(A.out);
+    if (start < 0 || (total64 + bs - 1) / bs > A.max_blocks || total64 > INT32_MAX - 2 * kModKeys) {
+        if (split != 0) return;  // a bad span: zero rows and a flag
+        if (first && threadIdx.x == 0 && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_CONTEXT);
+        if (A.nsplit > 1 && kh == 0 && threadIdx.x == 0) A.split_used[static_cast<int64_t>(b) * A.pairs + pair] = 1;
+        const int p0 = max(tile0 - 1, 0) * positions, p1 = min(n, (tile0 + 1) * positions);
+        for (int i = threadIdx.x; i < (p1 - p0) * G * kFastHeadDim; i += kModThreads) {
+            const int pi = i / (G * kFastHeadDim), rem = i - pi * G * kFastHeadDim;
+            out[(static_cast<int64_t>(q_begin + p0 + pi) * Hq + kh * G) * kFastHeadDim + rem] = from_f32<T>(0.f);
+        }
+        return;
+    }
+    const int total = static_cast<int>(total64);
+    // From here on every path goes to the common exit (the CTA holds TMEM).
+    if (warp == 9) tmem_alloc(smem_u32(smem + L::kTmemSlot), 512);
+    __syncthreads();  // the barriers and `range` are initialised
+
+    // Softmax threads: tile t = warp / 4, query row r of it: position r / G, head r % G.
+    const int t = warp >> 2;  // 2: service warps
+    const int r = threadIdx.x & (kModRows - 1);
+    const int q0 = (tile0 - t) * positions;
+    const int pi = r / G;
+    bool live = false;
+    int pos = 0, lo_r = 0, hi_r = 0;  // the row's position and its visible keys [lo_r, hi_r)
+    if (t < 2) {
+        live = tile0 - t >= 0 && q0 + pi < n;
+        pos = start + q0 + pi;
+        if (live) {
+            lo_r = A.key_starts ? max(A.key_starts[q_begin + q0 + pi], 0) : 0;
+            hi_r = min(total, max(pos + 1, A.prefix_lens ? A.prefix_lens[b] : 0));
+        }
+        if (lo_r >= hi_r) lo_r = hi_r = 0;
+        const int lo_w = __reduce_min_sync(0xffffffffu, hi_r > 0 ? lo_r : INT32_MAX);
+        const int hi_w = __reduce_max_sync(0xffffffffu, hi_r);
+        if (lane == 0 && hi_w > 0) {
+            atomicMin(range + 2 * t, lo_w);
+            atomicMax(range + 2 * t + 1, hi_w);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot);
+    // Blocks of each tile, of the CTA, and of this split.
+    int lo_t[2], hi_t[2], j0 = INT32_MAX, j1 = 0, key_lo = INT32_MAX;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int lo = range[2 * i], hi = range[2 * i + 1];
+        lo_t[i] = hi > 0 ? lo / kModKeys : 0;
+        hi_t[i] = hi > 0 ? (hi - 1) / kModKeys + 1 : 0;
+        if (hi > 0) {
+            j0 = min(j0, lo_t[i]);
+            j1 = max(j1, hi_t[i]);
+            key_lo = min(key_lo, lo);
+        }
+    }
+    if (j0 > j1) j0 = j1;  // no row of the CTA sees a key
+    bool partial = false;
+    if (A.nsplit > 1) {
+        const int nb = j1 - j0;
+        const int per = max((nb + A.nsplit - 1) / A.nsplit, kMinSplitBlocks);
+        const int used = nb > 0 ? (nb + per - 1) / per : 1;
+        if (split == 0 && kh == 0 && threadIdx.x == 0) A.split_used[static_cast<int64_t>(b) * A.pairs + pair] = used;
+        partial = used > 1;
+        if (split >= used) live = false;
+        j0 = min(j0 + split * per, j1);
+        j1 = min(j0 + per, j1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            lo_t[i] = max(lo_t[i], j0);
+            hi_t[i] = max(min(hi_t[i], j1), lo_t[i]);
+        }
+    }
+    const int nb = j1 - j0;
+    const uint64_t deadline = global_ns() + kModDeadlineNs;
+    bool timed_out = false;
+
+    if (warp >= 8) {
+        setmaxnreg_dec();
+        if (warp == 8) {
+            // ------------------------------------------------------------ producer warp
+            // Lane g < 8 owns keys 16 g .. 16 g + 15 of the block; the first lane of each
+            // chunk of 2^box_lg keys (consecutive in one page) copies it.  The next block's
+            // table entries and scales are loaded while the copies of this one wait.
+            const int32_t *row = A.block_tables + static_cast<int64_t>(b) * A.max_blocks;
+            const int box_rows = 1 << A.box_lg;
+            bool bad = false;
+            int id = -1;
+            float ks = 1.f, vs = 1.f;
+            auto fetch = [&](int j) {  // key / bs < ceil(total / bs) <= max_blocks
+                id = -1;
+                const int key = j * kModKeys + 16 * lane;
+                if (lane >= 8 || key >= total) return;
+                id = row[key / bs];
+                if (id < 0 || id >= A.num_blocks) {
+                    id = -2;
+                    bad = true;
+                } else if constexpr (C8) {
+                    const int64_t at = static_cast<int64_t>(id) * A.Hkv + kh;
+                    ks = __ldg(A.k_scale + at);
+                    vs = __ldg(A.v_scale + at);
+                }
+            };
+            auto wait_bar = [&](int i, uint32_t parity) -> bool {
+                int ok = 1;
+                if (lane == 0) ok = mbar_wait(bar(i), parity, deadline);
+                return __shfl_sync(0xffffffffu, ok, 0) != 0;
+            };
+            constexpr int kSlots = C8 ? L::kStage : kRing;
+            constexpr int kSlotBytes = C8 ? kModCodeTile : kModTile;
+            constexpr int kSlotFull = C8 ? L::kStFull : L::kFull, kSlotEmpty = C8 ? L::kStEmpty : L::kEmpty;
+            const uint32_t sDst = C8 ? sStage : sRing;
+            int issued = 0;
+            if (nb > 0) fetch(j0);
+            for (int jj = 0; jj < nb && !timed_out; ++jj) {
+                const int key = (j0 + jj) * kModKeys + 16 * lane;
+                const bool copied = lane < 8 && id >= 0 && (key | (box_rows - 1)) >= key_lo;  // the chunk reaches key_lo
+                const int copy_id = id;
+                const float my_ks = ks, my_vs = vs;
+                const unsigned miss = __ballot_sync(0xffffffffu, id == -2);
+                const unsigned neg = __ballot_sync(0xffffffffu, C8 && id >= 0 && !(my_ks >= 0.f));
+                const unsigned chunks = __ballot_sync(0xffffffffu, copied && (key & (box_rows - 1)) == 0);
+                const uint32_t chunk_bytes = static_cast<uint32_t>(box_rows) * (C8 ? 128 : 256);
+                const bool mine = (chunks >> lane) & 1;
+                const int slot_row = mine ? copy_id * bs + key % bs : 0;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int item = 2 * jj + kv, slot = item % kSlots;
+                    if (item >= kSlots && !wait_bar(kSlotEmpty + slot, ((item / kSlots) - 1) & 1)) {
+                        timed_out = true;
+                        break;
+                    }
+                    if (kv == 0) {
+                        // The slot of info jj held block jj - 4, whose readers are done: the wait
+                        // above was for MMAs (or conversions) that come after its softmax.
+                        ModInfo *f = info(jj);
+                        if (lane == 0) {
+                            f->miss = static_cast<int32_t>(miss);
+                            f->fix = miss || (j0 + jj) * kModKeys < key_lo || (j0 + jj + 1) * kModKeys > total;
+                            f->neg = neg != 0;
+                        }
+                        if (C8 && lane < 8) {
+                            f->ks[lane] = id >= 0 ? my_ks : 1.f;
+                            f->vs[lane] = id >= 0 ? my_vs : 1.f;
+                            f->lv[lane] = id >= 0 ? fmaxf(__log2f(my_vs), -100.f) : 0.f;  // also a scale of 0
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(L::kInfo + (jj & 3)));
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(bar(kSlotFull + slot), __popc(chunks) * chunk_bytes);
+                    __syncwarp();
+                    if (mine) {
+                        const CUtensorMap *tm = kv ? &tm_v : &tm_k;
+                        const uint32_t dst = sDst + static_cast<uint32_t>(slot) * kSlotBytes + (16 * lane) * 128;
+                        if constexpr (C8) {
+                            tma_load_3d(dst, tm, 0, slot_row, kh, bar(kSlotFull + slot));
+                        } else {
+                            tma_load_3d(dst, tm, 0, slot_row, 2 * kh, bar(kSlotFull + slot));
+                            tma_load_3d(dst + kModHalf, tm, 0, slot_row, 2 * kh + 1, bar(kSlotFull + slot));
+                        }
+                    }
+                    issued = item + 1;
+                    if (kv == 0 && jj + 1 < nb) fetch(j0 + jj + 1);
+                }
+            }
+            bad = __any_sync(0xffffffffu, bad);
+            if (lane == 0) {
+                if (bad && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_BLOCK_RANGE);
+                // no bulk copy may still be writing shared memory when the CTA exits
+                for (int i = max(issued - kSlots, 0); i < issued; ++i)
+                    if (!mbar_wait(bar(kSlotFull + i % kSlots), (i / kSlots) & 1, deadline)) timed_out = true;
+            }
+        } else if (warp == 9) {
+            // ------------------------------------------------------------ MMA warp
+            constexpr uint32_t kIdescS = umma_idesc_f16(kBf16, kModRows, kModKeys, false);
+            constexpr uint32_t kIdescO = umma_idesc_f16(kBf16, kModRows, kFastHeadDim, true);
+            auto wait_bar = [&](int i, uint32_t parity) -> bool {
+                return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, deadline));
+            };
+            auto active = [&](int tt, int j) { return lo_t[tt] <= j && j < hi_t[tt]; };
+            auto issue_qk = [&](int tt, int j) -> bool {
+                const int item = 2 * (j - j0), slot = item % kRing;
+                if (j == lo_t[tt] && !wait_bar(L::kQFull + tt, 0)) return false;
+                if (!wait_bar(L::kFull + slot, (item / kRing) & 1)) return false;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t kt = sRing + static_cast<uint32_t>(slot) * kModTile;
+                    const uint32_t qt = sQ + static_cast<uint32_t>(tt) * kModTile;
+#pragma unroll
+                    for (int k = 0; k < kFastHeadDim / 16; ++k) {  // 16 dims (32 bytes) per step
+                        const uint32_t off = (k >> 2) * kModHalf + (k & 3) * 32;
+                        umma_f16(tmem + tt * 256, umma_desc_sw128(qt + off, 16, 1024), umma_desc_sw128(kt + off, 16, 1024),
+                                 kIdescS, k > 0);
+                    }
+                    umma_commit(bar(L::kSFull + tt));
+                }
+                __syncwarp();
+                return true;
+            };
+            int fixed = -1;  // last block whose V rows were looked after
+            auto issue_pv = [&](int tt, int j) -> bool {
+                const int item = 2 * (j - j0) + 1, slot = item % kRing;
+                if (!wait_bar(L::kFull + slot, (item / kRing) & 1)) return false;
+                const uint32_t vt = sRing + static_cast<uint32_t>(slot) * kModTile;
+                if (!C8 && fixed != j) {
+                    fixed = j;
+                    const ModInfo *f = info(j - j0);
+                    if (f->fix) {  // V rows no row sees, past the sequence or of a missing page: zeros (0 x NaN would stay)
+                        for (int i = lane; i < kModKeys * 16; i += 32) {
+                            const int rr = i >> 4, c = i & 15, key = j * kModKeys + rr;
+                            if (key < key_lo || key >= total || (f->miss >> (rr >> 4) & 1))
+                                st_shared_v4(vt + (c >> 3) * kModHalf + rr * 128 + (c & 7) * 16, 0, 0, 0, 0);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                }
+                const uint32_t tc = tmem + tt * 256;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!wait_bar(L::kPFull + 2 * tt + h, (j - lo_t[tt]) & 1)) return false;
+                    tc_fence_after();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int k = 4 * h; k < 4 * h + 4; ++k)  // 16 keys per step: 8 P columns, two 8-row V groups
+                            umma_f16_tmem_a(tc + 128, tc + 8 * k, umma_desc_sw128(vt + k * 2048, kModHalf, 1024), kIdescO,
+                                            (j > lo_t[tt] || k > 0) ? 1u : 0u);
+                        if (h == 1 && j == hi_t[tt] - 1) umma_commit(bar(L::kOLast + tt));
+                    }
+                    __syncwarp();
+                }
+                return true;
+            };
+            auto release = [&](int item) {
+                if (lane == 0) umma_commit(bar(L::kEmpty + item % kRing));
+                __syncwarp();
+            };
+            // The tiles take turns: while one tile's softmax works on its S, the tensor
+            // core runs the other tile's PV and next QK.  Operations of one thread run in
+            // order, so a QK may be issued right behind the PV that reads P from the
+            // columns it writes, and a commit stands for everything before it.
+            bool ok = true;
+            if (nb > 0) {
+                if (active(0, j0)) ok = issue_qk(0, j0);
+                if (ok && active(1, j0)) ok = issue_qk(1, j0);
+                if (ok) release(0);
+            }
+            for (int j = j0; ok && j < j1; ++j) {
+                if (active(0, j)) ok = issue_pv(0, j);
+                if (ok && active(0, j + 1)) ok = issue_qk(0, j + 1);
+                if (ok && active(1, j)) ok = issue_pv(1, j);
+                if (ok) release(2 * (j - j0) + 1);
+                if (ok && active(1, j + 1)) ok = issue_qk(1, j + 1);
+                if (ok && j + 1 < j1) release(2 * (j + 1 - j0));
+            }
+            if (!ok) timed_out = true;
+            if (lane == 0) umma_commit(bar(L::kFinal));  // arrives once every MMA issued above has completed
+            __syncwarp();
+            if (!wait_bar(L::kFinal, 0)) timed_out = true;
+        } else if constexpr (C8) {
+            // ------------------------------------------------------------ converter warps
+            // Warp w widens rows 64 w .. 64 w + 63 of every code tile.  A lane takes 16 codes
+            // (one 16-byte chunk) and writes two chunks; lanes 4 .. 7 of each eight take the
+            // row four below and write their second chunk first, so that neither the reads
+            // nor the writes (both 128-byte swizzled) meet a bank twice.
+            const int w = warp - 10;
+            const int l8 = lane & 7, hi = l8 >> 2;
+            const int row0 = 64 * w + (lane >> 3) + 4 * hi;
+            for (int item = 0; item < 2 * nb; ++item) {
+                const int st = item % L::kStage, slot = item % kRing;
+                bool ok = mbar_wait(bar(L::kStFull + st), (item / L::kStage) & 1, deadline) &&
+                          (item < kRing || mbar_wait(bar(L::kEmpty + slot), ((item / kRing) - 1) & 1, deadline));
+                if (!__all_sync(0xffffffffu, ok)) {
+                    timed_out = true;
+                    break;
+                }
+                const ModInfo *f = info(item >> 1);
+                const bool fix = (item & 1) && f->fix;
+                const int miss = f->miss, key0 = (j0 + (item >> 1)) * kModKeys;
+                const uint32_t src = sStage + static_cast<uint32_t>(st) * kModCodeTile;
+                const uint32_t dst = sRing + static_cast<uint32_t>(slot) * kModTile;
+#pragma unroll 4
+                for (int i = 0; i < 16; ++i) {
+                    const int rr = row0 + 8 * (i >> 1), c4 = l8 & 3;
+                    const int c = c4 + 4 * (i & 1);
+                    uint32_t x[4];
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                 : "r"(src + rr * 128 + ((c ^ (rr & 7)) << 4)));
+                    uint32_t y[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) codes4_to_f16x4<FMT, false>(x[e], y[2 * e], y[2 * e + 1]);
+                    if (fix) {
+                        const int key = key0 + rr;
+                        if (key < key_lo || key >= total || (miss >> (rr >> 4) & 1)) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] = 0;
+                        }
+                    }
+                    const uint32_t d = dst + (i & 1) * kModHalf + rr * 128;
+                    const uint32_t d0 = d + (((2 * c4 + hi) ^ (rr & 7)) << 4), d1 = d + (((2 * c4 + (hi ^ 1)) ^ (rr & 7)) << 4);
+                    st_shared_v4(d0, hi ? y[4] : y[0], hi ? y[5] : y[1], hi ? y[6] : y[2], hi ? y[7] : y[3]);
+                    st_shared_v4(d1, hi ? y[0] : y[4], hi ? y[1] : y[5], hi ? y[2] : y[6], hi ? y[3] : y[7]);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(L::kStEmpty + st));
+                    mbar_arrive(bar(L::kFull + slot));
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax warps
+        setmaxnreg_inc();
+        const int lo_j = t == 0 ? lo_t[0] : lo_t[1], hi_j = t == 0 ? hi_t[0] : hi_t[1];
+        const int hd = r - pi * G;
+        const int64_t qrow = (static_cast<int64_t>(q_begin) + q0 + pi) * Hq + kh * G + hd;
+        float rq = 1.f;  // C8: what the row's scores are multiplied by, a power of two
+        if (lo_j < hi_j) {  // Q row into shared memory (zeros past the sequence)
+            const uint32_t sQt = sQ + static_cast<uint32_t>(t) * kModTile + r * 128;
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(A.q) + qrow * kFastHeadDim);
+            uint4 v[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) v[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+            if constexpr (C8 && std::is_same<T, __nv_bfloat16>::value) {
+                // f16 with the row's largest value moved to [2^13, 2^14)
+                uint32_t top = 0;
+                auto upto = [&](uint32_t x) { top = max(top, max((x & 0x7fffu) << 16, x & 0x7fff0000u)); };
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    upto(v[c].x);
+                    upto(v[c].y);
+                    upto(v[c].z);
+                    upto(v[c].w);
+                }
+                const int e = static_cast<int>(top >> 23);  // biased exponent of the largest value
+                const int k = top == 0 || e == 255 ? 0 : min(max(13 - (e - 127), -120), 120);
+                const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+                rq = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+                auto narrow = [&](uint32_t x) {
+                    return H::pack(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
+                };
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    v[c] = make_uint4(narrow(v[c].x), narrow(v[c].y), narrow(v[c].z), narrow(v[c].w));
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                st_shared_v4(sQt + (c >> 3) * kModHalf + (((c & 7) ^ (r & 7)) << 4), v[c].x, v[c].y, v[c].z, v[c].w);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(bar(L::kQFull + t));
+        }
+        const float nslope = ALIBI && A.slopes && live ? -A.slopes[kh * G + hd] * 1.4426950408889634f : 0.f;
+        // this warp's TMEM lanes (32 (warp % 4) ..) in the tile's columns: S / P at 0, O at 128
+        const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 256;
+        float m_ref = -INFINITY, l_sum = 0.f;
+        for (int j = lo_j; j < hi_j; ++j) {
+            const int it = j - lo_j, jj = j - j0;
+            bool ok = mbar_wait(bar(L::kInfo + (jj & 3)), (jj >> 2) & 1, deadline) &&
+                      mbar_wait(bar(L::kSFull + t), it & 1, deadline);
+            if (!__all_sync(0xffffffffu, ok)) {
+                timed_out = true;
+                break;
+            }
+            tc_fence_after();
+            const ModInfo *f = info(jj);
+            float x[kModKeys];
+#pragma unroll
+            for (int c0 = 0; c0 < kModKeys; c0 += 32) {
+                uint32_t v[32];
+                tmem_ld32(trow + c0, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[c0 + i] = __uint_as_float(v[i]);
+            }
+            // Keys a <= k < z of the block are visible to this row, but for missing pages.
+            const int a = lo_r - j * kModKeys, z = hi_r - j * kModKeys;
+            const int miss = f->miss;
+            const bool open = __all_sync(0xffffffffu, a <= 0 && z >= kModKeys && miss == 0);
+            // 1. scores in log2 units (RAW: left as they are, factor `mul` below)
+            bool scaled = !RAW;  // whether x holds final scores
+            if constexpr (CAP) {
+                const float cap = A.capl2;
+                const uint64_t one = splat2(1.f), c2 = splat2(cap), m2c = splat2(-2.f * cap);
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const uint64_t su = splat2(C8 ? A.su * f->ks[g] * rq : A.su);
+#pragma unroll
+                    for (int k = 16 * g; k < 16 * g + 16; k += 2) {
+                        float e0, e1;
+                        unpack2(mul2(pack2(x[k], x[k + 1]), su), e0, e1);
+                        unpack2(add2(pack2(fast_exp2(e0), fast_exp2(e1)), one), e0, e1);
+                        unpack2(fma2(pack2(fast_rcp(e0), fast_rcp(e1)), m2c, c2), x[k], x[k + 1]);
+                    }
+                }
+            }
+            if constexpr (ALIBI) {
+                // bias nslope |k - c|, c the row's own key in block coordinates
+                const float c = static_cast<float>(pos - j * kModKeys);
+                const bool past = __all_sync(0xffffffffu, pos - j * kModKeys >= kModKeys - 1);  // no key after any row
+                const uint64_t ns2 = splat2(-nslope), nc2 = splat2(nslope * c);
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const uint64_t sl = splat2(CAP ? 1.f : C8 ? A.sl * f->ks[g] * rq : A.sl);
+#pragma unroll
+                    for (int k = 16 * g; k < 16 * g + 16; k += 2) {
+                        uint64_t bias;
+                        if (past) {
+                            bias = fma2(pack2(static_cast<float>(k), static_cast<float>(k + 1)), ns2, nc2);
+                        } else {
+                            bias = pack2(nslope * fabsf(static_cast<float>(k) - c),
+                                         nslope * fabsf(static_cast<float>(k + 1) - c));
+                        }
+                        const uint64_t s = pack2(x[k], x[k + 1]);
+                        unpack2(CAP ? add2(s, bias) : fma2(s, sl, bias), x[k], x[k + 1]);
+                    }
+                }
+            }
+            // 2. masked keys
+            if constexpr (RAW && C8) {
+                if (!open || f->neg) {
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        const float s = A.sl * f->ks[g] * rq;
+#pragma unroll
+                        for (int k = 16 * g; k < 16 * g + 16; ++k) x[k] *= s;
+                    }
+                    scaled = true;
+                }
+            }
+            if (!open) {
+#pragma unroll
+                for (int k = 0; k < kModKeys; ++k) {
+                    const bool seen = k >= a && k < z && !(miss >> (k >> 4) & 1);
+                    x[k] = seen ? x[k] : -INFINITY;
+                }
+            }
+            // 3. the block's maximum, of s + log2 vs for 8-bit caches
+            float mx;
+            if constexpr (C8) {
+                mx = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    float m = max3f(x[16 * g], x[16 * g + 1], x[16 * g + 2]);
+#pragma unroll
+                    for (int k = 16 * g + 3; k < 16 * g + 15; k += 2) m = max3f(m, x[k], x[k + 1]);
+                    m = fmaxf(m, x[16 * g + 15]);
+                    if (RAW && !scaled) m *= A.sl * f->ks[g] * rq;
+                    mx = fmaxf(mx, m + f->lv[g]);
+                }
+            } else {
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four independent chains
+#pragma unroll
+                for (int k = 0; k < kModKeys; k += 2) m4[(k >> 1) & 3] = max3f(m4[(k >> 1) & 3], x[k], x[k + 1]);
+                mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                if (RAW) mx *= A.sl;
+            }
+            float resc = 1.f;
+            bool moved = false;
+            if (mx > m_ref + kModRescale) {  // also the row's first visible key (m_ref = -inf)
+                if (m_ref != -INFINITY) {
+                    resc = fast_exp2(m_ref - mx);
+                    moved = true;
+                }
+                m_ref = mx;
+            }
+            // O moves with the reference: S_j's barrier stands for the PV of block j - 1 too
+            if (__any_sync(0xffffffffu, moved)) {  // TMEM access is warp-wide; a factor of 1 leaves a row as it is
+#pragma unroll
+                for (int c0 = 0; c0 < kFastHeadDim; c0 += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(trow + 128 + c0, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * resc);
+                    tmem_st32(trow + 128 + c0, v);
+                }
+            }
+            // 4. P = 2^(s - m), in halves of 64 keys over the S columns it came from
+            const uint64_t nb2 = splat2(m_ref == -INFINITY ? 0.f : -m_ref);
+            float s4[4] = {0.f, 0.f, 0.f, 0.f};
+            uint64_t l2[2] = {0, 0};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int g = 4 * h; g < 4 * h + 4; ++g) {
+                    const uint64_t mul = splat2(RAW ? (C8 ? (scaled ? 1.f : A.sl * f->ks[g] * rq) : A.sl) : 1.f);
+                    const uint64_t sv = splat2(C8 ? f->vs[g] : 1.f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int k = 16 * g + 2 * i, o = 8 * g + i - 32 * h;
+                        float e0, e1;
+                        const uint64_t s = pack2(x[k], x[k + 1]);
+                        unpack2(RAW ? fma2(s, mul, nb2) : add2(s, nb2), e0, e1);
+                        e0 = fast_exp2(e0);
+                        e1 = fast_exp2(e1);
+                        if constexpr (C8) {
+                            const uint64_t p = pack2(e0, e1);
+                            l2[i & 1] = add2(l2[i & 1], p);
+                            unpack2(mul2(p, sv), e0, e1);
+                            pk[o] = H::pack(e0, e1);
+                        } else {
+                            pk[o] = H::pack(e0, e1);
+                            pair_acc<M16>(pk[o], s4[i & 1], s4[2 + (i & 1)]);  // the rounded P: weights sum to 1
+                        }
+                    }
+                }
+                tmem_st32(trow + 32 * h, pk);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(L::kPFull + 2 * t + h));
+            }
+            if constexpr (C8) unpack2(add2(l2[0], l2[1]), s4[0], s4[1]);
+            l_sum = l_sum * resc + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
+        }
+        // Epilogue: O row / row sum, or the split's share of both.
+        bool ok = !timed_out && (lo_j >= hi_j || mbar_wait(bar(L::kOLast + t), 0, deadline));
+        if (!__all_sync(0xffffffffu, ok)) {
+            timed_out = true;
+        } else if (__any_sync(0xffffffffu, live)) {
+            tc_fence_after();
+            const float inv = l_sum > 0.f ? 1.f / l_sum : (l_sum == l_sum ? 0.f : l_sum);
+            const int64_t prow = ((static_cast<int64_t>(b) * A.max_q_len + q0 + pi) * Hq + kh * G + hd) * A.nsplit + split;
+            if (partial && live) A.ml_part[prow] = make_float2(m_ref, l_sum);
+            T *dst = out + qrow * kFastHeadDim;
+            float *po = A.o_part + prow * kFastHeadDim;
+#pragma unroll
+            for (int c0 = 0; c0 < kFastHeadDim; c0 += 32) {
+                uint32_t v[32];
+                if (lo_j < hi_j) {
+                    tmem_ld32(trow + 128 + c0, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0;
+                }
+                if (!live) continue;
+                if (partial) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(po + c0 + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                } else {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[i] = Half16<T>::pack(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4 *>(dst + c0 + 8 * i) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+            }
+        }
+    }
+    // Common exit: copies landed (producer), MMAs completed (MMA warp), TMEM reads done.
+    if (timed_out && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// Joins the splits of a row: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
+// One warp per (sequence, query, head), lanes over the dims.  Splits without a
+// visible key carry m = -inf and weight 0, and their O is not read.
+constexpr int kModMergeThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kModMergeThreads)
+prefill_mod_merge_kernel(const __grid_constant__ ModArgs A, int64_t rows) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kModMergeThreads / 32) + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int h = static_cast<int>(row % A.Hq);
+    const int64_t bi = row / A.Hq;
+    const int b = static_cast<int>(bi / A.max_q_len), i = static_cast<int>(bi - static_cast<int64_t>(b) * A.max_q_len);
+    const int q_begin = A.cu_q[b], n = A.cu_q[b + 1] - q_begin;
+    if (i >= n || n > A.max_q_len) return;
+    const int positions = kModRows / A.G;
+    const int pair = ((n + positions - 1) / positions - 1 - i / positions) >> 1;
+    const int used = min(A.split_used[static_cast<int64_t>(b) * A.pairs + pair], A.nsplit);
+    if (used <= 1) return;  // written by the main kernel
+    const float2 *ml = A.ml_part + row * A.nsplit;
+    float M = -INFINITY;
+    for (int s = 0; s < used; ++s) M = fmaxf(M, ml[s].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    for (int s = 0; s < used; ++s) {
+        const float2 v = ml[s];
+        if (v.x == -INFINITY) continue;
+        const float w = exp2f(v.x - M);
+        const float4 o = __ldg(reinterpret_cast<const float4 *>(A.o_part + (row * A.nsplit + s) * kFastHeadDim) + lane);
+        acc.x = fmaf(w, o.x, acc.x);
+        acc.y = fmaf(w, o.y, acc.y);
+        acc.z = fmaf(w, o.z, acc.z);
+        acc.w = fmaf(w, o.w, acc.w);
+        l = fmaf(w, v.y, l);
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    uint2 o;
+    o.x = Half16<T>::pack(acc.x * inv, acc.y * inv);
+    o.y = Half16<T>::pack(acc.z * inv, acc.w * inv);
+    *(reinterpret_cast<uint2 *>(static_cast<T *>(A.out) + ((static_cast<int64_t>(q_begin) + i) * A.Hq + h) * kFastHeadDim) + lane) = o;
+}
+
+// ----------------------------------------------------------------------------- host side
+// Shared memory and the register count, once per (kernel, device).  A build that
+// gives the kernel fewer registers than the split above draws on would wait for
+// ever, so it is refused.
+template <typename T, int FMT, bool CAP, bool ALIBI>
+pkv_status prefill_mod_configure() {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (e == cudaSuccess && (done.load(std::memory_order_acquire) & bit)) return PKV_OK;
+    auto kern = prefill_mod_kernel<T, FMT, CAP, ALIBI>;
+    cudaFuncAttributes attr;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, kern);
+    if (e == cudaSuccess && attr.numRegs < kModLaunchRegs)
+        return set_error(PKV_ERR_CUDA, "prefill: the kernel was built with %d registers, not %d", attr.numRegs, kModLaunchRegs);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ModLayout<FMT != kCode16>::kAlloc);
+    if (e != cudaSuccess) return set_error(PKV_ERR_CUDA, "prefill: kernel attributes: %s", cudaGetErrorString(e));
+    done.fetch_or(bit, std::memory_order_acq_rel);
+    return PKV_OK;
+}
+
+template <typename T, int FMT, bool CAP, bool ALIBI>
+pkv_status prefill_mod_launch(const PrefillCall &c) {
+    int box_rows = kModKeys;  // chunk: gcd(block_size, 128) keys, consecutive in a page
+    while (c.block_size % box_rows) box_rows >>= 1;
+    CUtensorMap mk, mv;
+    const int64_t slots = static_cast<int64_t>(c.num_blocks) * c.block_size;
+    pkv_status st;
+    if constexpr (FMT != kCode16) {
+        st = make_kv_map_8bit(&mk, c.k_cache, slots, c.Hkv, box_rows, 1);
+        if (st == PKV_OK) st = make_kv_map_8bit(&mv, c.v_cache, slots, c.Hkv, box_rows, 1);
+    } else {
+        st = make_kv_map_box(&mk, c.k_cache, Half16<T>::kTmaType, slots, c.Hkv, box_rows, 1);
+        if (st == PKV_OK) st = make_kv_map_box(&mv, c.v_cache, Half16<T>::kTmaType, slots, c.Hkv, box_rows, 1);
+    }
+    if (st == PKV_OK) st = prefill_mod_configure<T, FMT, CAP, ALIBI>();
+    if (st != PKV_OK) return st;
+    const float log2e = 1.4426950408889634f;
+    ModArgs a{};
+    a.out = c.out;
+    a.q = c.q;
+    a.block_tables = c.block_tables;
+    a.starts = c.starts;
+    a.cu_q = c.cu_q;
+    a.k_scale = c.k_scale;
+    a.v_scale = c.v_scale;
+    a.slopes = c.mod.alibi_slopes;
+    a.key_starts = c.mod.key_starts;
+    a.prefix_lens = c.mod.prefix_lens;
+    a.max_blocks = c.max_blocks;
+    a.Hq = c.Hq;
+    a.Hkv = c.Hkv;
+    a.G = c.Hq / c.Hkv;
+    a.bs = c.block_size;
+    a.num_blocks = c.num_blocks;
+    a.box_lg = __builtin_ctz(box_rows);
+    a.max_q_len = c.max_q_len;
+    a.pairs = c.plan.pairs;
+    a.nsplit = c.plan.nsplit;
+    a.sl = c.scale * log2e;
+    a.su = CAP ? 2.f * log2e * c.scale / c.mod.softcap : 0.f;
+    a.capl2 = CAP ? c.mod.softcap * log2e : 0.f;
+    a.o_part = reinterpret_cast<float *>(c.workspace);
+    a.ml_part = reinterpret_cast<float2 *>(c.workspace + c.plan.o_bytes);
+    a.split_used = reinterpret_cast<int32_t *>(c.workspace + c.plan.o_bytes + c.plan.ml_bytes);
+    a.err_flag = c.err_flag;
+    cudaError_t e = launch_pdl(kPdlDecode, prefill_mod_kernel<T, FMT, CAP, ALIBI>,
+                               dim3(a.pairs * a.nsplit, c.Hkv, c.num_seqs), dim3(kModThreads),
+                               ModLayout<FMT != kCode16>::kAlloc, c.stream, mk, mv, a);
+    if (e == cudaSuccess && a.nsplit > 1) {
+        const int64_t rows = static_cast<int64_t>(c.num_seqs) * c.max_q_len * c.Hq;
+        constexpr int kRows = kModMergeThreads / 32;
+        e = launch_pdl(kPdlCombine, prefill_mod_merge_kernel<T>, dim3(static_cast<unsigned>((rows + kRows - 1) / kRows)),
+                       dim3(kModMergeThreads), 0, c.stream, a, rows);
+    }
+    if (e != cudaSuccess) return set_error(PKV_ERR_CUDA, "prefill launch: %s", cudaGetErrorString(e));
+    return PKV_OK;
+}
+
+template <int FMT>
+pkv_status prefill_mod_format(const PrefillCall &c) {
+    const bool cap = c.mod.softcap > 0.f;
+    // Without a cap or a bias the score's factor goes into the exponent, which
+    // wants it positive; other scales take the bias kernel with a bias of 0.
+    const bool bias = c.mod.alibi_slopes || (!cap && !(c.scale > 1e-30f));
+#define PKV_MOD(T) \
+    (cap ? (bias ? prefill_mod_launch<T, FMT, true, true>(c) : prefill_mod_launch<T, FMT, true, false>(c)) \
+         : (bias ? prefill_mod_launch<T, FMT, false, true>(c) : prefill_mod_launch<T, FMT, false, false>(c)))
+    return c.dtype == PKV_BF16 ? PKV_MOD(__nv_bfloat16) : PKV_MOD(__half);
+#undef PKV_MOD
+}
+
+}  // namespace
+}  // namespace pkv

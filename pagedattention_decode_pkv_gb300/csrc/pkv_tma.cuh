@@ -265,6 +265,26 @@ pkv_status make_kv_map_box(CUtensorMap *map, const void *pool, CUtensorMapDataTy
     return PKV_OK;
 }
 
+// 8-bit code pool [num_slots, Hkv, 128] of bytes viewed as (128 codes,
+// num_slots, Hkv heads): one 128-byte row per (token, head); a box is box_rows
+// slots of box_heads heads.
+pkv_status make_kv_map_8bit(CUtensorMap *map, const void *pool, int64_t num_slots, int Hkv, int box_rows,
+                            int box_heads) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return set_error(PKV_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kFastHeadDim), static_cast<cuuint64_t>(num_slots),
+                                static_cast<cuuint64_t>(Hkv)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(Hkv) * kFastHeadDim, kFastHeadDim};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kFastHeadDim), static_cast<cuuint32_t>(box_rows),
+                               static_cast<cuuint32_t>(box_heads)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(pool), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return set_error(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return PKV_OK;
+}
+
 // The decode boxes: kStageTokens slots of hpc heads (both halves of each).
 pkv_status make_kv_map(CUtensorMap *map, const void *pool, CUtensorMapDataType type, int64_t num_slots,
                        int Hkv, int hpc) {
