@@ -25,15 +25,15 @@
 // score's factor), so no bf16 magnitude overflows.
 //
 // The CTA.  Two tiles of 128 query rows (128 / G positions x G heads) of one KV
-// head, keys by blocks of 128, accumulators in tensor memory: 12 warps, of which
-// eight softmax warps hold one query row per thread, one producer copies pages by
-// TMA, one issues the tcgen05.mma, two widen codes.  K_j and V_j go through one
-// ring of 32 KB tiles in order K_0 V_0 K_1 V_1 ..  Per tile and block: S = Q K^T,
-// softmax, P (16 bit, over S's columns), O += P V.  P is handed over in two halves
-// of 64 keys, so that PV of the first runs while the second is computed.
-// Registers: the launch gives 168 per thread; the four service warps fall to 88
-// and the softmax warps rise to 208 (their row of 128 scores then stays in
-// registers), 256 x 208 + 128 x 88 = 384 x 168.
+// head, accumulators in tensor memory: 12 warps, of which eight softmax warps hold
+// one query row per thread, one producer copies pages by TMA, one issues the
+// tcgen05.mma, two widen codes.  K and V come in blocks of 128 keys through one
+// ring of 32 KB tiles in order K_0 V_0 K_1 V_1 ..; the work goes by half blocks of
+// 64 keys.  Per tile and half block h: S_h = Q K_h^T, softmax, P_h (16 bit, over
+// S_h's columns), O += P_h V_h.  A tile has two S buffers of 64 columns and
+// QK_{h+2} follows PV_h into the buffer that P_h leaves, so that S_{h+1} is there
+// when the softmax of h ends and its warps never wait for the tensor core's round
+// trip; with one 128-column buffer they waited more than half of the time.
 //
 // Few rows over a long context (a small chunk, few sequences) leave most SMs idle,
 // so the blocks of a tile pair are cut into up to nsplit runs, one CTA each, whose
@@ -61,9 +61,7 @@ namespace {
 constexpr int kModRows = 128;   // query rows per tile (MMA M, TMEM lanes)
 constexpr int kModKeys = 128;   // keys per block
 constexpr int kModThreads = 384;
-constexpr int kModLaunchRegs = 168, kModSoftRegs = 208, kModServiceRegs = 88;
-static_assert(256 * kModSoftRegs + 128 * kModServiceRegs <= kModThreads * kModLaunchRegs,
-              "the register split draws on what the block was launched with");
+constexpr int kHalfKeys = kModKeys / 2;  // keys per step of the softmax and the products
 constexpr int kModTile = 32768;       // a 128 x 128 tile of 16-bit values: two 64-column halves
 constexpr int kModHalf = kModTile / 2;
 constexpr int kModCodeTile = 16384;   // the same tile in codes
@@ -74,7 +72,7 @@ constexpr int kMinSplitBlocks = 2;    // blocks of a split at least
 // Scores of a block of keys as every consumer needs them.
 struct ModInfo {
     int32_t miss;  // bit g: the page of keys 16 g .. 16 g + 15 is out of range
-    int32_t fix;   // some V rows of the block hold nothing valid and must read as zero
+    int32_t fix;   // some V rows of the block hold nothing valid and must read as zero (8-bit caches)
     int32_t neg;   // a K scale is negative or NaN
     int32_t pad;
     float ks[8], vs[8], lv[8];  // scales of each 16 keys, and log2 of the V scale (at least -100)
@@ -91,23 +89,25 @@ struct ModLayout {
     static constexpr int kInfoOff = kStageOff + kStage * kModCodeTile;
     static constexpr int kRangeOff = kInfoOff + 4 * 128;
     static constexpr int kBarOff = kRangeOff + 32;
-    static constexpr int kTmemSlot = kBarOff + 256;
+    static constexpr int kTmemSlot = kBarOff + 320;
     static constexpr int kBytes = kTmemSlot + 16;
     static constexpr int kAlloc = kBytes + 1024;
     static_assert(kAlloc <= 227 * 1024, "shared memory per CTA");
     // mbarriers
     static constexpr int kFull = 0;                     // [kRing] tile landed (copy bytes) or widened (two warps)
-    static constexpr int kEmpty = kFull + kRing;        // [kRing] MMA commit: both query tiles are done with it
+    static constexpr int kEmpty = kFull + kRing;        // [kRing] MMA commits: each query tile is done with it
     static constexpr int kStFull = kEmpty + kRing;      // [kStage] codes landed
     static constexpr int kStEmpty = kStFull + kStage;   // [kStage] codes read by both converter warps
     static constexpr int kInfo = kStEmpty + kStage;     // [4] the block's ModInfo is written
-    static constexpr int kSFull = kInfo + 4;            // [2] S ready, and with it every earlier MMA done
-    static constexpr int kPFull = kSFull + 2;           // [2][2] a half of P written by the tile's 128 threads
+    static constexpr int kVLand = kInfo + 4;            // 16-bit: a V tile landed that the producer goes over first
+    static constexpr int kSFull = kVLand + 1;           // [2][2] S of a tile's buffer ready, and every earlier MMA done
+    static constexpr int kPFull = kSFull + 4;           // [2][2] P written by the tile's four warps
     static constexpr int kQFull = kPFull + 4;           // [2] Q rows written
-    static constexpr int kOLast = kQFull + 2;           // [2] the tile's last PV is done
+    static constexpr int kOPrev = kQFull + 2;           // [2] the tile's last PV but one is done
+    static constexpr int kOLast = kOPrev + 2;           // [2] the tile's last PV is done
     static constexpr int kFinal = kOLast + 2;           // every MMA of the CTA is done
     static constexpr int kNumBars = kFinal + 1;
-    static_assert(kNumBars * 8 <= 256, "mbarriers");
+    static_assert(kNumBars * 8 <= 320, "mbarriers");
 };
 
 struct ModArgs {
@@ -126,9 +126,6 @@ struct ModArgs {
     int32_t *split_used;  // [B * pairs]
     int32_t *err_flag;
 };
-
-__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kModSoftRegs)); }
-__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kModServiceRegs)); }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -151,7 +148,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int G = A.G, Hq = A.Hq, bs = A.bs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    int32_t *range = reinterpret_cast<int32_t *>(smem + L::kRangeOff);  // [tile]{lowest key seen, highest + 1}
+    int32_t *range = reinterpret_cast<int32_t *>(smem + L::kRangeOff);  // lowest key that a row sees, highest + 1
     auto info = [&](int jj) { return reinterpret_cast<ModInfo *>(smem + L::kInfoOff + (jj & 3) * 128); };
     const uint32_t bar0 = smem_u32(smem + L::kBarOff);
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -160,7 +157,6 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     if (warp == 8 && lane == 0) {
         for (int i = 0; i < kRing; ++i) {
             mbar_init(bar(L::kFull + i), C8 ? 2 : 1);
-            mbar_init(bar(L::kEmpty + i), 1);
         }
         for (int i = 0; i < L::kStage; ++i) {
             mbar_init(bar(L::kStFull + i), 1);
@@ -168,16 +164,17 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(L::kInfo + i), 1);
-            mbar_init(bar(L::kPFull + i), kModRows);
+            mbar_init(bar(L::kSFull + i), 1);
+            mbar_init(bar(L::kPFull + i), 4);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(bar(L::kSFull + t), 1);
-            mbar_init(bar(L::kQFull + t), kModRows);
+            mbar_init(bar(L::kQFull + t), 4);
+            mbar_init(bar(L::kOPrev + t), 1);
             mbar_init(bar(L::kOLast + t), 1);
-            range[2 * t] = INT32_MAX;
-            range[2 * t + 1] = 0;
         }
-        mbar_init(bar(L::kFinal), 1);
+        range[0] = INT32_MAX;
+        range[1] = 0;
+        mbar_init(bar(L::kVLand), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
@@ -208,6 +205,12 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     }
     const int total = static_cast<int>(total64);
     // From here on every path goes to the common exit (the CTA holds TMEM).
+    const int ntiles = tile0 > 0 ? 2 : 1;
+    if (warp == 8 && lane == 0) {  // barriers that count tiles
+        for (int i = 0; i < kRing; ++i) mbar_init(bar(L::kEmpty + i), ntiles);
+        mbar_init(bar(L::kFinal), C8 ? 1 : ntiles);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
     if (warp == 9) tmem_alloc(smem_u32(smem + L::kTmemSlot), 512);
     __syncthreads();  // the barriers and `range` are initialised
 
@@ -229,73 +232,59 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         const int lo_w = __reduce_min_sync(0xffffffffu, hi_r > 0 ? lo_r : INT32_MAX);
         const int hi_w = __reduce_max_sync(0xffffffffu, hi_r);
         if (lane == 0 && hi_w > 0) {
-            atomicMin(range + 2 * t, lo_w);
-            atomicMax(range + 2 * t + 1, hi_w);
+            atomicMin(range, lo_w);
+            atomicMax(range + 1, hi_w);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot);
-    // Blocks of each tile, of the CTA, and of this split.
-    int lo_t[2], hi_t[2], j0 = INT32_MAX, j1 = 0, key_lo = INT32_MAX;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int lo = range[2 * i], hi = range[2 * i + 1];
-        lo_t[i] = hi > 0 ? lo / kModKeys : 0;
-        hi_t[i] = hi > 0 ? (hi - 1) / kModKeys + 1 : 0;
-        if (hi > 0) {
-            j0 = min(j0, lo_t[i]);
-            j1 = max(j1, hi_t[i]);
-            key_lo = min(key_lo, lo);
-        }
-    }
-    if (j0 > j1) j0 = j1;  // no row of the CTA sees a key
+    // Half blocks [h0, h1) that a row of the CTA sees any key of, cut to this split.  Both
+    // tiles go through all of them: their ranges differ by a few halves at most, and every
+    // barrier then passes through the same phases for everybody.
+    const int key_lo = range[0];
+    int h0 = range[1] > 0 ? key_lo / kHalfKeys : 0, h1 = range[1] > 0 ? (range[1] - 1) / kHalfKeys + 1 : 0;
     bool partial = false;
     if (A.nsplit > 1) {
-        const int nb = j1 - j0;
-        const int per = max((nb + A.nsplit - 1) / A.nsplit, kMinSplitBlocks);
-        const int used = nb > 0 ? (nb + per - 1) / per : 1;
+        const int j0 = h0 >> 1, blocks = ((h1 + 1) >> 1) - j0;
+        const int per = max((blocks + A.nsplit - 1) / A.nsplit, kMinSplitBlocks);
+        const int used = blocks > 0 ? (blocks + per - 1) / per : 1;
         if (split == 0 && kh == 0 && threadIdx.x == 0) A.split_used[static_cast<int64_t>(b) * A.pairs + pair] = used;
         partial = used > 1;
         if (split >= used) live = false;
-        j0 = min(j0 + split * per, j1);
-        j1 = min(j0 + per, j1);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            lo_t[i] = max(lo_t[i], j0);
-            hi_t[i] = max(min(hi_t[i], j1), lo_t[i]);
-        }
+        const int s0 = 2 * (j0 + split * per), s1 = s0 + 2 * per;
+        h0 = min(max(h0, s0), h1);
+        h1 = max(min(h1, s1), h0);
     }
-    const int nb = j1 - j0;
+    const int j0 = h0 >> 1, j1 = (h1 + 1) >> 1;  // the blocks to load
+    const int nb = h1 > h0 ? j1 - j0 : 0;
     const uint64_t deadline = global_ns() + kModDeadlineNs;
     bool timed_out = false;
 
     if (warp >= 8) {
-        setmaxnreg_dec();
         if (warp == 8) {
             // ------------------------------------------------------------ producer warp
             // Lane g < 8 owns keys 16 g .. 16 g + 15 of the block; the first lane of each
-            // chunk of 2^box_lg keys (consecutive in one page) copies it.  The next block's
-            // table entries and scales are loaded while the copies of this one wait.
+            // chunk of 2^box_lg keys (consecutive in one page) copies it.  Table entries are
+            // loaded two blocks ahead and scales one, so that no copy waits for them.
             const int32_t *row = A.block_tables + static_cast<int64_t>(b) * A.max_blocks;
             const int box_rows = 1 << A.box_lg;
             bool bad = false;
-            int id = -1;
-            float ks = 1.f, vs = 1.f;
-            auto fetch = [&](int j) {  // key / bs < ceil(total / bs) <= max_blocks
-                id = -1;
-                const int key = j * kModKeys + 16 * lane;
-                if (lane >= 8 || key >= total) return;
-                id = row[key / bs];
-                if (id < 0 || id >= A.num_blocks) {
-                    id = -2;
-                    bad = true;
-                } else if constexpr (C8) {
-                    const int64_t at = static_cast<int64_t>(id) * A.Hkv + kh;
-                    ks = __ldg(A.k_scale + at);
-                    vs = __ldg(A.v_scale + at);
-                }
+            auto owned = [&](int j) { return lane < 8 && j * kModKeys + 16 * lane < total; };
+            auto entry = [&](int j) -> int {  // key / bs < ceil(total / bs) <= max_blocks
+                return owned(j) ? row[(j * kModKeys + 16 * lane) / bs] : 0;
+            };
+            // a page id, -1 past the sequence, -2 out of range
+            auto page = [&](int j, int raw) -> int {
+                if (!owned(j)) return -1;
+                if (raw >= 0 && raw < A.num_blocks) return raw;
+                bad = true;
+                return -2;
+            };
+            auto scale_of = [&](const float *scales, int page_id) -> float {
+                if constexpr (!C8) return 1.f;
+                return page_id >= 0 ? __ldg(scales + static_cast<int64_t>(page_id) * A.Hkv + kh) : 1.f;
             };
             auto wait_bar = [&](int i, uint32_t parity) -> bool {
                 int ok = 1;
@@ -307,18 +296,50 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             constexpr int kSlotFull = C8 ? L::kStFull : L::kFull, kSlotEmpty = C8 ? L::kStEmpty : L::kEmpty;
             const uint32_t sDst = C8 ? sStage : sRing;
             int issued = 0;
-            if (nb > 0) fetch(j0);
+            int fix_jj = -1;  // a block whose V rows are still to be zeroed
+            unsigned fix_miss = 0;
+            uint32_t lands = 0;  // blocks that went through kVLand
+            // V rows that no row sees, past the sequence or of a missing page read as
+            // zero (0 x NaN would stay): such a tile lands on a barrier of its own, and
+            // its full barrier is arrived on when the rows are zero.
+            auto zero_v = [&]() -> bool {
+                if (!wait_bar(L::kVLand, lands & 1)) return false;
+                ++lands;
+                __syncwarp();
+                const int slot = (2 * fix_jj + 1) % kRing;
+                const uint32_t vt = sRing + static_cast<uint32_t>(slot) * kModTile;
+                for (int i = lane; i < kModKeys * 16; i += 32) {
+                    const int rr = i >> 4, c = i & 15, key = (j0 + fix_jj) * kModKeys + rr;
+                    if (key < key_lo || key >= total || (fix_miss >> (rr >> 4) & 1))
+                        st_shared_v4(vt + (c >> 3) * kModHalf + rr * 128 + (c & 7) * 16, 0, 0, 0, 0);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::kFull + slot));
+                fix_jj = -1;
+                return true;
+            };
+            int id = -1, next_raw = 0;
+            float ks = 1.f, vs = 1.f;
+            if (nb > 0) {
+                const int raw = entry(j0);
+                next_raw = entry(j0 + 1);
+                id = page(j0, raw);
+                ks = scale_of(A.k_scale, id);
+                vs = scale_of(A.v_scale, id);
+            }
             for (int jj = 0; jj < nb && !timed_out; ++jj) {
                 const int key = (j0 + jj) * kModKeys + 16 * lane;
                 const bool copied = lane < 8 && id >= 0 && (key | (box_rows - 1)) >= key_lo;  // the chunk reaches key_lo
-                const int copy_id = id;
-                const float my_ks = ks, my_vs = vs;
                 const unsigned miss = __ballot_sync(0xffffffffu, id == -2);
-                const unsigned neg = __ballot_sync(0xffffffffu, C8 && id >= 0 && !(my_ks >= 0.f));
+                const unsigned neg = __ballot_sync(0xffffffffu, C8 && id >= 0 && !(ks >= 0.f));
                 const unsigned chunks = __ballot_sync(0xffffffffu, copied && (key & (box_rows - 1)) == 0);
                 const uint32_t chunk_bytes = static_cast<uint32_t>(box_rows) * (C8 ? 128 : 256);
                 const bool mine = (chunks >> lane) & 1;
-                const int slot_row = mine ? copy_id * bs + key % bs : 0;
+                const int slot_row = mine ? id * bs + key % bs : 0;
+                int next_id = -1;
+                float next_ks = 1.f, next_vs = 1.f;
+                const bool fix = miss || (j0 + jj) * kModKeys < key_lo || (j0 + jj + 1) * kModKeys > total;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     const int item = 2 * jj + kv, slot = item % kSlots;
@@ -332,33 +353,51 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         ModInfo *f = info(jj);
                         if (lane == 0) {
                             f->miss = static_cast<int32_t>(miss);
-                            f->fix = miss || (j0 + jj) * kModKeys < key_lo || (j0 + jj + 1) * kModKeys > total;
+                            f->fix = fix;
                             f->neg = neg != 0;
                         }
                         if (C8 && lane < 8) {
-                            f->ks[lane] = id >= 0 ? my_ks : 1.f;
-                            f->vs[lane] = id >= 0 ? my_vs : 1.f;
-                            f->lv[lane] = id >= 0 ? fmaxf(__log2f(my_vs), -100.f) : 0.f;  // also a scale of 0
+                            f->ks[lane] = ks;
+                            f->vs[lane] = vs;
+                            f->lv[lane] = fmaxf(__log2f(vs), -100.f);  // also a scale of 0
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(L::kInfo + (jj & 3)));
                     }
-                    if (lane == 0) mbar_arrive_expect_tx(bar(kSlotFull + slot), __popc(chunks) * chunk_bytes);
+                    const uint32_t landed = bar(!C8 && kv == 1 && fix ? L::kVLand : kSlotFull + slot);
+                    if (lane == 0) mbar_arrive_expect_tx(landed, __popc(chunks) * chunk_bytes);
                     __syncwarp();
                     if (mine) {
                         const CUtensorMap *tm = kv ? &tm_v : &tm_k;
                         const uint32_t dst = sDst + static_cast<uint32_t>(slot) * kSlotBytes + (16 * lane) * 128;
                         if constexpr (C8) {
-                            tma_load_3d(dst, tm, 0, slot_row, kh, bar(kSlotFull + slot));
+                            tma_load_3d(dst, tm, 0, slot_row, kh, landed);
                         } else {
-                            tma_load_3d(dst, tm, 0, slot_row, 2 * kh, bar(kSlotFull + slot));
-                            tma_load_3d(dst + kModHalf, tm, 0, slot_row, 2 * kh + 1, bar(kSlotFull + slot));
+                            tma_load_3d(dst, tm, 0, slot_row, 2 * kh, landed);
+                            tma_load_3d(dst + kModHalf, tm, 0, slot_row, 2 * kh + 1, landed);
                         }
                     }
                     issued = item + 1;
-                    if (kv == 0 && jj + 1 < nb) fetch(j0 + jj + 1);
+                    if (kv == 0 && jj + 1 < nb) {
+                        next_id = page(j0 + jj + 1, next_raw);
+                        next_ks = scale_of(A.k_scale, next_id);
+                        next_vs = scale_of(A.v_scale, next_id);
+                        next_raw = entry(j0 + jj + 2);
+                    }
+                    if (!C8 && kv == 0 && fix_jj >= 0 && !zero_v()) {
+                        timed_out = true;
+                        break;
+                    }
                 }
+                if (!C8 && fix && issued == 2 * jj + 2) {
+                    fix_jj = jj;
+                    fix_miss = miss;
+                }
+                id = next_id;
+                ks = next_ks;
+                vs = next_vs;
             }
+            if (!C8 && fix_jj >= 0 && !zero_v()) timed_out = true;  // on the way out of a broken pipeline too: the copy must land
             bad = __any_sync(0xffffffffu, bad);
             if (lane == 0) {
                 if (bad && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_BLOCK_RANGE);
@@ -366,93 +405,82 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 for (int i = max(issued - kSlots, 0); i < issued; ++i)
                     if (!mbar_wait(bar(kSlotFull + i % kSlots), (i / kSlots) & 1, deadline)) timed_out = true;
             }
-        } else if (warp == 9) {
-            // ------------------------------------------------------------ MMA warp
-            constexpr uint32_t kIdescS = umma_idesc_f16(kBf16, kModRows, kModKeys, false);
-            constexpr uint32_t kIdescO = umma_idesc_f16(kBf16, kModRows, kFastHeadDim, true);
-            auto wait_bar = [&](int i, uint32_t parity) -> bool {
-                return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, deadline));
-            };
-            auto active = [&](int tt, int j) { return lo_t[tt] <= j && j < hi_t[tt]; };
-            auto issue_qk = [&](int tt, int j) -> bool {
-                const int item = 2 * (j - j0), slot = item % kRing;
-                if (j == lo_t[tt] && !wait_bar(L::kQFull + tt, 0)) return false;
-                if (!wait_bar(L::kFull + slot, (item / kRing) & 1)) return false;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t kt = sRing + static_cast<uint32_t>(slot) * kModTile;
-                    const uint32_t qt = sQ + static_cast<uint32_t>(tt) * kModTile;
+        } else if (warp == 9 || (!C8 && warp == 10 && ntiles == 2)) {
+            // ------------------------------------------------------------ MMA warps
+            // 16-bit caches: one warp per tile; 8-bit: one for both.  The tensor core's queue
+            // is short: what an issuer does between two products (waits, descriptors) is lost
+            // unless another issuer's products run meanwhile (64 keys of both tiles, products
+            // alone: 1240 clk; one issuer 1700).  The loop's values are made warp-uniform
+            // first: operands in per-thread registers took longer to move than the product
+            // to run.
+            auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+            const int uh0 = uni(h0), uh1 = uni(h1), uj0 = uh0 >> 1, uitems = uni(2 * nb);
+            const uint32_t utmem = static_cast<uint32_t>(uni(static_cast<int>(tmem)));
+            const uint32_t ubar = static_cast<uint32_t>(uni(static_cast<int>(bar0)));
+            auto mbar = [&](int i) { return ubar + 8u * static_cast<uint32_t>(i); };
+            const uint32_t ring16 = static_cast<uint32_t>(uni(static_cast<int>(sRing))) >> 4;
+            const uint32_t q16 = static_cast<uint32_t>(uni(static_cast<int>(sQ))) >> 4;
+            const int tt0 = C8 ? 0 : uni(warp) - 9, tt1 = C8 ? uni(ntiles) : tt0 + 1;
+            if (elect_one()) {
+                constexpr uint32_t kIdescS = umma_idesc_f16(kBf16, kModRows, kHalfKeys, false);
+                constexpr uint32_t kIdescO = umma_idesc_f16(kBf16, kModRows, kFastHeadDim, true);
+                const uint64_t kmajor = umma_desc_sw128(0, 16, 1024), vmajor = umma_desc_sw128(0, kModHalf, 1024);
+                // Operations of one thread run in order: a QK may be issued right behind the PV
+                // that reads P from the columns it writes, and a commit stands for everything
+                // before it.  Step h issues PV_h and QK_{h+2} (the first two steps no PV); the
+                // tiles release a K tile with the QKs of its second half, a V tile with the PVs
+                // of its second half, where the producer fills the slot again.  One copy of the
+                // code, as short as it gets: its warp shares the instruction cache with the
+                // softmax warps.
+                bool ok = true;
+#pragma unroll 1
+                for (int h = uh0 - 2; ok && h < uh1; ++h) {
+                    const bool second = h & 1;  // second half of its block
+                    const int vitem = 2 * ((h >> 1) - uj0) + 1, kitem = vitem + 1;  // V of h, K of h + 2
+                    const int vslot = vitem % kRing, vuse = vitem / kRing, kslot = kitem % kRing, kuse = kitem / kRing;
+#pragma unroll 1
+                    for (int tt = tt0; tt < tt1; ++tt) {
+                        const uint32_t tc = utmem + tt * 256;
+                        if (h >= uh0) {
+                            // O += P_h V_h
+                            if (!second || h == uh0) ok = mbar_wait(mbar(L::kFull + vslot), vuse & 1, deadline);
+                            ok = ok && mbar_wait(mbar(L::kPFull + 2 * tt + (h & 1)), ((h - uh0) >> 1) & 1, deadline);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t vd = vmajor + (ring16 + (vslot * kModTile + (h & 1) * (kHalfKeys * 128)) / 16);
+                            const uint32_t pc = tc + (h & 1) * kHalfKeys;
+                            umma_f16_tmem_a(tc + 128, pc, vd, kIdescO, h > uh0 ? 1u : 0u);
 #pragma unroll
-                    for (int k = 0; k < kFastHeadDim / 16; ++k) {  // 16 dims (32 bytes) per step
-                        const uint32_t off = (k >> 2) * kModHalf + (k & 3) * 32;
-                        umma_f16(tmem + tt * 256, umma_desc_sw128(qt + off, 16, 1024), umma_desc_sw128(kt + off, 16, 1024),
-                                 kIdescS, k > 0);
-                    }
-                    umma_commit(bar(L::kSFull + tt));
-                }
-                __syncwarp();
-                return true;
-            };
-            int fixed = -1;  // last block whose V rows were looked after
-            auto issue_pv = [&](int tt, int j) -> bool {
-                const int item = 2 * (j - j0) + 1, slot = item % kRing;
-                if (!wait_bar(L::kFull + slot, (item / kRing) & 1)) return false;
-                const uint32_t vt = sRing + static_cast<uint32_t>(slot) * kModTile;
-                if (!C8 && fixed != j) {
-                    fixed = j;
-                    const ModInfo *f = info(j - j0);
-                    if (f->fix) {  // V rows no row sees, past the sequence or of a missing page: zeros (0 x NaN would stay)
-                        for (int i = lane; i < kModKeys * 16; i += 32) {
-                            const int rr = i >> 4, c = i & 15, key = j * kModKeys + rr;
-                            if (key < key_lo || key >= total || (f->miss >> (rr >> 4) & 1))
-                                st_shared_v4(vt + (c >> 3) * kModHalf + rr * 128 + (c & 7) * 16, 0, 0, 0, 0);
+                            for (int k = 1; k < kHalfKeys / 16; ++k)  // 16 keys per step: 8 P columns, two 8-row V groups
+                                umma_f16_tmem_a(tc + 128, pc + 8 * k, vd + k * 128, kIdescO, 1u);
+                            if (h == uh1 - 2) umma_commit(mbar(L::kOPrev + tt));
+                            if (h == uh1 - 1) umma_commit(mbar(L::kOLast + tt));
+                            if (second && vitem + kRing < uitems) umma_commit(mbar(L::kEmpty + vslot));
                         }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
+                        if (h + 2 < uh1) {
+                            // S_{h+2} = Q K_{h+2}^T
+                            if (h + 2 == uh0) ok = mbar_wait(mbar(L::kQFull + tt), 0, deadline);
+                            if (ok && (!second || h + 2 == uh0)) ok = mbar_wait(mbar(L::kFull + kslot), kuse & 1, deadline);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t kd = kmajor + (ring16 + (kslot * kModTile + (h & 1) * (kHalfKeys * 128)) / 16);
+                            const uint64_t qd = kmajor + (q16 + tt * kModTile / 16);
+                            const uint32_t sc = tc + (h & 1) * kHalfKeys;
+#pragma unroll
+                            for (int k = 0; k < kFastHeadDim / 16; ++k) {  // 16 dims (32 bytes) per step
+                                const uint32_t off = ((k >> 2) * kModHalf + (k & 3) * 32) / 16;
+                                umma_f16(sc, qd + off, kd + off, kIdescS, k > 0);
+                            }
+                            umma_commit(mbar(L::kSFull + 2 * tt + (h & 1)));
+                            if (second && kitem + kRing < uitems) umma_commit(mbar(L::kEmpty + kslot));
+                        }
                     }
                 }
-                const uint32_t tc = tmem + tt * 256;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!wait_bar(L::kPFull + 2 * tt + h, (j - lo_t[tt]) & 1)) return false;
-                    tc_fence_after();
-                    if (lane == 0) {
-#pragma unroll
-                        for (int k = 4 * h; k < 4 * h + 4; ++k)  // 16 keys per step: 8 P columns, two 8-row V groups
-                            umma_f16_tmem_a(tc + 128, tc + 8 * k, umma_desc_sw128(vt + k * 2048, kModHalf, 1024), kIdescO,
-                                            (j > lo_t[tt] || k > 0) ? 1u : 0u);
-                        if (h == 1 && j == hi_t[tt] - 1) umma_commit(bar(L::kOLast + tt));
-                    }
-                    __syncwarp();
-                }
-                return true;
-            };
-            auto release = [&](int item) {
-                if (lane == 0) umma_commit(bar(L::kEmpty + item % kRing));
-                __syncwarp();
-            };
-            // The tiles take turns: while one tile's softmax works on its S, the tensor
-            // core runs the other tile's PV and next QK.  Operations of one thread run in
-            // order, so a QK may be issued right behind the PV that reads P from the
-            // columns it writes, and a commit stands for everything before it.
-            bool ok = true;
-            if (nb > 0) {
-                if (active(0, j0)) ok = issue_qk(0, j0);
-                if (ok && active(1, j0)) ok = issue_qk(1, j0);
-                if (ok) release(0);
+                if (!ok) timed_out = true;
+                umma_commit(mbar(L::kFinal));  // arrives once every MMA of this thread has completed
+                if (!mbar_wait(mbar(L::kFinal), 0, deadline)) timed_out = true;
             }
-            for (int j = j0; ok && j < j1; ++j) {
-                if (active(0, j)) ok = issue_pv(0, j);
-                if (ok && active(0, j + 1)) ok = issue_qk(0, j + 1);
-                if (ok && active(1, j)) ok = issue_pv(1, j);
-                if (ok) release(2 * (j - j0) + 1);
-                if (ok && active(1, j + 1)) ok = issue_qk(1, j + 1);
-                if (ok && j + 1 < j1) release(2 * (j + 1 - j0));
-            }
-            if (!ok) timed_out = true;
-            if (lane == 0) umma_commit(bar(L::kFinal));  // arrives once every MMA issued above has completed
             __syncwarp();
-            if (!wait_bar(L::kFinal, 0)) timed_out = true;
         } else if constexpr (C8) {
             // ------------------------------------------------------------ converter warps
             // Warp w widens rows 64 w .. 64 w + 63 of every code tile.  A lane takes 16 codes
@@ -508,79 +536,85 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
     } else {
         // ---------------------------------------------------------------- softmax warps
-        setmaxnreg_inc();
-        const int lo_j = t == 0 ? lo_t[0] : lo_t[1], hi_j = t == 0 ? hi_t[0] : hi_t[1];
+        const bool on = t < ntiles && h0 < h1;  // the tile exists and sees a key
         const int hd = r - pi * G;
-        const int64_t qrow = (static_cast<int64_t>(q_begin) + q0 + pi) * Hq + kh * G + hd;
         float rq = 1.f;  // C8: what the row's scores are multiplied by, a power of two
-        if (lo_j < hi_j) {  // Q row into shared memory (zeros past the sequence)
-            const uint32_t sQt = sQ + static_cast<uint32_t>(t) * kModTile + r * 128;
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(A.q) + qrow * kFastHeadDim);
+        if (on) {
+            // The warp's 32 Q rows into shared memory, two rows of 16 chunks at a time (zeros past the sequence)
+            const uint32_t sQt = sQ + static_cast<uint32_t>(t) * kModTile;
+            const int c = lane & 15;
             uint4 v[16];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-            if constexpr (C8 && std::is_same<T, __nv_bfloat16>::value) {
-                // f16 with the row's largest value moved to [2^13, 2^14)
-                uint32_t top = 0;
-                auto upto = [&](uint32_t x) { top = max(top, max((x & 0x7fffu) << 16, x & 0x7fff0000u)); };
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    upto(v[c].x);
-                    upto(v[c].y);
-                    upto(v[c].z);
-                    upto(v[c].w);
-                }
-                const int e = static_cast<int>(top >> 23);  // biased exponent of the largest value
-                const int k = top == 0 || e == 255 ? 0 : min(max(13 - (e - 127), -120), 120);
-                const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-                rq = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-                auto narrow = [&](uint32_t x) {
-                    return H::pack(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
-                };
-#pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    v[c] = make_uint4(narrow(v[c].x), narrow(v[c].y), narrow(v[c].z), narrow(v[c].w));
+            for (int i = 0; i < 16; ++i) {
+                const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4), pr = rr / G;
+                const int64_t row = (static_cast<int64_t>(q_begin) + q0 + pr) * Hq + kh * G + (rr - pr * G);
+                v[i] = q0 + pr < n ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(A.q) + row * kFastHeadDim) + c)
+                                   : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-                st_shared_v4(sQt + (c >> 3) * kModHalf + (((c & 7) ^ (r & 7)) << 4), v[c].x, v[c].y, v[c].z, v[c].w);
+            for (int i = 0; i < 16; ++i) {
+                const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4);
+                if constexpr (C8 && std::is_same<T, __nv_bfloat16>::value) {
+                    // f16 with the row's largest value moved to [2^13, 2^14)
+                    uint32_t top = 0;
+                    auto upto = [&](uint32_t x) { top = max(top, max((x & 0x7fffu) << 16, x & 0x7fff0000u)); };
+                    upto(v[i].x);
+                    upto(v[i].y);
+                    upto(v[i].z);
+                    upto(v[i].w);
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int e = static_cast<int>(top >> 23);  // biased exponent of the largest value
+                    const int k = top == 0 || e == 255 ? 0 : min(max(13 - (e - 127), -120), 120);
+                    const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+                    auto narrow = [&](uint32_t x) {
+                        return H::pack(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
+                    };
+                    v[i] = make_uint4(narrow(v[i].x), narrow(v[i].y), narrow(v[i].z), narrow(v[i].w));
+                    const int mine = __shfl_sync(0xffffffffu, k, (lane & 1) * 16);  // of row 2 i + (lane & 1)
+                    if (lane >> 1 == i) rq = __uint_as_float(static_cast<uint32_t>(127 - mine) << 23);
+                }
+                st_shared_v4(sQt + (c >> 3) * kModHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+            }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(bar(L::kQFull + t));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::kQFull + t));
         }
         const float nslope = ALIBI && A.slopes && live ? -A.slopes[kh * G + hd] * 1.4426950408889634f : 0.f;
-        // this warp's TMEM lanes (32 (warp % 4) ..) in the tile's columns: S / P at 0, O at 128
+        // this warp's TMEM lanes (32 (warp % 4) ..) in the tile's columns: S / P at 0 and 64, O at 128
         const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 256;
         float m_ref = -INFINITY, l_sum = 0.f;
-        for (int j = lo_j; j < hi_j; ++j) {
-            const int it = j - lo_j, jj = j - j0;
+        for (int h = h0; on && h < h1; ++h) {
+            const int jj = (h >> 1) - j0, g0 = (h & 1) * 4;  // the half's first group of 16 keys
+            const uint32_t scol = trow + (h & 1) * kHalfKeys;
             bool ok = mbar_wait(bar(L::kInfo + (jj & 3)), (jj >> 2) & 1, deadline) &&
-                      mbar_wait(bar(L::kSFull + t), it & 1, deadline);
+                      mbar_wait(bar(L::kSFull + 2 * t + (h & 1)), ((h - h0) >> 1) & 1, deadline);
             if (!__all_sync(0xffffffffu, ok)) {
                 timed_out = true;
                 break;
             }
             tc_fence_after();
             const ModInfo *f = info(jj);
-            float x[kModKeys];
+            float x[kHalfKeys];
 #pragma unroll
-            for (int c0 = 0; c0 < kModKeys; c0 += 32) {
+            for (int c0 = 0; c0 < kHalfKeys; c0 += 32) {
                 uint32_t v[32];
-                tmem_ld32(trow + c0, v);
+                tmem_ld32(scol + c0, v);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[c0 + i] = __uint_as_float(v[i]);
             }
-            // Keys a <= k < z of the block are visible to this row, but for missing pages.
-            const int a = lo_r - j * kModKeys, z = hi_r - j * kModKeys;
-            const int miss = f->miss;
-            const bool open = __all_sync(0xffffffffu, a <= 0 && z >= kModKeys && miss == 0);
+            // Keys a <= k < z of the half are visible to this row, but for missing pages.
+            const int a = lo_r - h * kHalfKeys, z = hi_r - h * kHalfKeys;
+            const int miss = f->miss >> g0 & 15;
+            const bool open = __all_sync(0xffffffffu, a <= 0 && z >= kHalfKeys && miss == 0);
             // 1. scores in log2 units (RAW: left as they are, factor `mul` below)
             bool scaled = !RAW;  // whether x holds final scores
             if constexpr (CAP) {
                 const float cap = A.capl2;
                 const uint64_t one = splat2(1.f), c2 = splat2(cap), m2c = splat2(-2.f * cap);
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const uint64_t su = splat2(C8 ? A.su * f->ks[g] * rq : A.su);
+                for (int g = 0; g < 4; ++g) {
+                    const uint64_t su = splat2(C8 ? A.su * f->ks[g0 + g] * rq : A.su);
 #pragma unroll
                     for (int k = 16 * g; k < 16 * g + 16; k += 2) {
                         float e0, e1;
@@ -591,13 +625,13 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
             }
             if constexpr (ALIBI) {
-                // bias nslope |k - c|, c the row's own key in block coordinates
-                const float c = static_cast<float>(pos - j * kModKeys);
-                const bool past = __all_sync(0xffffffffu, pos - j * kModKeys >= kModKeys - 1);  // no key after any row
+                // bias nslope |k - c|, c the row's own key in the half's coordinates
+                const float c = static_cast<float>(pos - h * kHalfKeys);
+                const bool past = __all_sync(0xffffffffu, pos - h * kHalfKeys >= kHalfKeys - 1);  // no key after any row
                 const uint64_t ns2 = splat2(-nslope), nc2 = splat2(nslope * c);
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const uint64_t sl = splat2(CAP ? 1.f : C8 ? A.sl * f->ks[g] * rq : A.sl);
+                for (int g = 0; g < 4; ++g) {
+                    const uint64_t sl = splat2(CAP ? 1.f : C8 ? A.sl * f->ks[g0 + g] * rq : A.sl);
 #pragma unroll
                     for (int k = 16 * g; k < 16 * g + 16; k += 2) {
                         uint64_t bias;
@@ -616,8 +650,8 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             if constexpr (RAW && C8) {
                 if (!open || f->neg) {
 #pragma unroll
-                    for (int g = 0; g < 8; ++g) {
-                        const float s = A.sl * f->ks[g] * rq;
+                    for (int g = 0; g < 4; ++g) {
+                        const float s = A.sl * f->ks[g0 + g] * rq;
 #pragma unroll
                         for (int k = 16 * g; k < 16 * g + 16; ++k) x[k] *= s;
                     }
@@ -626,28 +660,28 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             }
             if (!open) {
 #pragma unroll
-                for (int k = 0; k < kModKeys; ++k) {
+                for (int k = 0; k < kHalfKeys; ++k) {
                     const bool seen = k >= a && k < z && !(miss >> (k >> 4) & 1);
                     x[k] = seen ? x[k] : -INFINITY;
                 }
             }
-            // 3. the block's maximum, of s + log2 vs for 8-bit caches
+            // 3. the half's maximum, of s + log2 vs for 8-bit caches
             float mx;
             if constexpr (C8) {
                 mx = -INFINITY;
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
+                for (int g = 0; g < 4; ++g) {
                     float m = max3f(x[16 * g], x[16 * g + 1], x[16 * g + 2]);
 #pragma unroll
                     for (int k = 16 * g + 3; k < 16 * g + 15; k += 2) m = max3f(m, x[k], x[k + 1]);
                     m = fmaxf(m, x[16 * g + 15]);
-                    if (RAW && !scaled) m *= A.sl * f->ks[g] * rq;
-                    mx = fmaxf(mx, m + f->lv[g]);
+                    if (RAW && !scaled) m *= A.sl * f->ks[g0 + g] * rq;
+                    mx = fmaxf(mx, m + f->lv[g0 + g]);
                 }
             } else {
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four independent chains
 #pragma unroll
-                for (int k = 0; k < kModKeys; k += 2) m4[(k >> 1) & 3] = max3f(m4[(k >> 1) & 3], x[k], x[k + 1]);
+                for (int k = 0; k < kHalfKeys; k += 2) m4[(k >> 1) & 3] = max3f(m4[(k >> 1) & 3], x[k], x[k + 1]);
                 mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 if (RAW) mx *= A.sl;
             }
@@ -660,8 +694,17 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
                 m_ref = mx;
             }
-            // O moves with the reference: S_j's barrier stands for the PV of block j - 1 too
+            // O moves with the reference, once the PV before this half's is done: the next S
+            // stands for it, or its own barrier in the tile's last half.  (A row has no
+            // reference to move in the tile's first half.)
             if (__any_sync(0xffffffffu, moved)) {  // TMEM access is warp-wide; a factor of 1 leaves a row as it is
+                ok = h + 1 < h1 ? mbar_wait(bar(L::kSFull + 2 * t + ((h + 1) & 1)), ((h + 1 - h0) >> 1) & 1, deadline)
+                                  : mbar_wait(bar(L::kOPrev + t), 0, deadline);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    timed_out = true;
+                    break;
+                }
+                tc_fence_after();
 #pragma unroll
                 for (int c0 = 0; c0 < kFastHeadDim; c0 += 32) {
                     uint32_t v[32];
@@ -671,46 +714,44 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     tmem_st32(trow + 128 + c0, v);
                 }
             }
-            // 4. P = 2^(s - m), in halves of 64 keys over the S columns it came from
+            // 4. P = 2^(s - m) over the S columns it came from
             const uint64_t nb2 = splat2(m_ref == -INFINITY ? 0.f : -m_ref);
             float s4[4] = {0.f, 0.f, 0.f, 0.f};
             uint64_t l2[2] = {0, 0};
+            uint32_t pk[32];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t pk[32];
+            for (int g = 0; g < 4; ++g) {
+                const uint64_t mul = splat2(RAW ? (C8 ? (scaled ? 1.f : A.sl * f->ks[g0 + g] * rq) : A.sl) : 1.f);
+                const uint64_t sv = splat2(C8 ? f->vs[g0 + g] : 1.f);
 #pragma unroll
-                for (int g = 4 * h; g < 4 * h + 4; ++g) {
-                    const uint64_t mul = splat2(RAW ? (C8 ? (scaled ? 1.f : A.sl * f->ks[g] * rq) : A.sl) : 1.f);
-                    const uint64_t sv = splat2(C8 ? f->vs[g] : 1.f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int k = 16 * g + 2 * i, o = 8 * g + i - 32 * h;
-                        float e0, e1;
-                        const uint64_t s = pack2(x[k], x[k + 1]);
-                        unpack2(RAW ? fma2(s, mul, nb2) : add2(s, nb2), e0, e1);
-                        e0 = fast_exp2(e0);
-                        e1 = fast_exp2(e1);
-                        if constexpr (C8) {
-                            const uint64_t p = pack2(e0, e1);
-                            l2[i & 1] = add2(l2[i & 1], p);
-                            unpack2(mul2(p, sv), e0, e1);
-                            pk[o] = H::pack(e0, e1);
-                        } else {
-                            pk[o] = H::pack(e0, e1);
-                            pair_acc<M16>(pk[o], s4[i & 1], s4[2 + (i & 1)]);  // the rounded P: weights sum to 1
-                        }
+                for (int i = 0; i < 8; ++i) {
+                    const int k = 16 * g + 2 * i, o = 8 * g + i;
+                    float e0, e1;
+                    const uint64_t s = pack2(x[k], x[k + 1]);
+                    unpack2(RAW ? fma2(s, mul, nb2) : add2(s, nb2), e0, e1);
+                    e0 = fast_exp2(e0);
+                    e1 = fast_exp2(e1);
+                    if constexpr (C8) {
+                        const uint64_t p = pack2(e0, e1);
+                        l2[i & 1] = add2(l2[i & 1], p);
+                        unpack2(mul2(p, sv), e0, e1);
+                        pk[o] = H::pack(e0, e1);
+                    } else {
+                        pk[o] = H::pack(e0, e1);
+                        pair_acc<M16>(pk[o], s4[i & 1], s4[2 + (i & 1)]);  // the rounded P: weights sum to 1
                     }
                 }
-                tmem_st32(trow + 32 * h, pk);
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(bar(L::kPFull + 2 * t + h));
             }
+            tmem_st32(scol, pk);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::kPFull + 2 * t + (h & 1)));
             if constexpr (C8) unpack2(add2(l2[0], l2[1]), s4[0], s4[1]);
             l_sum = l_sum * resc + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
         }
         // Epilogue: O row / row sum, or the split's share of both.
-        bool ok = !timed_out && (lo_j >= hi_j || mbar_wait(bar(L::kOLast + t), 0, deadline));
+        bool ok = !timed_out && (!on || mbar_wait(bar(L::kOLast + t), 0, deadline));
         if (!__all_sync(0xffffffffu, ok)) {
             timed_out = true;
         } else if (__any_sync(0xffffffffu, live)) {
@@ -718,30 +759,50 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             const float inv = l_sum > 0.f ? 1.f / l_sum : (l_sum == l_sum ? 0.f : l_sum);
             const int64_t prow = ((static_cast<int64_t>(b) * A.max_q_len + q0 + pi) * Hq + kh * G + hd) * A.nsplit + split;
             if (partial && live) A.ml_part[prow] = make_float2(m_ref, l_sum);
-            T *dst = out + qrow * kFastHeadDim;
             float *po = A.o_part + prow * kFastHeadDim;
+            // 16-bit rows go through the tile's Q rows in shared memory (its last QK is done),
+            // so that they leave as whole lines.
+            const uint32_t sOt = sQ + static_cast<uint32_t>(t) * kModTile;
 #pragma unroll
             for (int c0 = 0; c0 < kFastHeadDim; c0 += 32) {
                 uint32_t v[32];
-                if (lo_j < hi_j) {
+                if (on) {
                     tmem_ld32(trow + 128 + c0, v);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0;
                 }
-                if (!live) continue;
                 if (partial) {
+                    if (live) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4 *>(po + c0 + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4 *>(po + c0 + 4 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    }
                 } else {
-                    uint32_t o[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[i] = Half16<T>::pack(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t o[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4 *>(dst + c0 + 8 * i) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = Half16<T>::pack(__uint_as_float(v[8 * i + 2 * e]) * inv, __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
+                        const int c = c0 / 8 + i;
+                        st_shared_v4(sOt + (c >> 3) * kModHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+                    }
+                }
+            }
+            if (!partial) {
+                __syncwarp();
+                const int c = lane & 15;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4), pr = rr / G;
+                    if (q0 + pr >= n) continue;
+                    uint4 v;
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "r"(sOt + (c >> 3) * kModHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)));
+                    const int64_t row = (static_cast<int64_t>(q_begin) + q0 + pr) * Hq + kh * G + (rr - pr * G);
+                    *(reinterpret_cast<uint4 *>(out + row * kFastHeadDim) + c) = v;
                 }
             }
         }
@@ -800,9 +861,7 @@ prefill_mod_merge_kernel(const __grid_constant__ ModArgs A, int64_t rows) {
 }
 
 // ----------------------------------------------------------------------------- host side
-// Shared memory and the register count, once per (kernel, device).  A build that
-// gives the kernel fewer registers than the split above draws on would wait for
-// ever, so it is refused.
+// The shared-memory attribute, once per (kernel, device).
 template <typename T, int FMT, bool CAP, bool ALIBI>
 pkv_status prefill_mod_configure() {
     static std::atomic<uint64_t> done{0};
@@ -811,10 +870,6 @@ pkv_status prefill_mod_configure() {
     const uint64_t bit = 1ull << (dev & 63);
     if (e == cudaSuccess && (done.load(std::memory_order_acquire) & bit)) return PKV_OK;
     auto kern = prefill_mod_kernel<T, FMT, CAP, ALIBI>;
-    cudaFuncAttributes attr;
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, kern);
-    if (e == cudaSuccess && attr.numRegs < kModLaunchRegs)
-        return set_error(PKV_ERR_CUDA, "prefill: the kernel was built with %d registers, not %d", attr.numRegs, kModLaunchRegs);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ModLayout<FMT != kCode16>::kAlloc);
     if (e != cudaSuccess) return set_error(PKV_ERR_CUDA, "prefill: kernel attributes: %s", cudaGetErrorString(e));

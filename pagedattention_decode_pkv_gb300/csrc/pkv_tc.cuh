@@ -24,6 +24,15 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// True in one lane of a converged warp.  A branch on it, unlike one on the lane
+// number, is known to run in a single thread, so the tcgen05 operands below go to
+// uniform registers directly.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t pred;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(pred));
+    return pred != 0;
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle.  The operand is stored as
 // 1024-byte atoms of 8 rows x 128 bytes (16-byte chunk c of row r at c ^ (r & 7)).
 // K-major operands: rows are the M (or N) index, 64 K-elements per row; `sbo` is
