@@ -117,7 +117,7 @@ struct ModArgs {
     const float *k_scale, *v_scale;
     const float *slopes;
     const int32_t *key_starts, *prefix_lens;
-    int32_t max_blocks, Hq, Hkv, G, bs, num_blocks, box_lg, max_q_len, pairs, nsplit;
+    int32_t max_blocks, Hq, Hkv, lg_g, bs, num_blocks, box_lg, max_q_len, pairs, nsplit;
     float sl;     // scale log2 e: raw score -> log2 units
     float su;     // softcap: raw score -> 2 log2 e scale / c
     float capl2;  // softcap in log2 units
@@ -145,7 +145,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int b = blockIdx.z, kh = blockIdx.y;
     const int pair = blockIdx.x / A.nsplit, split = blockIdx.x - pair * A.nsplit;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = A.G, Hq = A.Hq, bs = A.bs;
+    const int lg_g = A.lg_g, G = 1 << lg_g, Hq = A.Hq, bs = A.bs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     int32_t *range = reinterpret_cast<int32_t *>(smem + L::kRangeOff);  // lowest key that a row sees, highest + 1
@@ -187,8 +187,8 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if (n != 0 && first && threadIdx.x == 0 && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_CONTEXT);
         return;
     }
-    const int positions = kModRows / G;
-    const int tile0 = (n + positions - 1) / positions - 1 - 2 * pair;  // the CTA's tiles: tile0, tile0 - 1
+    const int positions = kModRows >> lg_g;
+    const int tile0 = ((n + positions - 1) >> (7 - lg_g)) - 1 - 2 * pair;  // the CTA's tiles: tile0, tile0 - 1
     if (tile0 < 0) return;
     const int64_t total64 = static_cast<int64_t>(start) + n;
     T *out = static_cast<T *>(A.out);
@@ -218,7 +218,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int t = warp >> 2;  // 2: service warps
     const int r = threadIdx.x & (kModRows - 1);
     const int q0 = (tile0 - t) * positions;
-    const int pi = r / G;
+    const int pi = r >> lg_g;
     bool live = false;
     int pos = 0, lo_r = 0, hi_r = 0;  // the row's position and its visible keys [lo_r, hi_r)
     if (t < 2) {
@@ -537,19 +537,19 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     } else {
         // ---------------------------------------------------------------- softmax warps
         const bool on = t < ntiles && h0 < h1;  // the tile exists and sees a key
-        const int hd = r - pi * G;
+        const int hd = r & (G - 1);
+        const int64_t tile_row = (static_cast<int64_t>(q_begin) + q0) * Hq + kh * G;  // the tile's first q / out row
         float rq = 1.f;  // C8: what the row's scores are multiplied by, a power of two
         if (on) {
             // The warp's 32 Q rows into shared memory, two rows of 16 chunks at a time (zeros past the sequence)
             const uint32_t sQt = sQ + static_cast<uint32_t>(t) * kModTile;
             const int c = lane & 15;
+            const uint4 *src = static_cast<const uint4 *>(A.q) + tile_row * 16 + c;  // 16 chunks of 16 bytes a row
             uint4 v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4), pr = rr / G;
-                const int64_t row = (static_cast<int64_t>(q_begin) + q0 + pr) * Hq + kh * G + (rr - pr * G);
-                v[i] = q0 + pr < n ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(A.q) + row * kFastHeadDim) + c)
-                                   : make_uint4(0, 0, 0, 0);
+                const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4), pr = rr >> lg_g;
+                v[i] = q0 + pr < n ? __ldg(src + (pr * Hq + (rr & (G - 1))) * 16) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -793,16 +793,16 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             if (!partial) {
                 __syncwarp();
                 const int c = lane & 15;
+                uint4 *dst = static_cast<uint4 *>(A.out) + tile_row * 16 + c;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4), pr = rr / G;
+                    const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4), pr = rr >> lg_g;
                     if (q0 + pr >= n) continue;
                     uint4 v;
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                                  : "r"(sOt + (c >> 3) * kModHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)));
-                    const int64_t row = (static_cast<int64_t>(q_begin) + q0 + pr) * Hq + kh * G + (rr - pr * G);
-                    *(reinterpret_cast<uint4 *>(out + row * kFastHeadDim) + c) = v;
+                    dst[(pr * Hq + (rr & (G - 1))) * 16] = v;
                 }
             }
         }
@@ -833,8 +833,8 @@ prefill_mod_merge_kernel(const __grid_constant__ ModArgs A, int64_t rows) {
     const int b = static_cast<int>(bi / A.max_q_len), i = static_cast<int>(bi - static_cast<int64_t>(b) * A.max_q_len);
     const int q_begin = A.cu_q[b], n = A.cu_q[b + 1] - q_begin;
     if (i >= n || n > A.max_q_len) return;
-    const int positions = kModRows / A.G;
-    const int pair = ((n + positions - 1) / positions - 1 - i / positions) >> 1;
+    const int lg_p = 7 - A.lg_g;  // log2 of the positions of a tile
+    const int pair = (((n + (1 << lg_p) - 1) >> lg_p) - 1 - (i >> lg_p)) >> 1;
     const int used = min(A.split_used[static_cast<int64_t>(b) * A.pairs + pair], A.nsplit);
     if (used <= 1) return;  // written by the main kernel
     const float2 *ml = A.ml_part + row * A.nsplit;
@@ -908,7 +908,7 @@ pkv_status prefill_mod_launch(const PrefillCall &c) {
     a.max_blocks = c.max_blocks;
     a.Hq = c.Hq;
     a.Hkv = c.Hkv;
-    a.G = c.Hq / c.Hkv;
+    a.lg_g = __builtin_ctz(c.Hq / c.Hkv);  // 1, 2, 4 or 8
     a.bs = c.block_size;
     a.num_blocks = c.num_blocks;
     a.box_lg = __builtin_ctz(box_rows);
