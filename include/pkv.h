@@ -490,6 +490,31 @@ PKV_API pkv_status pkv_paged_attention_prefill(void *out, const void *q, const v
                                                float scale, pkv_dtype dtype, int32_t *err_flag, void *stream);
 
 /*
+ * pkv_paged_attention_decode_mod -- pkv_paged_attention_decode with score rules
+ * (`mod`, may be NULL; key_starts [num_seqs]) and over any cache format, and with the
+ * step's new row appended first when key and value are given (as
+ * pkv_paged_attention_decode_append, or its fp8 / int8 form): one call for a decode
+ * step of a model with capped scores, a distance bias, or local attention, whose
+ * window makes the call read only the blocks from key_starts[b] on.
+ *
+ *   key, value        device [num_seqs, num_kv_heads, head_dim] (dtype), both or
+ *                     neither
+ *   k_scale, v_scale  as pkv_paged_attention_prefill_mod
+ *   workspace         pkv_paged_attention_decode_workspace_size bytes; calls that may
+ *                     overlap need one each
+ *   other arguments, shapes and device errors as pkv_paged_attention_decode, and its
+ *   fp8 / int8 forms for 8-bit caches.  A sequence whose key_starts is not below its
+ *   context length has a zero row (no error).  More than 512 sequences run as
+ *   consecutive launches over groups of at most 512.
+ */
+PKV_API pkv_status pkv_paged_attention_decode_mod(
+    void *out, const void *q, const void *key, const void *value, void *k_cache, void *v_cache, const float *k_scale,
+    const float *v_scale, pkv_cache_format format, const int32_t *block_tables, int32_t max_blocks_per_seq,
+    const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t block_size, int32_t num_blocks, int32_t max_context_len, float scale, const pkv_score_mod *mod,
+    pkv_dtype dtype, void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/*
  * pkv_paged_attention_prefill_mod -- pkv_paged_attention_prefill with score rules
  * (`mod`, may be NULL) and over any cache format: chunked prefill of a model with
  * capped scores, a distance bias, packed documents, local windows or a bidirectional

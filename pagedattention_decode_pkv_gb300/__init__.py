@@ -63,6 +63,9 @@ _SIGS = {
                                         _i64, _vp], ctypes.c_int),
     "pkv_paged_attention_prefill": ([_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
                                      _i32, _f32, ctypes.c_int, _vp, _vp], ctypes.c_int),
+    "pkv_paged_attention_decode_mod": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _vp, _i32, _vp, _i32,
+                                        _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, ctypes.c_int, _vp, _sz, _vp,
+                                        _vp], ctypes.c_int),
     "pkv_paged_attention_prefill_mod_workspace_size": ([_i32] * 7, _sz),
     "pkv_paged_attention_prefill_mod": ([_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _vp, _i32, _vp, _vp, _i32, _i32,
                                          _i32, _i32, _i32, _i32, _i32, _f32, _vp, ctypes.c_int, _vp, _sz, _vp, _vp],
@@ -454,6 +457,42 @@ def _score_mod(softcap, alibi_slopes, key_starts, prefix_lens, Hq, rows, B):
             if t.numel() != n:
                 raise ValueError(f"{name} needs {n} entries")
     return _ScoreMod(softcap, *(None if t is None else t.data_ptr() for t in (alibi_slopes, key_starts, prefix_lens)))
+
+
+def pkv_paged_attention_decode_mod(q, k_cache, v_cache, block_tables, context_lens, scale: float,
+                                   max_context_len: int, *, key=None, value=None, softcap: float = 0.0,
+                                   alibi_slopes=None, key_starts=None, k_scale=None, v_scale=None, out=None,
+                                   workspace=None, err_flag=None, stream=None):
+    """Decode attention with score rules, over caches of q's type or of 8-bit codes
+    (uint8 E4M3 or int8, with k_scale / v_scale): softcap * tanh(s / softcap), minus
+    alibi_slopes[h] * (query - key position); sequence b sees keys from
+    key_starts[b] on.  With key / value the step's new row is appended first."""
+    dev = _dev(q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, alibi_slopes, key_starts,
+               out, workspace, err_flag)
+    fmt = _cache_format(q, k_cache, v_cache, k_scale, v_scale)
+    _want(block_tables, torch.int32, "block_tables")
+    _want(context_lens, torch.int32, "context_lens")
+    B, Hq, d = q.shape
+    nb, bs, Hkv, _ = k_cache.shape
+    if context_lens.numel() != B or block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("inconsistent shapes")
+    if (key is None) != (value is None):
+        raise ValueError("key and value go together")
+    if key is not None and not (key.dtype == value.dtype == q.dtype and key.shape == value.shape == (B, Hkv, d)):
+        raise ValueError("key, value: [num_seqs, num_kv_heads, head_dim] of the q dtype")
+    mod = _score_mod(softcap, alibi_slopes, key_starts, None, Hq, B, B)
+    if out is None:
+        out = torch.empty_like(q)
+    ws = pkv_paged_attention_decode_workspace_size(B, Hq, Hkv, d, bs, max_context_len, q.dtype) if B else 0
+    if ws and workspace is None:
+        workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(_lib.pkv_paged_attention_decode_mod(
+            _ptr(out), _ptr(q), _ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), fmt,
+            _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B, Hq, Hkv, d, bs, nb, max_context_len,
+            float(scale), ctypes.byref(mod), _DTYPE[q.dtype], _ptr(workspace) if ws else None,
+            workspace.numel() * workspace.element_size() if ws else 0, _ptr(err_flag), _stream(dev, stream)))
+    return out
 
 
 def pkv_paged_attention_prefill_mod_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,

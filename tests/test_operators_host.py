@@ -105,3 +105,31 @@ def test_prefill_mod_workspace(pkv):
     assert size(64, 16, 8, 128, 16, 4096, 800) == 0  # many CTAs
     assert size(2, 16, 8, 128, 16, 20, 8) == 0       # one block of keys
     assert size(0, 16, 8, 128, 16, 20, 800) == size(2, 16, 8, 64, 16, 20, 800) == 0
+
+
+def _decode(pkv, lib, **kw):
+    mod = kw.pop("mod", None)
+    a = dict(out=_p(), q=_p(), key=None, value=None, k=_p(), v=_p(), ks=None, vs=None, fmt=pkv.PKV_CACHE_DTYPE,
+             tables=_p(), max_blocks=8, ctx=_p(), num_seqs=2, Hq=16, Hkv=8, d=128, bs=16, nb=100, max_ctx=100,
+             scale=0.1, mod=ctypes.byref(pkv._ScoreMod(*mod)) if mod else None, dtype=pkv.PKV_BF16, ws=_p(),
+             ws_bytes=1 << 40, err=None, stream=None)
+    a.update(kw)
+    return lib.pkv_paged_attention_decode_mod(*a.values())
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(dtype=7), "INVALID_ARG"), (dict(fmt=-1), "INVALID_ARG"), (dict(num_seqs=-1), "INVALID_ARG"),
+    (dict(Hq=12), "INVALID_ARG"), (dict(max_ctx=-1), "INVALID_ARG"), (dict(nb=1 << 28), "INVALID_ARG"),
+    (dict(mod=(-0.5,)), "INVALID_ARG"), (dict(mod=(float("nan"),)), "INVALID_ARG"),
+    (dict(mod=(float("inf"),)), "INVALID_ARG"), (dict(key=_p()), "INVALID_ARG"), (dict(value=_p()), "INVALID_ARG"),
+    (dict(out=None), "INVALID_ARG"), (dict(ctx=None), "INVALID_ARG"), (dict(fmt=1), "INVALID_ARG"),
+    (dict(fmt=1, ks=_p(), vs=_p(), dtype=0), "UNSUPPORTED"), (dict(fmt=2, ks=_p(), vs=_p(), d=64), "UNSUPPORTED"),
+    (dict(num_seqs=65536), "UNSUPPORTED"), (dict(d=2048), "UNSUPPORTED"), (dict(ws=None), "WORKSPACE"),
+    (dict(ws_bytes=10), "WORKSPACE")])
+def test_decode_mod_refuses(pkv, bad, status):
+    assert _decode(pkv, pkv._lib, **bad) == getattr(pkv, "PKV_ERR_" + status)
+    assert b"decode" in pkv._lib.pkv_last_error_string()
+
+
+def test_decode_mod_of_nothing(pkv):
+    assert _decode(pkv, pkv._lib, num_seqs=0) == pkv.PKV_OK
