@@ -11,10 +11,14 @@
 // hold a boundary; blocks that no row of the CTA sees are never loaded.  Then the
 // softmax and the sum over V_t; a row that sees nothing is zero.
 //
-// tanh comes from one exponential and one reciprocal, c tanh(u) = c - 2 c / (1 +
-// e^{2u}): its absolute error is a few 2^-23 c (both units are good to about
-// 2^-22), far below the rounding of P, where the one-instruction tanh
-// approximation (relative 2^-11) would cost more than that rounding.
+// tanh(u), |u| <= 0.7 in every score of a warp's 64-key step (35 of a cap of 50), is
+// u times a polynomial of degree 4 in u^2, the minimax fit in relative error (linear
+// programming on a Chebyshev grid): 3e-7, at seven packed FMA-unit operations a pair
+// of scores.  Larger scores take c tanh(u) = c - 2 c / (1 + e^{2u}), one exponential and
+// one reciprocal, off by a few 2^-23 c: two more trips through the special-function
+// unit, which the softmax needs as well (8 prompts of 4k, cap 50: 1432 us with it
+// alone).  Both errors are far below the rounding of P; the one-instruction tanh
+// (relative 2^-11) is not.
 //
 // 8-bit caches: K_t = ks code, V_t = vs code, one scale per (block, KV head).  Both
 // code formats are exact in f16, so K and V codes are widened to f16 tiles by
@@ -60,13 +64,22 @@ namespace {
 
 constexpr int kModRows = 128;   // query rows per tile (MMA M, TMEM lanes)
 constexpr int kModKeys = 128;   // keys per block
-constexpr int kModThreads = 384;
+// Threads: eight softmax warps, a producer, an MMA warp per tile, and over 8-bit
+// caches four converter warps.  384 threads have 168 registers each.  512 have 128,
+// of which the service warps give up 40 so that the softmax warps get theirs:
+// 256 x 168 + 256 x 88 = 512 x 128.
+template <bool C8> constexpr int kModThreads = C8 ? 512 : 384;
+constexpr int kModLaunchRegs = 128, kModSoftRegs = 168, kModServiceRegs = 88;  // 8-bit caches
+static_assert(256 * (kModSoftRegs + kModServiceRegs) <= 512 * kModLaunchRegs, "the split draws on the launch's registers");
+constexpr int kConvWarps = 4;
 constexpr int kHalfKeys = kModKeys / 2;  // keys per step of the softmax and the products
 constexpr int kModTile = 32768;       // a 128 x 128 tile of 16-bit values: two 64-column halves
 constexpr int kModHalf = kModTile / 2;
 constexpr int kModCodeTile = 16384;   // the same tile in codes
 constexpr uint64_t kModDeadlineNs = 2000000000ull;
 constexpr float kModRescale = 8.f;    // log2 units a block may exceed the reference maximum by before O is rescaled
+constexpr float kTanhLimit = 0.7f;    // |score / cap| up to which the polynomial stands for tanh
+constexpr double kTanhFit[5] = {0.9999996973, -0.3333021287, 0.1328111218, -0.05083622068, 0.0137736928};
 constexpr int kMinSplitBlocks = 2;    // blocks of a split at least
 
 // Scores of a block of keys as every consumer needs them.
@@ -94,10 +107,10 @@ struct ModLayout {
     static constexpr int kAlloc = kBytes + 1024;
     static_assert(kAlloc <= 227 * 1024, "shared memory per CTA");
     // mbarriers
-    static constexpr int kFull = 0;                     // [kRing] tile landed (copy bytes) or widened (two warps)
+    static constexpr int kFull = 0;                     // [kRing] tile landed (copy bytes) or widened (every converter warp)
     static constexpr int kEmpty = kFull + kRing;        // [kRing] MMA commits: each query tile is done with it
     static constexpr int kStFull = kEmpty + kRing;      // [kStage] codes landed
-    static constexpr int kStEmpty = kStFull + kStage;   // [kStage] codes read by both converter warps
+    static constexpr int kStEmpty = kStFull + kStage;   // [kStage] codes read by every converter warp
     static constexpr int kInfo = kStEmpty + kStage;     // [4] the block's ModInfo is written
     static constexpr int kVLand = kInfo + 4;            // 16-bit: a V tile landed that the producer goes over first
     static constexpr int kSFull = kVLand + 1;           // [2][2] S of a tile's buffer ready, and every earlier MMA done
@@ -119,7 +132,9 @@ struct ModArgs {
     const int32_t *key_starts, *prefix_lens;
     int32_t max_blocks, Hq, Hkv, lg_g, bs, num_blocks, box_lg, max_q_len, pairs, nsplit;
     float sl;     // scale log2 e: raw score -> log2 units
+    float sa;     // softcap: raw score -> scale / c
     float su;     // softcap: raw score -> 2 log2 e scale / c
+    float tanh_poly[5];  // softcap in log2 units times the fit's coefficients
     float capl2;  // softcap in log2 units
     float *o_part;
     float2 *ml_part;
@@ -131,8 +146,15 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&x)[4]) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 template <typename T, int FMT, bool CAP, bool ALIBI>
-__global__ void __launch_bounds__(kModThreads, 1)
+__global__ void __launch_bounds__(kModThreads<FMT != kCode16>, 1)
 prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ ModArgs A) {
     constexpr bool C8 = FMT != kCode16;
@@ -156,11 +178,11 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const uint32_t sStage = smem_u32(smem + L::kStageOff);
     if (warp == 8 && lane == 0) {
         for (int i = 0; i < kRing; ++i) {
-            mbar_init(bar(L::kFull + i), C8 ? 2 : 1);
+            mbar_init(bar(L::kFull + i), C8 ? kConvWarps : 1);
         }
         for (int i = 0; i < L::kStage; ++i) {
             mbar_init(bar(L::kStFull + i), 1);
-            mbar_init(bar(L::kStEmpty + i), 2);
+            mbar_init(bar(L::kStEmpty + i), kConvWarps);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(L::kInfo + i), 1);
@@ -197,7 +219,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if (first && threadIdx.x == 0 && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_CONTEXT);
         if (A.nsplit > 1 && kh == 0 && threadIdx.x == 0) A.split_used[static_cast<int64_t>(b) * A.pairs + pair] = 1;
         const int p0 = max(tile0 - 1, 0) * positions, p1 = min(n, (tile0 + 1) * positions);
-        for (int i = threadIdx.x; i < (p1 - p0) * G * kFastHeadDim; i += kModThreads) {
+        for (int i = threadIdx.x; i < (p1 - p0) * G * kFastHeadDim; i += kModThreads<C8>) {
             const int pi = i / (G * kFastHeadDim), rem = i - pi * G * kFastHeadDim;
             out[(static_cast<int64_t>(q_begin + p0 + pi) * Hq + kh * G) * kFastHeadDim + rem] = from_f32<T>(0.f);
         }
@@ -208,7 +230,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int ntiles = tile0 > 0 ? 2 : 1;
     if (warp == 8 && lane == 0) {  // barriers that count tiles
         for (int i = 0; i < kRing; ++i) mbar_init(bar(L::kEmpty + i), ntiles);
-        mbar_init(bar(L::kFinal), C8 ? 1 : ntiles);
+        mbar_init(bar(L::kFinal), ntiles);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 9) tmem_alloc(smem_u32(smem + L::kTmemSlot), 512);
@@ -263,6 +285,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     bool timed_out = false;
 
     if (warp >= 8) {
+        if constexpr (C8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kModServiceRegs));
         if (warp == 8) {
             // ------------------------------------------------------------ producer warp
             // Lane g < 8 owns keys 16 g .. 16 g + 15 of the block; the first lane of each
@@ -405,14 +428,13 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 for (int i = max(issued - kSlots, 0); i < issued; ++i)
                     if (!mbar_wait(bar(kSlotFull + i % kSlots), (i / kSlots) & 1, deadline)) timed_out = true;
             }
-        } else if (warp == 9 || (!C8 && warp == 10 && ntiles == 2)) {
+        } else if (warp < 11) {
             // ------------------------------------------------------------ MMA warps
-            // 16-bit caches: one warp per tile; 8-bit: one for both.  The tensor core's queue
-            // is short: what an issuer does between two products (waits, descriptors) is lost
-            // unless another issuer's products run meanwhile (64 keys of both tiles, products
-            // alone: 1240 clk; one issuer 1700).  The loop's values are made warp-uniform
-            // first: operands in per-thread registers took longer to move than the product
-            // to run.
+            // One per tile that exists.  The tensor core's queue is short: what an issuer does
+            // between two products (waits, descriptors) is lost unless another issuer's products
+            // run meanwhile (64 keys of both tiles, products alone: 1240 clk; one issuer 1700).
+            // The loop's values are made warp-uniform first: operands in per-thread registers
+            // took longer to move than the product to run.
             auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
             const int uh0 = uni(h0), uh1 = uni(h1), uj0 = uh0 >> 1, uitems = uni(2 * nb);
             const uint32_t utmem = static_cast<uint32_t>(uni(static_cast<int>(tmem)));
@@ -420,8 +442,9 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             auto mbar = [&](int i) { return ubar + 8u * static_cast<uint32_t>(i); };
             const uint32_t ring16 = static_cast<uint32_t>(uni(static_cast<int>(sRing))) >> 4;
             const uint32_t q16 = static_cast<uint32_t>(uni(static_cast<int>(sQ))) >> 4;
-            const int tt0 = C8 ? 0 : uni(warp) - 9, tt1 = C8 ? uni(ntiles) : tt0 + 1;
-            if (elect_one()) {
+            const int tt = uni(warp) - 9;
+            const uint32_t tc = utmem + tt * 256;
+            if (tt < uni(ntiles) && elect_one()) {
                 constexpr uint32_t kIdescS = umma_idesc_f16(kBf16, kModRows, kHalfKeys, false);
                 constexpr uint32_t kIdescO = umma_idesc_f16(kBf16, kModRows, kFastHeadDim, true);
                 const uint64_t kmajor = umma_desc_sw128(0, 16, 1024), vmajor = umma_desc_sw128(0, kModHalf, 1024);
@@ -438,42 +461,38 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     const bool second = h & 1;  // second half of its block
                     const int vitem = 2 * ((h >> 1) - uj0) + 1, kitem = vitem + 1;  // V of h, K of h + 2
                     const int vslot = vitem % kRing, vuse = vitem / kRing, kslot = kitem % kRing, kuse = kitem / kRing;
-#pragma unroll 1
-                    for (int tt = tt0; tt < tt1; ++tt) {
-                        const uint32_t tc = utmem + tt * 256;
-                        if (h >= uh0) {
-                            // O += P_h V_h
-                            if (!second || h == uh0) ok = mbar_wait(mbar(L::kFull + vslot), vuse & 1, deadline);
-                            ok = ok && mbar_wait(mbar(L::kPFull + 2 * tt + (h & 1)), ((h - uh0) >> 1) & 1, deadline);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint64_t vd = vmajor + (ring16 + (vslot * kModTile + (h & 1) * (kHalfKeys * 128)) / 16);
-                            const uint32_t pc = tc + (h & 1) * kHalfKeys;
-                            umma_f16_tmem_a(tc + 128, pc, vd, kIdescO, h > uh0 ? 1u : 0u);
+                    if (h >= uh0) {
+                        // O += P_h V_h
+                        if (!second || h == uh0) ok = mbar_wait(mbar(L::kFull + vslot), vuse & 1, deadline);
+                        ok = ok && mbar_wait(mbar(L::kPFull + 2 * tt + (h & 1)), ((h - uh0) >> 1) & 1, deadline);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vd = vmajor + (ring16 + (vslot * kModTile + (h & 1) * (kHalfKeys * 128)) / 16);
+                        const uint32_t pc = tc + (h & 1) * kHalfKeys;
+                        umma_f16_tmem_a(tc + 128, pc, vd, kIdescO, h > uh0 ? 1u : 0u);
 #pragma unroll
-                            for (int k = 1; k < kHalfKeys / 16; ++k)  // 16 keys per step: 8 P columns, two 8-row V groups
-                                umma_f16_tmem_a(tc + 128, pc + 8 * k, vd + k * 128, kIdescO, 1u);
-                            if (h == uh1 - 2) umma_commit(mbar(L::kOPrev + tt));
-                            if (h == uh1 - 1) umma_commit(mbar(L::kOLast + tt));
-                            if (second && vitem + kRing < uitems) umma_commit(mbar(L::kEmpty + vslot));
-                        }
-                        if (h + 2 < uh1) {
-                            // S_{h+2} = Q K_{h+2}^T
-                            if (h + 2 == uh0) ok = mbar_wait(mbar(L::kQFull + tt), 0, deadline);
-                            if (ok && (!second || h + 2 == uh0)) ok = mbar_wait(mbar(L::kFull + kslot), kuse & 1, deadline);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint64_t kd = kmajor + (ring16 + (kslot * kModTile + (h & 1) * (kHalfKeys * 128)) / 16);
-                            const uint64_t qd = kmajor + (q16 + tt * kModTile / 16);
-                            const uint32_t sc = tc + (h & 1) * kHalfKeys;
+                        for (int k = 1; k < kHalfKeys / 16; ++k)  // 16 keys per step: 8 P columns, two 8-row V groups
+                            umma_f16_tmem_a(tc + 128, pc + 8 * k, vd + k * 128, kIdescO, 1u);
+                        if (h == uh1 - 2) umma_commit(mbar(L::kOPrev + tt));
+                        if (h == uh1 - 1) umma_commit(mbar(L::kOLast + tt));
+                        if (second && vitem + kRing < uitems) umma_commit(mbar(L::kEmpty + vslot));
+                    }
+                    if (h + 2 < uh1) {
+                        // S_{h+2} = Q K_{h+2}^T
+                        if (h + 2 == uh0) ok = mbar_wait(mbar(L::kQFull + tt), 0, deadline);
+                        if (ok && (!second || h + 2 == uh0)) ok = mbar_wait(mbar(L::kFull + kslot), kuse & 1, deadline);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t kd = kmajor + (ring16 + (kslot * kModTile + (h & 1) * (kHalfKeys * 128)) / 16);
+                        const uint64_t qd = kmajor + (q16 + tt * kModTile / 16);
+                        const uint32_t sc = tc + (h & 1) * kHalfKeys;
 #pragma unroll
-                            for (int k = 0; k < kFastHeadDim / 16; ++k) {  // 16 dims (32 bytes) per step
-                                const uint32_t off = ((k >> 2) * kModHalf + (k & 3) * 32) / 16;
-                                umma_f16(sc, qd + off, kd + off, kIdescS, k > 0);
-                            }
-                            umma_commit(mbar(L::kSFull + 2 * tt + (h & 1)));
-                            if (second && kitem + kRing < uitems) umma_commit(mbar(L::kEmpty + kslot));
+                        for (int k = 0; k < kFastHeadDim / 16; ++k) {  // 16 dims (32 bytes) per step
+                            const uint32_t off = ((k >> 2) * kModHalf + (k & 3) * 32) / 16;
+                            umma_f16(sc, qd + off, kd + off, kIdescS, k > 0);
                         }
+                        umma_commit(mbar(L::kSFull + 2 * tt + (h & 1)));
+                        if (second && kitem + kRing < uitems) umma_commit(mbar(L::kEmpty + kslot));
                     }
                 }
                 if (!ok) timed_out = true;
@@ -483,14 +502,14 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             __syncwarp();
         } else if constexpr (C8) {
             // ------------------------------------------------------------ converter warps
-            // Warp w widens rows 64 w .. 64 w + 63 of every code tile.  A lane takes 16 codes
+            // Warp w widens rows 32 w .. 32 w + 31 of every code tile.  A lane takes 16 codes
             // (one 16-byte chunk) and writes two chunks; lanes 4 .. 7 of each eight take the
             // row four below and write their second chunk first, so that neither the reads
             // nor the writes (both 128-byte swizzled) meet a bank twice.
-            const int w = warp - 10;
+            const int w = warp - 11;
             const int l8 = lane & 7, hi = l8 >> 2;
-            const int row0 = 64 * w + (lane >> 3) + 4 * hi;
-            for (int item = 0; item < 2 * nb; ++item) {
+            const int row0 = 32 * w + (lane >> 3) + 4 * hi;
+            for (int item = 0; item < 2 * nb && w < kConvWarps; ++item) {
                 const int st = item % L::kStage, slot = item % kRing;
                 bool ok = mbar_wait(bar(L::kStFull + st), (item / L::kStage) & 1, deadline) &&
                           (item < kRing || mbar_wait(bar(L::kEmpty + slot), ((item / kRing) - 1) & 1, deadline));
@@ -504,13 +523,11 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const uint32_t src = sStage + static_cast<uint32_t>(st) * kModCodeTile;
                 const uint32_t dst = sRing + static_cast<uint32_t>(slot) * kModTile;
 #pragma unroll 4
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     const int rr = row0 + 8 * (i >> 1), c4 = l8 & 3;
                     const int c = c4 + 4 * (i & 1);
                     uint32_t x[4];
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                 : "r"(src + rr * 128 + ((c ^ (rr & 7)) << 4)));
+                    ld_shared_v4(src + rr * 128 + ((c ^ (rr & 7)) << 4), x);
                     uint32_t y[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) codes4_to_f16x4<FMT, false>(x[e], y[2 * e], y[2 * e + 1]);
@@ -536,6 +553,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
     } else {
         // ---------------------------------------------------------------- softmax warps
+        if constexpr (C8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kModSoftRegs));
         const bool on = t < ntiles && h0 < h1;  // the tile exists and sees a key
         const int hd = r & (G - 1);
         const int64_t tile_row = (static_cast<int64_t>(q_begin) + q0) * Hq + kh * G;  // the tile's first q / out row
@@ -554,27 +572,36 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4);
-                if constexpr (C8 && std::is_same<T, __nv_bfloat16>::value) {
-                    // f16 with the row's largest value moved to [2^13, 2^14)
-                    uint32_t top = 0;
-                    auto upto = [&](uint32_t x) { top = max(top, max((x & 0x7fffu) << 16, x & 0x7fff0000u)); };
-                    upto(v[i].x);
-                    upto(v[i].y);
-                    upto(v[i].z);
-                    upto(v[i].w);
-#pragma unroll
-                    for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const int e = static_cast<int>(top >> 23);  // biased exponent of the largest value
-                    const int k = top == 0 || e == 255 ? 0 : min(max(13 - (e - 127), -120), 120);
-                    const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-                    auto narrow = [&](uint32_t x) {
-                        return H::pack(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
-                    };
-                    v[i] = make_uint4(narrow(v[i].x), narrow(v[i].y), narrow(v[i].z), narrow(v[i].w));
-                    const int mine = __shfl_sync(0xffffffffu, k, (lane & 1) * 16);  // of row 2 i + (lane & 1)
-                    if (lane >> 1 == i) rq = __uint_as_float(static_cast<uint32_t>(127 - mine) << 23);
-                }
                 st_shared_v4(sQt + (c >> 3) * kModHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+            }
+            if constexpr (C8 && std::is_same<T, __nv_bfloat16>::value) {
+                // bf16 becomes f16 with the row's largest value moved to [2^13, 2^14), a row per
+                // thread in place (rolled loops: unrolled over the loads above they cost every CTA
+                // more in instruction fetches than they save)
+                __syncwarp();
+                const uint32_t mine = sQt + r * 128;
+                auto chunk = [&](int i) { return mine + (i >> 3) * kModHalf + (((i & 7) ^ (r & 7)) << 4); };
+                uint32_t top = 0;
+#pragma unroll 4
+                for (int i = 0; i < 16; ++i) {
+                    uint32_t x[4];
+                    ld_shared_v4(chunk(i), x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = max(top, max((x[e] & 0x7fffu) << 16, x[e] & 0x7fff0000u));
+                }
+                const int e = static_cast<int>(top >> 23);  // biased exponent of the largest value
+                const int k = top == 0 || e == 255 ? 0 : min(max(13 - (e - 127), -120), 120);
+                const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+                rq = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+#pragma unroll 4
+                for (int i = 0; i < 16; ++i) {
+                    uint32_t x[4];
+                    ld_shared_v4(chunk(i), x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = H::pack(__uint_as_float(x[e] << 16) * f, __uint_as_float(x[e] & 0xffff0000u) * f);
+                    st_shared_v4(chunk(i), x[0], x[1], x[2], x[3]);
+                }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -610,17 +637,41 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             // 1. scores in log2 units (RAW: left as they are, factor `mul` below)
             bool scaled = !RAW;  // whether x holds final scores
             if constexpr (CAP) {
-                const float cap = A.capl2;
-                const uint64_t one = splat2(1.f), c2 = splat2(cap), m2c = splat2(-2.f * cap);
+                uint64_t c[5];
+#pragma unroll
+                for (int i = 0; i < 5; ++i) c[i] = splat2(A.tanh_poly[i]);
+                float top = 0.f;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const uint64_t su = splat2(C8 ? A.su * f->ks[g0 + g] * rq : A.su);
+                    const uint64_t sa = splat2(C8 ? A.sa * f->ks[g0 + g] * rq : A.sa);
 #pragma unroll
                     for (int k = 16 * g; k < 16 * g + 16; k += 2) {
-                        float e0, e1;
-                        unpack2(mul2(pack2(x[k], x[k + 1]), su), e0, e1);
-                        unpack2(add2(pack2(fast_exp2(e0), fast_exp2(e1)), one), e0, e1);
-                        unpack2(fma2(pack2(fast_rcp(e0), fast_rcp(e1)), m2c, c2), x[k], x[k + 1]);
+                        const uint64_t u = mul2(pack2(x[k], x[k + 1]), sa), u2 = mul2(u, u);
+                        float z0, z1;
+                        unpack2(u2, z0, z1);
+                        top = max3f(top, z0, z1);
+                        unpack2(mul2(u, fma2(u2, fma2(u2, fma2(u2, fma2(u2, c[4], c[3]), c[2]), c[1]), c[0])), x[k], x[k + 1]);
+                    }
+                }
+                if (!__all_sync(0xffffffffu, top <= kTanhLimit * kTanhLimit)) {  // S is still there: once more
+#pragma unroll
+                    for (int c0 = 0; c0 < kHalfKeys; c0 += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(scol + c0, v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[c0 + i] = __uint_as_float(v[i]);
+                    }
+                    const uint64_t one = splat2(1.f), c2 = splat2(A.capl2), m2c = splat2(-2.f * A.capl2);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const uint64_t su = splat2(C8 ? A.su * f->ks[g0 + g] * rq : A.su);
+#pragma unroll
+                        for (int k = 16 * g; k < 16 * g + 16; k += 2) {
+                            float e0, e1;
+                            unpack2(mul2(pack2(x[k], x[k + 1]), su), e0, e1);
+                            unpack2(add2(pack2(fast_exp2(e0), fast_exp2(e1)), one), e0, e1);
+                            unpack2(fma2(pack2(fast_rcp(e0), fast_rcp(e1)), m2c, c2), x[k], x[k + 1]);
+                        }
                     }
                 }
             }
@@ -628,21 +679,24 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 // bias nslope |k - c|, c the row's own key in the half's coordinates
                 const float c = static_cast<float>(pos - h * kHalfKeys);
                 const bool past = __all_sync(0xffffffffu, pos - h * kHalfKeys >= kHalfKeys - 1);  // no key after any row
-                const uint64_t ns2 = splat2(-nslope), nc2 = splat2(nslope * c);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const uint64_t sl = splat2(CAP ? 1.f : C8 ? A.sl * f->ks[g0 + g] * rq : A.sl);
+                    if (past) {  // nslope (c - k), two keys on by one addition
+                        uint64_t bias = pack2(nslope * (c - 16 * g), nslope * (c - 16 * g - 1));
+                        const uint64_t on = splat2(-2.f * nslope);
 #pragma unroll
-                    for (int k = 16 * g; k < 16 * g + 16; k += 2) {
-                        uint64_t bias;
-                        if (past) {
-                            bias = fma2(pack2(static_cast<float>(k), static_cast<float>(k + 1)), ns2, nc2);
-                        } else {
-                            bias = pack2(nslope * fabsf(static_cast<float>(k) - c),
-                                         nslope * fabsf(static_cast<float>(k + 1) - c));
+                        for (int k = 16 * g; k < 16 * g + 16; k += 2) {
+                            const uint64_t s = pack2(x[k], x[k + 1]);
+                            unpack2(CAP ? add2(s, bias) : fma2(s, sl, bias), x[k], x[k + 1]);
+                            bias = add2(bias, on);
                         }
-                        const uint64_t s = pack2(x[k], x[k + 1]);
-                        unpack2(CAP ? add2(s, bias) : fma2(s, sl, bias), x[k], x[k + 1]);
+                    } else {
+#pragma unroll
+                        for (int k = 16 * g; k < 16 * g + 16; ++k) {
+                            const float bias = nslope * fabsf(static_cast<float>(k) - c);
+                            x[k] = CAP ? x[k] + bias : fmaf(x[k], C8 ? A.sl * f->ks[g0 + g] * rq : A.sl, bias);
+                        }
                     }
                 }
             }
@@ -798,11 +852,9 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 for (int i = 0; i < 16; ++i) {
                     const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4), pr = rr >> lg_g;
                     if (q0 + pr >= n) continue;
-                    uint4 v;
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                 : "r"(sOt + (c >> 3) * kModHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)));
-                    dst[(pr * Hq + (rr & (G - 1))) * 16] = v;
+                    uint32_t o[4];
+                    ld_shared_v4(sOt + (c >> 3) * kModHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), o);
+                    dst[(pr * Hq + (rr & (G - 1))) * 16] = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
         }
@@ -861,7 +913,8 @@ prefill_mod_merge_kernel(const __grid_constant__ ModArgs A, int64_t rows) {
 }
 
 // ----------------------------------------------------------------------------- host side
-// The shared-memory attribute, once per (kernel, device).
+// The shared-memory attribute and a check of the build, once per (kernel, device):
+// with fewer registers than its split draws on, an 8-bit kernel would wait for ever.
 template <typename T, int FMT, bool CAP, bool ALIBI>
 pkv_status prefill_mod_configure() {
     static std::atomic<uint64_t> done{0};
@@ -870,6 +923,10 @@ pkv_status prefill_mod_configure() {
     const uint64_t bit = 1ull << (dev & 63);
     if (e == cudaSuccess && (done.load(std::memory_order_acquire) & bit)) return PKV_OK;
     auto kern = prefill_mod_kernel<T, FMT, CAP, ALIBI>;
+    cudaFuncAttributes attr;
+    if (FMT != kCode16 && e == cudaSuccess) e = cudaFuncGetAttributes(&attr, kern);
+    if (FMT != kCode16 && e == cudaSuccess && attr.numRegs < kModLaunchRegs)
+        return set_error(PKV_ERR_CUDA, "prefill: the kernel was built with %d registers, not %d", attr.numRegs, kModLaunchRegs);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ModLayout<FMT != kCode16>::kAlloc);
     if (e != cudaSuccess) return set_error(PKV_ERR_CUDA, "prefill: kernel attributes: %s", cudaGetErrorString(e));
@@ -916,6 +973,8 @@ pkv_status prefill_mod_launch(const PrefillCall &c) {
     a.pairs = c.plan.pairs;
     a.nsplit = c.plan.nsplit;
     a.sl = c.scale * log2e;
+    a.sa = CAP ? c.scale / c.mod.softcap : 0.f;
+    for (int i = 0; i < 5; ++i) a.tanh_poly[i] = static_cast<float>(kTanhFit[i] * c.mod.softcap * 1.4426950408889634);
     a.su = CAP ? 2.f * log2e * c.scale / c.mod.softcap : 0.f;
     a.capl2 = CAP ? c.mod.softcap * log2e : 0.f;
     a.o_part = reinterpret_cast<float *>(c.workspace);
@@ -923,7 +982,7 @@ pkv_status prefill_mod_launch(const PrefillCall &c) {
     a.split_used = reinterpret_cast<int32_t *>(c.workspace + c.plan.o_bytes + c.plan.ml_bytes);
     a.err_flag = c.err_flag;
     cudaError_t e = launch_pdl(kPdlDecode, prefill_mod_kernel<T, FMT, CAP, ALIBI>,
-                               dim3(a.pairs * a.nsplit, c.Hkv, c.num_seqs), dim3(kModThreads),
+                               dim3(a.pairs * a.nsplit, c.Hkv, c.num_seqs), dim3(kModThreads<FMT != kCode16>),
                                ModLayout<FMT != kCode16>::kAlloc, c.stream, mk, mv, a);
     if (e == cudaSuccess && a.nsplit > 1) {
         const int64_t rows = static_cast<int64_t>(c.num_seqs) * c.max_q_len * c.Hq;

@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kTabThreads = 512;
 constexpr int kTabWarps = kTabThreads / 32;
+constexpr int kShrinkThreads = 128;
 constexpr int kMaxTabChunks = 2048;      // chunks of ref_counts (every assigning CTA sums all their free counts)
 constexpr int kTabSmemSeqs = 4096;       // need prefixes kept in shared memory up to this many sequences
 
@@ -231,25 +232,25 @@ table_assign_kernel(int32_t *__restrict__ block_tables, int32_t max_blocks, cons
     }
 }
 
-// One warp per sequence: table entries of the blocks that hold positions
+// One CTA per sequence: table entries of the blocks that hold positions
 // [keep, len) only go back; a block is free again when its count reaches 0.
-__global__ void __launch_bounds__(kTabThreads)
+// Each entry is a load and an atomic that waits for it, so the entries of a long
+// sequence are spread over the threads.
+__global__ void __launch_bounds__(kShrinkThreads)
 table_shrink_kernel(int32_t *__restrict__ block_tables, int32_t max_blocks, const int32_t *__restrict__ keeps,
-                    const int32_t *__restrict__ lens, int32_t B, int32_t bs, int32_t *__restrict__ ref_counts,
+                    const int32_t *__restrict__ lens, int32_t bs, int32_t *__restrict__ ref_counts,
                     int32_t num_blocks, int32_t *__restrict__ err_flag) {
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int b = blockIdx.x * kTabWarps + (threadIdx.x >> 5);
-    if (b >= B) return;
+    const int b = blockIdx.x;
     const Growth g = growth_of(keeps[b], lens[b], bs, max_blocks);
     if (!g.valid) {
-        if (lane == 0 && err_flag) atomicOr(err_flag, PKV_ERRBIT_CONTEXT);
+        if (threadIdx.x == 0 && err_flag) atomicOr(err_flag, PKV_ERRBIT_CONTEXT);
         return;
     }
     int32_t *row = block_tables + static_cast<int64_t>(b) * max_blocks;
     int bits = 0;
-    for (int64_t j = g.held + lane; j < g.grown; j += 32) {
+    for (int64_t j = g.held + threadIdx.x; j < g.grown; j += kShrinkThreads) {
         const int32_t id = row[j];
         if (id == -1) continue;  // never granted, or given back already
         row[j] = -1;
@@ -334,9 +335,9 @@ extern "C" pkv_status pkv_shrink_block_tables(int32_t *block_tables, int32_t max
     if (!keeps || !lens || (max_blocks_per_seq > 0 && !block_tables) || (num_blocks > 0 && !ref_counts))
         return set_error(PKV_ERR_INVALID_ARG, "shrink: NULL pointer");
     const cudaError_t e = launch_pdl(kPdlSlotMapping, table_shrink_kernel,
-                                     dim3((num_seqs + kTabWarps - 1) / kTabWarps), dim3(kTabThreads), 0,
-                                     static_cast<cudaStream_t>(stream), block_tables, max_blocks_per_seq, keeps, lens,
-                                     num_seqs, block_size, ref_counts, num_blocks, err_flag);
+                                     dim3(num_seqs), dim3(kShrinkThreads), 0, static_cast<cudaStream_t>(stream),
+                                     block_tables, max_blocks_per_seq, keeps, lens, block_size, ref_counts,
+                                     num_blocks, err_flag);
     if (e != cudaSuccess) return set_error(PKV_ERR_CUDA, "shrink launch: %s", cudaGetErrorString(e));
     return ok();
 }
