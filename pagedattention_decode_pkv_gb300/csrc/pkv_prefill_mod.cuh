@@ -522,7 +522,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const int miss = f->miss, key0 = (j0 + (item >> 1)) * kModKeys;
                 const uint32_t src = sStage + static_cast<uint32_t>(st) * kModCodeTile;
                 const uint32_t dst = sRing + static_cast<uint32_t>(slot) * kModTile;
-#pragma unroll 4
+#pragma unroll 2  // more (4: -6 % with int8) costs the other warps their instruction cache
                 for (int i = 0; i < 8; ++i) {
                     const int rr = row0 + 8 * (i >> 1), c4 = l8 & 3;
                     const int c = c4 + 4 * (i & 1);
@@ -623,12 +623,11 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             tc_fence_after();
             const ModInfo *f = info(jj);
             float x[kHalfKeys];
+            {
+                uint32_t v[64];
+                tmem_ld64(scol, v);
 #pragma unroll
-            for (int c0 = 0; c0 < kHalfKeys; c0 += 32) {
-                uint32_t v[32];
-                tmem_ld32(scol + c0, v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[c0 + i] = __uint_as_float(v[i]);
+                for (int i = 0; i < 64; ++i) x[i] = __uint_as_float(v[i]);
             }
             // Keys a <= k < z of the half are visible to this row, but for missing pages.
             const int a = lo_r - h * kHalfKeys, z = hi_r - h * kHalfKeys;
