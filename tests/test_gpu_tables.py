@@ -83,7 +83,8 @@ def _state(rng, B, bs, nb, max_new, width, shared=False):
 
 @pytest.mark.parametrize("B,bs,nb,max_new,width", [
     (1, 1, 1, 1, 1), (1, 16, 7, 60, 6), (3, 4, 40, 9, 8), (64, 16, 20000, 1, 40), (65, 16, 1500, 300, 40),
-    (513, 256, 4096, 700, 6), (700, 16, 9001, 33, 5), (17, 48, 300000, 2000, 90), (4500, 32, 30000, 40, 4)])
+    (513, 256, 4096, 700, 6), (700, 16, 9001, 33, 5), (17, 48, 300000, 2000, 90), (4500, 32, 30000, 40, 4),
+    (2048, 16, 20000, 70, 7), (30, 16, 262144, 3000, 200), (9, 3, 1025, 500, 190)])
 def test_grow_matches_model(pkv, cuda_dev, B, bs, nb, max_new, width):
     rng = random.Random(B + bs + nb)
     tables, starts, ends, ref = _state(rng, B, bs, nb, max_new, width)
@@ -95,12 +96,13 @@ def test_grow_matches_model(pkv, cuda_dev, B, bs, nb, max_new, width):
         assert got == (t, r, cu, slots, bits)
 
 
-@pytest.mark.parametrize("nb", [0, 1, 5, 12, 30, 600, 1100])
-def test_grow_when_blocks_run_out(pkv, cuda_dev, nb):
+@pytest.mark.parametrize("times", [20, 300])
+@pytest.mark.parametrize("nb", [0, 1, 5, 12, 30, 600, 1100, 5000])
+def test_grow_when_blocks_run_out(pkv, cuda_dev, nb, times):
     """Sequences are served in order until one does not fit; later ones that need no block still are."""
     bs = 4
-    starts = [0, 3, 8, 2, 0, 5, 0] * 20
-    ends = [9, 20, 9, 4, 11, 8, 30] * 20
+    starts = [0, 3, 8, 2, 0, 5, 0] * times
+    ends = [9, 20, 9, 4, 11, 8, 30] * times
     tables = [[0 if j < _cdiv(s, bs) and nb else -1 for j in range(8)] for s in starts]
     ref = [1 if i % 3 == 0 else 0 for i in range(nb)]
     cap = sum(e - s for s, e in zip(starts, ends))
