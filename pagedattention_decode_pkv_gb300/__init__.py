@@ -511,6 +511,8 @@ def pkv_paged_attention_decode_mod(q, k_cache, v_cache, block_tables, context_le
     mod = _score_mod(softcap, alibi_slopes, key_starts, None, Hq, B, B)
     if out is None:
         out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have the shape and type of q")
     ws = pkv_paged_attention_decode_workspace_size(B, Hq, Hkv, d, bs, max_context_len, q.dtype) if B else 0
     if ws and workspace is None:
         workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
@@ -549,6 +551,8 @@ def pkv_paged_attention_prefill_mod(q, k_cache, v_cache, block_tables, starts, c
     mod = _score_mod(softcap, alibi_slopes, key_starts, prefix_lens, Hq, rows, B)
     if out is None:
         out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have the shape and type of q")
     ws = _lib.pkv_paged_attention_prefill_mod_workspace_size(B, Hq, Hkv, d, bs, max_q_len, block_tables.shape[1])
     if ws and workspace is None:
         workspace = torch.empty(ws, dtype=torch.uint8, device=dev)

@@ -101,7 +101,7 @@ struct ModLayout {
     static constexpr int kStageOff = kRingOff + kRing * kModTile;
     static constexpr int kInfoOff = kStageOff + kStage * kModCodeTile;
     static constexpr int kRangeOff = kInfoOff + 4 * 128;
-    static constexpr int kBarOff = kRangeOff + 32;
+    static constexpr int kBarOff = kRangeOff + 64;
     static constexpr int kTmemSlot = kBarOff + 320;
     static constexpr int kBytes = kTmemSlot + 16;
     static constexpr int kAlloc = kBytes + 1024;
@@ -170,7 +170,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int lg_g = A.lg_g, G = 1 << lg_g, Hq = A.Hq, bs = A.bs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    int32_t *range = reinterpret_cast<int32_t *>(smem + L::kRangeOff);  // lowest key that a row sees, highest + 1
+    int2 *range = reinterpret_cast<int2 *>(smem + L::kRangeOff);  // per softmax warp: lowest key that a row sees, highest + 1
     auto info = [&](int jj) { return reinterpret_cast<ModInfo *>(smem + L::kInfoOff + (jj & 3) * 128); };
     const uint32_t bar0 = smem_u32(smem + L::kBarOff);
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -194,8 +194,6 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             mbar_init(bar(L::kOPrev + t), 1);
             mbar_init(bar(L::kOLast + t), 1);
         }
-        range[0] = INT32_MAX;
-        range[1] = 0;
         mbar_init(bar(L::kVLand), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_tensormap(&tm_k);
@@ -234,17 +232,30 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 9) tmem_alloc(smem_u32(smem + L::kTmemSlot), 512);
-    __syncthreads();  // the barriers and `range` are initialised
 
     // Softmax threads: tile t = warp / 4, query row r of it: position r / G, head r % G.
-    const int t = warp >> 2;  // 2: service warps
+    const int t = warp >> 2;  // 2 and more: service warps
     const int r = threadIdx.x & (kModRows - 1);
     const int q0 = (tile0 - t) * positions;
     const int pi = r >> lg_g;
+    const int64_t tile_row = (static_cast<int64_t>(q_begin) + q0) * Hq + kh * G;  // the tile's first q / out row
     bool live = false;
     int pos = 0, lo_r = 0, hi_r = 0;  // the row's position and its visible keys [lo_r, hi_r)
+    // The warp's 32 Q rows, two rows of 16 chunks at a time (zeros past the sequence).  Over
+    // 16-bit caches they are in flight over the barrier; the 8-bit kernels have no registers for
+    // that before their split.
+    uint4 qv[16];
+    auto load_q = [&] {
+        const uint4 *src = static_cast<const uint4 *>(A.q) + tile_row * 16 + (lane & 15);  // 16 chunks of 16 bytes a row
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4), pr = rr >> lg_g;
+            qv[i] = t < ntiles && q0 + pr < n ? __ldg(src + (pr * Hq + (rr & (G - 1))) * 16) : make_uint4(0, 0, 0, 0);
+        }
+    };
     if (t < 2) {
-        live = tile0 - t >= 0 && q0 + pi < n;
+        if constexpr (!C8) load_q();
+        live = t < ntiles && q0 + pi < n;
         pos = start + q0 + pi;
         if (live) {
             lo_r = A.key_starts ? max(A.key_starts[q_begin + q0 + pi], 0) : 0;
@@ -253,20 +264,22 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if (lo_r >= hi_r) lo_r = hi_r = 0;
         const int lo_w = __reduce_min_sync(0xffffffffu, hi_r > 0 ? lo_r : INT32_MAX);
         const int hi_w = __reduce_max_sync(0xffffffffu, hi_r);
-        if (lane == 0 && hi_w > 0) {
-            atomicMin(range, lo_w);
-            atomicMax(range + 1, hi_w);
-        }
+        if (lane == 0) range[warp] = make_int2(lo_w, hi_w);
     }
     tc_fence_before();
-    __syncthreads();
+    __syncthreads();  // the barriers, the ranges and the TMEM address are there
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot);
     // Half blocks [h0, h1) that a row of the CTA sees any key of, cut to this split.  Both
     // tiles go through all of them: their ranges differ by a few halves at most, and every
     // barrier then passes through the same phases for everybody.
-    const int key_lo = range[0];
-    int h0 = range[1] > 0 ? key_lo / kHalfKeys : 0, h1 = range[1] > 0 ? (range[1] - 1) / kHalfKeys + 1 : 0;
+    int key_lo = INT32_MAX, key_hi = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        key_lo = min(key_lo, range[i].x);
+        key_hi = max(key_hi, range[i].y);
+    }
+    int h0 = key_hi > 0 ? key_lo / kHalfKeys : 0, h1 = key_hi > 0 ? (key_hi - 1) / kHalfKeys + 1 : 0;
     bool partial = false;
     if (A.nsplit > 1) {
         const int j0 = h0 >> 1, blocks = ((h1 + 1) >> 1) - j0;
@@ -556,23 +569,14 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if constexpr (C8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kModSoftRegs));
         const bool on = t < ntiles && h0 < h1;  // the tile exists and sees a key
         const int hd = r & (G - 1);
-        const int64_t tile_row = (static_cast<int64_t>(q_begin) + q0) * Hq + kh * G;  // the tile's first q / out row
         float rq = 1.f;  // C8: what the row's scores are multiplied by, a power of two
         if (on) {
-            // The warp's 32 Q rows into shared memory, two rows of 16 chunks at a time (zeros past the sequence)
             const uint32_t sQt = sQ + static_cast<uint32_t>(t) * kModTile;
-            const int c = lane & 15;
-            const uint4 *src = static_cast<const uint4 *>(A.q) + tile_row * 16 + c;  // 16 chunks of 16 bytes a row
-            uint4 v[16];
+            if constexpr (C8) load_q();
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4), pr = rr >> lg_g;
-                v[i] = q0 + pr < n ? __ldg(src + (pr * Hq + (rr & (G - 1))) * 16) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4);
-                st_shared_v4(sQt + (c >> 3) * kModHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+                const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4), c = lane & 15;
+                st_shared_v4(sQt + (c >> 3) * kModHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), qv[i].x, qv[i].y, qv[i].z, qv[i].w);
             }
             if constexpr (C8 && std::is_same<T, __nv_bfloat16>::value) {
                 // bf16 becomes f16 with the row's largest value moved to [2^13, 2^14), a row per
@@ -816,7 +820,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             // 16-bit rows go through the tile's Q rows in shared memory (its last QK is done),
             // so that they leave as whole lines.
             const uint32_t sOt = sQ + static_cast<uint32_t>(t) * kModTile;
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < kFastHeadDim; c0 += 32) {
                 uint32_t v[32];
                 if (on) {
@@ -847,7 +851,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 __syncwarp();
                 const int c = lane & 15;
                 uint4 *dst = static_cast<uint4 *>(A.out) + tile_row * 16 + c;
-#pragma unroll
+#pragma unroll 4
                 for (int i = 0; i < 16; ++i) {
                     const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4), pr = rr >> lg_g;
                     if (q0 + pr >= n) continue;
