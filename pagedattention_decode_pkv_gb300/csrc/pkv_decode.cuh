@@ -422,9 +422,9 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     float *scl = reinterpret_cast<float *>(smem + L::kScaleOffset);  // C8: [STAGES][2][HPC] K / V scales
     float *bscl = reinterpret_cast<float *>(smem + L::kBatchScaleOffset);  // C8: [2 batches][32][2][HPC]
     int32_t *fk = reinterpret_cast<int32_t *>(smem + L::kFirstOffset);     // MOD: first visible key
-    int32_t *dist = reinterpret_cast<int32_t *>(smem + L::kDistOffset);    // MOD: [STAGES] query - first token
+    int32_t *dist = reinterpret_cast<int32_t *>(smem + L::kDistOffset);    // MOD: [STAGES] query - first token, -1: none visible
     // stages in front of sequence b's first visible key, and its stages from there on
-    auto skipped = [&](int b) -> int { return MOD ? fk[b] / kStageTokens : 0; };
+    auto skipped = [&](int b) -> int { return MOD ? (fk[b] < 0 ? -1 - fk[b] : fk[b]) / kStageTokens : 0; };
     auto stages_of = [&](int b) -> int64_t { return (cx[b] + kStageTokens - 1) / kStageTokens - skipped(b); };
     const bool windowed = MOD && mod.key_starts != nullptr;  // the equal-length guess below does not hold
     auto pre_all = [&](int b) { return pref[b]; };
@@ -540,8 +540,10 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         cx[b] = context_ok(ctx, max_ctx, bs, max_blocks) ? ctx : 0;
         if constexpr (MOD) {
             const int first = first_key(mod.key_starts, b);
-            if (first >= cx[b]) cx[b] = 0;  // nothing visible
-            fk[b] = cx[b] > 0 ? first : 0;
+            const bool blind = first >= cx[b];  // nothing visible
+            if (blind && !new_k) cx[b] = 0;
+            // a blind sequence whose new row is to be appended goes through its last stage
+            fk[b] = cx[b] == 0 ? 0 : blind ? -1 - (cx[b] - 1) / kStageTokens * kStageTokens : first;
         }
     }
     __syncthreads();
@@ -651,7 +653,7 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             meta = min(kStageTokens, ctx - pos0) | flags | in_blk << 16;
             if constexpr (MOD) {  // tokens of the stage in front of the first visible one, and the distance of its first
                 meta |= max(fk[b] - pos0, 0) << kFrontShift;
-                far = ctx - 1 - pos0;
+                far = fk[b] < 0 ? -1 : ctx - 1 - pos0;
             }
             if constexpr (C8) {  // this stage's (block, head) scales, 0 for a block that will be skipped
                 float *dst = bscl + (buf * 32 + lane) * 2 * HPC;
@@ -958,7 +960,8 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             continue;
         }
         const int nvalid = meta & 0xff;
-        const int front = MOD ? meta >> kFrontShift & 15 : 0;  // tokens front .. nvalid - 1 are visible
+        // tokens front .. nvalid - 1 are visible
+        const int front = !MOD ? 0 : dist[slot] < 0 ? kStageTokens : meta >> kFrontShift & 15;
         const bool partial = nvalid < kStageTokens || (MOD && front > 0);
         const int hk = hg * HPC + warp;
         if (meta & kFlagFirst) {

@@ -129,6 +129,35 @@ def test_append(pkv, cuda_dev, fmt):
     sr.assert_within(out, ref, vc, vs)
 
 
+@pytest.mark.parametrize("fmt", [None, "fp8", "int8"])
+def test_append_where_nothing_is_visible(pkv, cuda_dev, fmt):
+    """A window that ends before the new token: the row is stored all the same, the output row is zero."""
+    ctx = [5, 16, 17, 900, 1, 64]
+    batch = _batch(torch.float16, 16, 8, 128, 16, ctx, 6, cuda_dev)
+    first = torch.tensor([5, 100, 3, 900, 1, 64], dtype=torch.int32, device=cuda_dev)
+    kc, ks, vc, vs = batch.k_cache, None, batch.v_cache, None
+    if fmt:
+        (kc, ks), (vc, vs) = _codes(pkv, fmt, batch, cuda_dev)
+    k2, v2 = kc.clone(), vc.clone()
+    key, value = (torch.randn(len(ctx), 8, 128, device=cuda_dev).half() for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+    out = pkv.pkv_paged_attention_decode_mod(batch.q, kc, vc, batch.block_tables, batch.context_lens, batch.scale, 900,
+                                             key=key, value=value, k_scale=ks, v_scale=vs, key_starts=first,
+                                             err_flag=err)
+    slots = torch.tensor([int(batch.block_tables[b, (c - 1) // 16]) * 16 + (c - 1) % 16 for b, c in enumerate(ctx)],
+                         dtype=torch.int32, device=cuda_dev)
+    if fmt:
+        getattr(pkv, "pkv_store_kvcache_" + fmt)(key, value, k2, v2, ks, vs, slots)
+    else:
+        pkv.pkv_store_kvcache(key, value, k2, v2, slots)
+    as_bits = (lambda x: x) if fmt else (lambda x: x.view(torch.int16))
+    assert torch.equal(as_bits(kc), as_bits(k2)) and torch.equal(as_bits(vc), as_bits(v2))
+    ref = _reference(batch.q, sr.dequantize(kc, ks), sr.dequantize(vc, vs), batch.block_tables, ctx, batch.scale,
+                     {"key_starts": first})
+    sr.assert_within(out, ref, vc, vs)
+    assert int(err.item()) == 0 and torch.count_nonzero(out[[0, 1, 3, 4, 5]]) == 0
+
+
 def test_plain_rule_gives_the_plain_call(pkv, cuda_dev):
     """Without a rule the kernel does the arithmetic of the plain call: the same bits."""
     batch = _batch(torch.bfloat16, 16, 8, 128, 16, CTX, 7, cuda_dev)
