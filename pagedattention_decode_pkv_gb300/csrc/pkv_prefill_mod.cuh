@@ -569,6 +569,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if constexpr (C8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kModSoftRegs));
         const bool on = t < ntiles && h0 < h1;  // the tile exists and sees a key
         const int hd = r & (G - 1);
+        if (!live) hi_r = INT32_MAX;  // a row that is not written must not make its warp mask
         float rq = 1.f;  // C8: what the row's scores are multiplied by, a power of two
         if (on) {
             const uint32_t sQt = sQ + static_cast<uint32_t>(t) * kModTile;
@@ -681,13 +682,16 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             if constexpr (ALIBI) {
                 // bias nslope |k - c|, c the row's own key in the half's coordinates
                 const float c = static_cast<float>(pos - h * kHalfKeys);
-                const bool past = __all_sync(0xffffffffu, pos - h * kHalfKeys >= kHalfKeys - 1);  // no key after any row
+                // on one side of every row's own key the bias is linear
+                const bool past = __all_sync(0xffffffffu, pos - h * kHalfKeys >= kHalfKeys - 1);
+                const bool ahead = __all_sync(0xffffffffu, pos - h * kHalfKeys <= 0);
+                const float by = ahead ? -nslope : nslope;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const uint64_t sl = splat2(CAP ? 1.f : C8 ? A.sl * f->ks[g0 + g] * rq : A.sl);
-                    if (past) {  // nslope (c - k), two keys on by one addition
-                        uint64_t bias = pack2(nslope * (c - 16 * g), nslope * (c - 16 * g - 1));
-                        const uint64_t on = splat2(-2.f * nslope);
+                    if (past || ahead) {  // by (c - k), two keys on by one addition
+                        uint64_t bias = pack2(by * (c - 16 * g), by * (c - 16 * g - 1));
+                        const uint64_t on = splat2(-2.f * by);
 #pragma unroll
                         for (int k = 16 * g; k < 16 * g + 16; k += 2) {
                             const uint64_t s = pack2(x[k], x[k + 1]);
@@ -715,11 +719,18 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     scaled = true;
                 }
             }
-            if (!open) {
+            if (!open) {  // one boundary at a time: seldom more than one of them is in a warp's half
+                if (__any_sync(0xffffffffu, z < kHalfKeys)) {
 #pragma unroll
-                for (int k = 0; k < kHalfKeys; ++k) {
-                    const bool seen = k >= a && k < z && !(miss >> (k >> 4) & 1);
-                    x[k] = seen ? x[k] : -INFINITY;
+                    for (int k = 0; k < kHalfKeys; ++k) x[k] = k < z ? x[k] : -INFINITY;
+                }
+                if (__any_sync(0xffffffffu, a > 0)) {
+#pragma unroll
+                    for (int k = 0; k < kHalfKeys; ++k) x[k] = k >= a ? x[k] : -INFINITY;
+                }
+                if (miss) {
+#pragma unroll
+                    for (int k = 0; k < kHalfKeys; ++k) x[k] = miss >> (k >> 4) & 1 ? -INFINITY : x[k];
                 }
             }
             // 3. the half's maximum, of s + log2 vs for 8-bit caches
