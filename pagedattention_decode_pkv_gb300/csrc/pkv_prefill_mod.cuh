@@ -16,9 +16,10 @@
 // programming on a Chebyshev grid): 3e-7, at seven packed FMA-unit operations a pair
 // of scores.  Larger scores take c tanh(u) = c - 2 c / (1 + e^{2u}), one exponential and
 // one reciprocal, off by a few 2^-23 c: two more trips through the special-function
-// unit, which the softmax needs as well (8 prompts of 4k, cap 50: 1432 us with it
-// alone).  Both errors are far below the rounding of P; the one-instruction tanh
-// (relative 2^-11) is not.
+// unit, which the softmax needs as well (8 prompts of 4k, cap 50: 1432 us with that
+// alone, 1279 with the polynomial, at that step of the kernel).  Both errors are far
+// below the rounding of P; the one-instruction tanh (relative 2^-11) is not.  A capped
+// score is bounded, so over bf16 caches P = 2^s needs no reference maximum (kFreeCap).
 //
 // 8-bit caches: K_t = ks code, V_t = vs code, one scale per (block, KV head).  Both
 // code formats are exact in f16, so K and V codes are widened to f16 tiles by
@@ -29,19 +30,29 @@
 // score's factor), so no bf16 magnitude overflows.
 //
 // The CTA.  Two tiles of 128 query rows (128 / G positions x G heads) of one KV
-// head, accumulators in tensor memory: 12 warps, of which eight softmax warps hold
-// one query row per thread, one producer copies pages by TMA, one issues the
-// tcgen05.mma, two widen codes.  K and V come in blocks of 128 keys through one
-// ring of 32 KB tiles in order K_0 V_0 K_1 V_1 ..; the work goes by half blocks of
-// 64 keys.  Per tile and half block h: S_h = Q K_h^T, softmax, P_h (16 bit, over
-// S_h's columns), O += P_h V_h.  A tile has two S buffers of 64 columns and
-// QK_{h+2} follows PV_h into the buffer that P_h leaves, so that S_{h+1} is there
-// when the softmax of h ends and its warps never wait for the tensor core's round
-// trip; with one 128-column buffer they waited more than half of the time.
+// head, accumulators in tensor memory: eight softmax warps hold one query row per
+// thread, one producer warp copies pages by TMA, two warps issue the tcgen05.mma, one
+// for each tile, and over 8-bit caches four widen codes.  K and V come in blocks of 128
+// keys through one ring of 32 KB tiles in order K_0 V_0 K_1 V_1 ..; the work goes by
+// half blocks of 64 keys.  Per tile and half block h: S_h = Q K_h^T, softmax, P_h (16
+// bit, over S_h's columns), O += P_h V_h.  A tile has two S buffers of 64 columns and
+// QK_{h+2} follows PV_h into the buffer that P_h leaves, so that S_{h+1} is there when
+// the softmax of h ends and its warps never wait for the tensor core's round trip.
+//
+// What bounds it.  Plain scores, 8 prompts of 4k (32 heads, 8 KV heads): 927 us, 1070
+// TFLOP/s.  A step of 64 keys of both tiles is 1240 clk of products alone: Q K^T at 64
+// keys reads its operands from shared memory at 386 clk where the arithmetic takes 256
+// (128 keys at once, one S buffer a tile, read less and ran 976 us: both tiles then sit
+// in their softmax together).  With the copies into the ring the step is 1534, with the
+// softmax warps beside it 1834.  Cap 50: 1071 us; the polynomial's operations come on
+// top.  E4M3 and int8: 1360 and 1420; widening writes every tile once more.  Short
+// spans: of a CTA's ~15k clk of setup, first products and output nothing overlaps, for
+// both tiles do them together (2 x 8k rows of packed documents of 60 to 2500 rows: 169
+// us, 589 TFLOP/s).
 //
 // Few rows over a long context (a small chunk, few sequences) leave most SMs idle,
 // so the blocks of a tile pair are cut into up to nsplit runs, one CTA each, whose
-// (O, m, l) a second kernel joins.
+// (O, m, l) a second kernel joins (prefill_plan).
 #pragma once
 
 #include <cuda.h>
@@ -78,6 +89,13 @@ constexpr int kModHalf = kModTile / 2;
 constexpr int kModCodeTile = 16384;   // the same tile in codes
 constexpr uint64_t kModDeadlineNs = 2000000000ull;
 constexpr float kModRescale = 8.f;    // log2 units a block may exceed the reference maximum by before O is rescaled
+// CAP: no cap, a cap, or a cap that bounds the scores so far that no reference
+// maximum is needed: P = 2^s itself, |s| <= kFreeCap, is in bf16's range with all its
+// bits, and its sums times V are in f32's as long as keys x max |V| < 2^54. Without the
+// maximum and the rescaling 8 prompts of 4096 rows (32 heads, 8 KV heads, cap 50) take
+// 1071 us instead of 1249.
+enum { kNoCap = 0, kCap = 1, kCapBounded = 2 };
+constexpr float kFreeCap = 73.f;
 constexpr float kTanhLimit = 0.7f;    // |score / cap| up to which the polynomial stands for tanh
 constexpr double kTanhFit[5] = {0.9999996973, -0.3333021287, 0.1328111218, -0.05083622068, 0.0137736928};
 constexpr int kMinSplitBlocks = 2;    // blocks of a split at least
@@ -153,7 +171,7 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&x)[4]) {
                  : "memory");
 }
 
-template <typename T, int FMT, bool CAP, bool ALIBI>
+template <typename T, int FMT, int CAP, bool ALIBI>
 __global__ void __launch_bounds__(kModThreads<FMT != kCode16>, 1)
 prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ ModArgs A) {
@@ -163,6 +181,8 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     using M16 = typename std::conditional<C8, __half, T>::type;  // operand type of the products
     using H = Half16<M16>;
     constexpr bool kBf16 = std::is_same<M16, __nv_bfloat16>::value;
+    constexpr bool kFree = CAP == kCapBounded;
+    static_assert(!kFree || (kBf16 && !ALIBI), "P = 2^s needs bf16's range and bounded scores");
     constexpr int kRing = L::kRing;
     const int b = blockIdx.z, kh = blockIdx.y;
     const int pair = blockIdx.x / A.nsplit, split = blockIdx.x - pair * A.nsplit;
@@ -615,7 +635,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         const float nslope = ALIBI && A.slopes && live ? -A.slopes[kh * G + hd] * 1.4426950408889634f : 0.f;
         // this warp's TMEM lanes (32 (warp % 4) ..) in the tile's columns: S / P at 0 and 64, O at 128
         const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 256;
-        float m_ref = -INFINITY, l_sum = 0.f;
+        float m_ref = kFree ? 0.f : -INFINITY, l_sum = 0.f;
         for (int h = h0; on && h < h1; ++h) {
             const int jj = (h >> 1) - j0, g0 = (h & 1) * 4;  // the half's first group of 16 keys
             const uint32_t scol = trow + (h & 1) * kHalfKeys;
@@ -734,8 +754,11 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
             }
             // 3. the half's maximum, of s + log2 vs for 8-bit caches
-            float mx;
-            if constexpr (C8) {
+            float mx, resc = 1.f;
+            bool moved = false;
+            if constexpr (kFree) {
+                mx = 0.f;
+            } else if constexpr (C8) {
                 mx = -INFINITY;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
@@ -753,9 +776,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 if (RAW) mx *= A.sl;
             }
-            float resc = 1.f;
-            bool moved = false;
-            if (mx > m_ref + kModRescale) {  // also the row's first visible key (m_ref = -inf)
+            if (!kFree && mx > m_ref + kModRescale) {  // also the row's first visible key (m_ref = -inf)
                 if (m_ref != -INFINITY) {
                     resc = fast_exp2(m_ref - mx);
                     moved = true;
@@ -765,7 +786,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             // O moves with the reference, once the PV before this half's is done: the next S
             // stands for it, or its own barrier in the tile's last half.  (A row has no
             // reference to move in the tile's first half.)
-            if (__any_sync(0xffffffffu, moved)) {  // TMEM access is warp-wide; a factor of 1 leaves a row as it is
+            if (!kFree && __any_sync(0xffffffffu, moved)) {  // TMEM access is warp-wide; a factor of 1 leaves a row as it is
                 ok = h + 1 < h1 ? mbar_wait(bar(L::kSFull + 2 * t + ((h + 1) & 1)), ((h + 1 - h0) >> 1) & 1, deadline)
                                   : mbar_wait(bar(L::kOPrev + t), 0, deadline);
                 if (!__all_sync(0xffffffffu, ok)) {
@@ -796,7 +817,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     const int k = 16 * g + 2 * i, o = 8 * g + i;
                     float e0, e1;
                     const uint64_t s = pack2(x[k], x[k + 1]);
-                    unpack2(RAW ? fma2(s, mul, nb2) : add2(s, nb2), e0, e1);
+                    unpack2(RAW ? fma2(s, mul, nb2) : kFree ? s : add2(s, nb2), e0, e1);
                     e0 = fast_exp2(e0);
                     e1 = fast_exp2(e1);
                     if constexpr (C8) {
@@ -929,7 +950,7 @@ prefill_mod_merge_kernel(const __grid_constant__ ModArgs A, int64_t rows) {
 // ----------------------------------------------------------------------------- host side
 // The shared-memory attribute and a check of the build, once per (kernel, device):
 // with fewer registers than its split draws on, an 8-bit kernel would wait for ever.
-template <typename T, int FMT, bool CAP, bool ALIBI>
+template <typename T, int FMT, int CAP, bool ALIBI>
 pkv_status prefill_mod_configure() {
     static std::atomic<uint64_t> done{0};
     int dev = 0;
@@ -948,7 +969,7 @@ pkv_status prefill_mod_configure() {
     return PKV_OK;
 }
 
-template <typename T, int FMT, bool CAP, bool ALIBI>
+template <typename T, int FMT, int CAP, bool ALIBI>
 pkv_status prefill_mod_launch(const PrefillCall &c) {
     int box_rows = kModKeys;  // chunk: gcd(block_size, 128) keys, consecutive in a page
     while (c.block_size % box_rows) box_rows >>= 1;
@@ -1015,8 +1036,11 @@ pkv_status prefill_mod_format(const PrefillCall &c) {
     // wants it positive; other scales take the bias kernel with a bias of 0.
     const bool bias = c.mod.alibi_slopes || (!cap && !(c.scale > 1e-30f));
 #define PKV_MOD(T) \
-    (cap ? (bias ? prefill_mod_launch<T, FMT, true, true>(c) : prefill_mod_launch<T, FMT, true, false>(c)) \
-         : (bias ? prefill_mod_launch<T, FMT, false, true>(c) : prefill_mod_launch<T, FMT, false, false>(c)))
+    (cap ? (bias ? prefill_mod_launch<T, FMT, kCap, true>(c) : prefill_mod_launch<T, FMT, kCap, false>(c)) \
+         : (bias ? prefill_mod_launch<T, FMT, kNoCap, true>(c) : prefill_mod_launch<T, FMT, kNoCap, false>(c)))
+    if constexpr (FMT == kCode16)
+        if (c.dtype == PKV_BF16 && cap && !bias && c.mod.softcap * 1.4426950408889634f <= kFreeCap)
+            return prefill_mod_launch<__nv_bfloat16, FMT, kCapBounded, false>(c);
     return c.dtype == PKV_BF16 ? PKV_MOD(__nv_bfloat16) : PKV_MOD(__half);
 #undef PKV_MOD
 }

@@ -124,6 +124,18 @@ def test_split_keys(pkv, cuda_dev, rule, fmt, spans):
            _codes(pkv, fmt, batch, 8, cuda_dev) if fmt else None, max_q=max(ns) + 300)
 
 
+@pytest.mark.parametrize("softcap", [0.01, 3.0, 50.5, 51.0, 300.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("q_gain", [0.1, 30.0])
+def test_caps_of_any_size(pkv, cuda_dev, softcap, dtype, q_gain):
+    """Scores far below and far above the cap (up to where tanh is 1), caps on both sides of the
+    bound up to which P needs no reference maximum, whole rows of scores at minus the cap."""
+    spans = [(0, 150), (700, 20)]
+    batch, q, starts, cu, ns = _case(dtype, 8, 8, 16, spans, 11, cuda_dev, q_gain)
+    q[::7] = -q_gain * batch.k_cache[batch.block_tables[0, 0].item(), 0].to(dtype)  # against key 0
+    _check(pkv, batch, q, starts, cu, ns, spans, {"softcap": softcap}, batch.scale)
+
+
 def test_plain_rule_equals_the_plain_call(pkv, cuda_dev):
     """Both kernels round P the same way; their reference maxima move alike, so only the summing order differs."""
     batch, q, starts, cu, ns = _case(torch.bfloat16, 16, 8, 16, SPANS, 6, cuda_dev)
