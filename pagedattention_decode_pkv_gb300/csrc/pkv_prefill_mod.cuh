@@ -47,8 +47,8 @@
 // softmax warps beside it 1834.  Cap 50: 1071 us; the polynomial's operations come on
 // top.  E4M3 and int8: 1360 and 1420; widening writes every tile once more.  Short
 // spans: of a CTA's ~15k clk of setup, first products and output nothing overlaps, for
-// both tiles do them together (2 x 8k rows of packed documents of 60 to 2500 rows: 169
-// us, 589 TFLOP/s).
+// both tiles do them together (2 x 8k rows of packed documents of 60 to 2500 rows: 162
+// us, 614 TFLOP/s).
 //
 // Few rows over a long context (a small chunk, few sequences) leave most SMs idle,
 // so the blocks of a tile pair are cut into up to nsplit runs, one CTA each, whose
@@ -646,6 +646,20 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 break;
             }
             tc_fence_after();
+            // Keys a <= k < z of the half are visible to this row, but for missing pages.
+            const int a = lo_r - h * kHalfKeys, z = hi_r - h * kHalfKeys;
+            // A warp that sees none of them (the other tile's keys, rows past the sequence) is
+            // done: P = 0.  Packed documents 162 us against 169; the capped and the 8-bit kernels
+            // lose 2 % by the longer loop (1071 us to 1097, 547 to 560) and go without.
+            if (!CAP && !C8 && __all_sync(0xffffffffu, !live || a >= kHalfKeys || z <= 0)) {
+                const uint32_t none[32] = {};
+                tmem_st32(scol, none);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::kPFull + 2 * t + (h & 1)));
+                continue;
+            }
             const ModInfo *f = info(jj);
             float x[kHalfKeys];
             {
@@ -654,8 +668,6 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll
                 for (int i = 0; i < 64; ++i) x[i] = __uint_as_float(v[i]);
             }
-            // Keys a <= k < z of the half are visible to this row, but for missing pages.
-            const int a = lo_r - h * kHalfKeys, z = hi_r - h * kHalfKeys;
             const int miss = f->miss >> g0 & 15;
             const bool open = __all_sync(0xffffffffu, a <= 0 && z >= kHalfKeys && miss == 0);
             // 1. scores in log2 units (RAW: left as they are, factor `mul` below)
