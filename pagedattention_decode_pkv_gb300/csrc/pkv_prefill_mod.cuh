@@ -185,12 +185,16 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     static_assert(!kFree || (kBf16 && !ALIBI), "P = 2^s needs bf16's range and bounded scores");
     constexpr int kRing = L::kRing;
     const int b = blockIdx.z, kh = blockIdx.y;
-    const int pair = blockIdx.x / A.nsplit, split = blockIdx.x - pair * A.nsplit;
+    const int pair = A.nsplit == 1 ? blockIdx.x : blockIdx.x / A.nsplit, split = blockIdx.x - pair * A.nsplit;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int lg_g = A.lg_g, G = 1 << lg_g, Hq = A.Hq, bs = A.bs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    int2 *range = reinterpret_cast<int2 *>(smem + L::kRangeOff);  // per softmax warp: lowest key that a row sees, highest + 1
+    // [0, 1]: the lowest key that a row of the CTA sees, the highest + 1.  [2, 3]: the sequence's
+    // first row and row count, which the epilogue reads again: kept in registers over the loop
+    // they cost its warps more (E4M3 chunks 547 us against 541).
+    volatile int32_t *cta = reinterpret_cast<volatile int32_t *>(smem + L::kRangeOff);
+    int raw0 = 0, raw1 = 0;  // producer: table entries of the first two blocks
     auto info = [&](int jj) { return reinterpret_cast<ModInfo *>(smem + L::kInfoOff + (jj & 3) * 128); };
     const uint32_t bar0 = smem_u32(smem + L::kBarOff);
     auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -232,7 +236,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     if (tile0 < 0) return;
     const int64_t total64 = static_cast<int64_t>(start) + n;
     T *out = static_cast<T *>(A.out);
-    if (start < 0 || (total64 + bs - 1) / bs > A.max_blocks || total64 > INT32_MAX - 2 * kModKeys) {
+    if (start < 0 || total64 > static_cast<int64_t>(A.max_blocks) * bs || total64 > INT32_MAX - 2 * kModKeys) {
         if (split != 0) return;  // a bad span: zero rows and a flag
         if (first && threadIdx.x == 0 && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_CONTEXT);
         if (A.nsplit > 1 && kh == 0 && threadIdx.x == 0) A.split_used[static_cast<int64_t>(b) * A.pairs + pair] = 1;
@@ -260,45 +264,74 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int pi = r >> lg_g;
     const int64_t tile_row = (static_cast<int64_t>(q_begin) + q0) * Hq + kh * G;  // the tile's first q / out row
     bool live = false;
-    int pos = 0, lo_r = 0, hi_r = 0;  // the row's position and its visible keys [lo_r, hi_r)
+    int pos = 0;  // the row's position
     // The warp's 32 Q rows, two rows of 16 chunks at a time (zeros past the sequence).  Over
     // 16-bit caches they are in flight over the barrier; the 8-bit kernels have no registers for
-    // that before their split.
+    // that before their split.  Row and head of r0 + 2 i are those of r0 plus those of 2 i (their
+    // bits are apart), so what depends on i is uniform: a CTA's first instructions are fetched
+    // anew, and cost more than they do.
     uint4 qv[16];
     auto load_q = [&] {
-        const uint4 *src = static_cast<const uint4 *>(A.q) + tile_row * 16 + (lane & 15);  // 16 chunks of 16 bytes a row
+        const int r0 = (warp & 3) * 32 + (lane >> 4), pr = r0 >> lg_g;
+        const uint4 *src = static_cast<const uint4 *>(A.q) + (tile_row + pr * Hq + (r0 & (G - 1))) * 16 + (lane & 15);
+        const int left = t < ntiles ? n - q0 - pr : 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4), pr = rr >> lg_g;
-            qv[i] = t < ntiles && q0 + pr < n ? __ldg(src + (pr * Hq + (rr & (G - 1))) * 16) : make_uint4(0, 0, 0, 0);
+            const int up = (2 * i) >> lg_g;
+            qv[i] = up < left ? __ldg(src + (up * Hq + ((2 * i) & (G - 1))) * 16) : make_uint4(0, 0, 0, 0);
         }
+    };
+    // The sequence's table entry for this lane's 16 keys of block j (0: none)
+    const int32_t *table = A.block_tables + static_cast<int64_t>(b) * A.max_blocks;
+    auto owned = [&](int j) { return lane < 8 && j * kModKeys + 16 * lane < total; };
+    auto entry = [&](int j) -> int {  // key / bs < ceil(total / bs) <= max_blocks
+        return owned(j) ? table[(j * kModKeys + 16 * lane) / bs] : 0;
     };
     if (t < 2) {
         if constexpr (!C8) load_q();
         live = t < ntiles && q0 + pi < n;
         pos = start + q0 + pi;
-        if (live) {
-            lo_r = A.key_starts ? max(A.key_starts[q_begin + q0 + pi], 0) : 0;
-            hi_r = min(total, max(pos + 1, A.prefix_lens ? A.prefix_lens[b] : 0));
+    } else if (warp == 8) {
+        // What the first copy waits for is a chain of loads (offsets, key starts, table entries):
+        // the producer goes through it alone, beside the loads of Q, which take longer.  (Key
+        // starts by every row, behind its Q, and the table entries behind the barrier: the first
+        // S 1800 clk later, 8 prompts of 4k, cap 50, 1071 us against 1052, packed documents 163
+        // against 156.)
+        const int prefix = A.prefix_lens ? A.prefix_lens[b] : 0;
+        const int p0 = (tile0 - ntiles + 1) * positions, p1 = min(n, (tile0 + 1) * positions);
+        int key_lo = 0, key_hi = min(total, max(start + p1, prefix));
+        if (A.key_starts) {
+            int lo = INT32_MAX, hi = 0;
+#pragma unroll
+            for (int i = 0; i < 2 * kModRows / 32; ++i) {
+                const int p = p0 + 32 * i + lane;
+                const int from = p < p1 ? max(A.key_starts[q_begin + p], 0) : INT32_MAX;
+                const int to = min(total, max(start + p + 1, prefix));
+                if (from < to) {
+                    lo = min(lo, from);
+                    hi = max(hi, to);
+                }
+            }
+            key_lo = __reduce_min_sync(0xffffffffu, lo);
+            key_hi = __reduce_max_sync(0xffffffffu, hi);
         }
-        if (lo_r >= hi_r) lo_r = hi_r = 0;
-        const int lo_w = __reduce_min_sync(0xffffffffu, hi_r > 0 ? lo_r : INT32_MAX);
-        const int hi_w = __reduce_max_sync(0xffffffffu, hi_r);
-        if (lane == 0) range[warp] = make_int2(lo_w, hi_w);
+        if (lane == 0) {
+            cta[0] = key_lo;
+            cta[1] = key_hi;
+            cta[2] = q_begin;
+            cta[3] = n;
+        }
+        raw0 = entry(key_lo / kModKeys);
+        raw1 = entry(key_lo / kModKeys + 1);
     }
     tc_fence_before();
-    __syncthreads();  // the barriers, the ranges and the TMEM address are there
+    __syncthreads();  // the barriers, the range and the TMEM address are there
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot);
     // Half blocks [h0, h1) that a row of the CTA sees any key of, cut to this split.  Both
     // tiles go through all of them: their ranges differ by a few halves at most, and every
     // barrier then passes through the same phases for everybody.
-    int key_lo = INT32_MAX, key_hi = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        key_lo = min(key_lo, range[i].x);
-        key_hi = max(key_hi, range[i].y);
-    }
+    const int key_lo = cta[0], key_hi = cta[1];
     int h0 = key_hi > 0 ? key_lo / kHalfKeys : 0, h1 = key_hi > 0 ? (key_hi - 1) / kHalfKeys + 1 : 0;
     bool partial = false;
     if (A.nsplit > 1) {
@@ -324,13 +357,8 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             // Lane g < 8 owns keys 16 g .. 16 g + 15 of the block; the first lane of each
             // chunk of 2^box_lg keys (consecutive in one page) copies it.  Table entries are
             // loaded two blocks ahead and scales one, so that no copy waits for them.
-            const int32_t *row = A.block_tables + static_cast<int64_t>(b) * A.max_blocks;
             const int box_rows = 1 << A.box_lg;
             bool bad = false;
-            auto owned = [&](int j) { return lane < 8 && j * kModKeys + 16 * lane < total; };
-            auto entry = [&](int j) -> int {  // key / bs < ceil(total / bs) <= max_blocks
-                return owned(j) ? row[(j * kModKeys + 16 * lane) / bs] : 0;
-            };
             // a page id, -1 past the sequence, -2 out of range
             auto page = [&](int j, int raw) -> int {
                 if (!owned(j)) return -1;
@@ -378,9 +406,12 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             int id = -1, next_raw = 0;
             float ks = 1.f, vs = 1.f;
             if (nb > 0) {
-                const int raw = entry(j0);
-                next_raw = entry(j0 + 1);
-                id = page(j0, raw);
+                if (split != 0) {  // the first split starts at the lowest key's block
+                    raw0 = entry(j0);
+                    raw1 = entry(j0 + 1);
+                }
+                id = page(j0, raw0);
+                next_raw = raw1;
                 ks = scale_of(A.k_scale, id);
                 vs = scale_of(A.v_scale, id);
             }
@@ -589,7 +620,13 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         if constexpr (C8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kModSoftRegs));
         const bool on = t < ntiles && h0 < h1;  // the tile exists and sees a key
         const int hd = r & (G - 1);
-        if (!live) hi_r = INT32_MAX;  // a row that is not written must not make its warp mask
+        // The row's visible keys [lo_r, hi_r).  A row that is not written must not make its warp mask.
+        int lo_r = 0, hi_r = INT32_MAX;
+        if (live) {
+            lo_r = A.key_starts ? max(A.key_starts[q_begin + q0 + pi], 0) : 0;
+            hi_r = min(total, max(pos + 1, A.prefix_lens ? A.prefix_lens[b] : 0));
+            if (lo_r >= hi_r) lo_r = hi_r = 0;
+        }
         float rq = 1.f;  // C8: what the row's scores are multiplied by, a power of two
         if (on) {
             const uint32_t sQt = sQ + static_cast<uint32_t>(t) * kModTile;
@@ -857,6 +894,9 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             timed_out = true;
         } else if (__any_sync(0xffffffffu, live)) {
             tc_fence_after();
+            const int q_begin = cta[2], n = cta[3];
+            const int q0 = (((n + positions - 1) >> (7 - lg_g)) - 1 - 2 * pair - t) * positions, pi = r >> lg_g, hd = r & (G - 1);
+            const int64_t tile_row = (static_cast<int64_t>(q_begin) + q0) * Hq + kh * G;
             const float inv = l_sum > 0.f ? 1.f / l_sum : (l_sum == l_sum ? 0.f : l_sum);
             const int64_t prow = ((static_cast<int64_t>(b) * A.max_q_len + q0 + pi) * Hq + kh * G + hd) * A.nsplit + split;
             if (partial && live) A.ml_part[prow] = make_float2(m_ref, l_sum);
