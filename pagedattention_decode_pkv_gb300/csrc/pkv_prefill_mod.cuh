@@ -236,7 +236,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     if (tile0 < 0) return;
     const int64_t total64 = static_cast<int64_t>(start) + n;
     T *out = static_cast<T *>(A.out);
-    if (start < 0 || total64 > static_cast<int64_t>(A.max_blocks) * bs || total64 > INT32_MAX - 2 * kModKeys) {
+    if (start < 0 || total64 > static_cast<int64_t>(A.max_blocks) * bs || total64 > INT32_MAX - 4 * kModKeys) {
         if (split != 0) return;  // a bad span: zero rows and a flag
         if (first && threadIdx.x == 0 && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_CONTEXT);
         if (A.nsplit > 1 && kh == 0 && threadIdx.x == 0) A.split_used[static_cast<int64_t>(b) * A.pairs + pair] = 1;
@@ -312,8 +312,8 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     hi = max(hi, to);
                 }
             }
-            key_lo = __reduce_min_sync(0xffffffffu, lo);
             key_hi = __reduce_max_sync(0xffffffffu, hi);
+            key_lo = key_hi > 0 ? __reduce_min_sync(0xffffffffu, lo) : 0;  // 0 where no row sees a key
         }
         if (lane == 0) {
             cta[0] = key_lo;

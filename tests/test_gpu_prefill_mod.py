@@ -166,6 +166,17 @@ def test_nonfinite_in_masked_places(pkv, cuda_dev, fmt):
     _check(pkv, batch, q, starts, cu, ns, spans, {"key_starts": ks}, batch.scale, caches)
 
 
+@pytest.mark.parametrize("fmt", [None, "int8"])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_tiles_that_see_nothing(pkv, cuda_dev, fmt, softcap):
+    """No row of whole query tiles sees a key: zero rows, nothing read for them, no error."""
+    spans = [(0, 400), (600, 70), (30, 20)]
+    batch, q, starts, cu, ns = _case(torch.bfloat16, 16, 8, 16, spans, 21, cuda_dev)
+    ks = torch.tensor([2 ** 31 - 1] * 300 + [310] * 100 + [2 ** 31 - 1] * 70 + [50] * 20, dtype=torch.int32, device=cuda_dev)
+    _check(pkv, batch, q, starts, cu, ns, spans, {"key_starts": ks, "softcap": softcap}, batch.scale,
+           _codes(pkv, fmt, batch, 3, cuda_dev) if fmt else None)
+
+
 @pytest.mark.parametrize("fmt", ["fp8", "int8"])
 @pytest.mark.parametrize("gain", [1e-30, 1.0, 1e15])
 def test_extreme_scales(pkv, cuda_dev, fmt, gain):
