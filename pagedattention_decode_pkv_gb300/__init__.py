@@ -175,6 +175,22 @@ def _raw_stream(dev, stream):
     return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 
+def _empty(n, dtype, dev, stream):
+    """An uninitialised tensor that belongs to the stream its kernel runs on: what the
+    allocator hands out has no pending use there, and a workspace that is freed on return
+    is not given to another stream while the kernel still runs."""
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=dev)
+
+
+def _flag(err_flag):
+    if err_flag is not None and err_flag.dtype != torch.int32:
+        raise TypeError("err_flag must be int32")
+    return _addr(err_flag)
+
+
 def _call(dev, fn, *args):
     """Calls a library function with `dev` current and raises on its status."""
     if torch.cuda.current_device() == dev.index:
@@ -235,18 +251,18 @@ def pkv_grow_block_tables(block_tables, starts, ends, ref_counts, block_size: in
     B, max_blocks = _table_args(block_tables, starts, ends, ref_counts, ("starts", "ends"))
     nb = ref_counts.numel()
     if cu_new is None:
-        cu_new = (torch.empty if B else torch.zeros)(B + 1, dtype=torch.int32, device=dev)
+        cu_new = _empty(B + 1, torch.int32, dev, stream) if B else torch.zeros(1, dtype=torch.int32, device=dev)
     if out is None:
-        out = torch.empty(num_new_tokens, dtype=torch.int32, device=dev)
+        out = _empty(num_new_tokens, torch.int32, dev, stream)
     _want(cu_new, torch.int32, "cu_new")
     _want(out, torch.int32, "out")
     if cu_new.numel() != B + 1 or out.numel() != num_new_tokens:
         raise ValueError("cu_new needs num_seqs + 1 entries and out num_new_tokens")
     if workspace is None:
-        workspace = torch.empty(_lib.pkv_grow_block_tables_workspace_size(B, nb), dtype=torch.uint8, device=dev)
+        workspace = _empty(_lib.pkv_grow_block_tables_workspace_size(B, nb), torch.uint8, dev, stream)
     _call(dev, _lib.pkv_grow_block_tables, _addr(block_tables), max_blocks, _addr(starts), _addr(ends), B, block_size,
           _addr(ref_counts), nb, _addr(cu_new), _addr(out), num_new_tokens, _addr(workspace),
-          workspace.numel() * workspace.element_size(), _addr(err_flag), _raw_stream(dev, stream))
+          workspace.numel() * workspace.element_size(), _flag(err_flag), _raw_stream(dev, stream))
     return cu_new, out
 
 
@@ -256,7 +272,7 @@ def pkv_shrink_block_tables(block_tables, keeps, lens, ref_counts, block_size: i
     dev = _device_of(block_tables, keeps, lens, ref_counts, err_flag)
     B, max_blocks = _table_args(block_tables, keeps, lens, ref_counts, ("keeps", "lens"))
     _call(dev, _lib.pkv_shrink_block_tables, _addr(block_tables), max_blocks, _addr(keeps), _addr(lens), B, block_size,
-          _addr(ref_counts), ref_counts.numel(), _addr(err_flag), _raw_stream(dev, stream))
+          _addr(ref_counts), ref_counts.numel(), _flag(err_flag), _raw_stream(dev, stream))
 
 
 def pkv_store_kvcache(key, value, k_cache, v_cache, slot_mapping, *, err_flag=None, stream=None):
@@ -513,17 +529,17 @@ def pkv_paged_attention_decode_mod(q, k_cache, v_cache, block_tables, context_le
         raise ValueError("key, value: [num_seqs, num_kv_heads, head_dim] of the q dtype")
     mod = _score_mod(softcap, alibi_slopes, key_starts, None, Hq, B, B)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, dev, stream)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have the shape and type of q")
     ws = pkv_paged_attention_decode_workspace_size(B, Hq, Hkv, d, bs, max_context_len, q.dtype) if B else 0
     if ws and workspace is None:
-        workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+        workspace = _empty(ws, torch.uint8, dev, stream)
     _call(dev, _lib.pkv_paged_attention_decode_mod, _addr(out), _addr(q), _addr(key), _addr(value), _addr(k_cache),
           _addr(v_cache), _addr(k_scale), _addr(v_scale), fmt, _addr(block_tables), block_tables.shape[1],
           _addr(context_lens), B, Hq, Hkv, d, bs, nb, max_context_len, scale, ctypes.byref(mod), _DTYPE[q.dtype],
           _addr(workspace) if ws else None, workspace.numel() * workspace.element_size() if ws else 0,
-          _addr(err_flag), _raw_stream(dev, stream))
+          _flag(err_flag), _raw_stream(dev, stream))
     return out
 
 
@@ -553,16 +569,16 @@ def pkv_paged_attention_prefill_mod(q, k_cache, v_cache, block_tables, starts, c
         raise ValueError("inconsistent shapes")
     mod = _score_mod(softcap, alibi_slopes, key_starts, prefix_lens, Hq, rows, B)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, dev, stream)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have the shape and type of q")
     ws = _lib.pkv_paged_attention_prefill_mod_workspace_size(B, Hq, Hkv, d, bs, max_q_len, block_tables.shape[1])
     if ws and workspace is None:
-        workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+        workspace = _empty(ws, torch.uint8, dev, stream)
     _call(dev, _lib.pkv_paged_attention_prefill_mod, _addr(out), _addr(q), _addr(k_cache), _addr(v_cache),
           _addr(k_scale), _addr(v_scale), fmt, _addr(block_tables), block_tables.shape[1], _addr(starts), _addr(cu_q), B,
           max_q_len, Hq, Hkv, d, bs, nb, scale, ctypes.byref(mod), _DTYPE[q.dtype], _addr(workspace) if ws else None,
-          workspace.numel() * workspace.element_size() if ws else 0, _addr(err_flag), _raw_stream(dev, stream))
+          workspace.numel() * workspace.element_size() if ws else 0, _flag(err_flag), _raw_stream(dev, stream))
     return out
 
 
