@@ -174,8 +174,9 @@ PKV_API pkv_status pkv_compute_slot_mapping(const int32_t *block_tables, int32_t
  *                     sequence b's new positions from cu_new[b] on, and -1 past
  *                     cu_new[num_seqs] (the store skips those), so that
  *                     num_new_tokens may be an upper bound
- *     workspace       pkv_grow_block_tables_workspace_size bytes, 256-byte
- *                     aligned; calls that may overlap need one each
+ *     workspace       pkv_grow_block_tables_workspace_size bytes (0 for small
+ *                     calls), 256-byte aligned; calls that may overlap need one
+ *                     each
  *   Device errors: a sequence that gets no blocks keeps its counts, its new
  *   table entries and slots are -1, PKV_ERRBIT_NO_BLOCKS; lengths that are
  *   negative, decreasing or longer than the table row: slots -1, table as it
@@ -193,7 +194,7 @@ PKV_API pkv_status pkv_compute_slot_mapping(const int32_t *block_tables, int32_t
  *
  * num_blocks * block_size < 2^31, at most 65535 sequences per call.
  */
-PKV_API size_t pkv_grow_block_tables_workspace_size(int32_t num_seqs, int32_t num_blocks);
+PKV_API size_t pkv_grow_block_tables_workspace_size(int32_t num_seqs, int32_t num_blocks, int64_t num_new_tokens);
 PKV_API pkv_status pkv_grow_block_tables(int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *starts,
                                          const int32_t *ends, int32_t num_seqs, int32_t block_size,
                                          int32_t *ref_counts, int32_t num_blocks, int32_t *cu_new,

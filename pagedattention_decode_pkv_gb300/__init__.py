@@ -86,7 +86,7 @@ _SIGS = {
     "pkv_paged_attention_decode_append_int8": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32,
                                                 _i32, _i32, _i32, _i32, _i32, _f32, ctypes.c_int, _vp, _sz, _vp, _vp],
                                                ctypes.c_int),
-    "pkv_grow_block_tables_workspace_size": ([_i32, _i32], _sz),
+    "pkv_grow_block_tables_workspace_size": ([_i32, _i32, _i64], _sz),
     "pkv_grow_block_tables": ([_vp, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _i64, _vp, _sz, _vp, _vp],
                               ctypes.c_int),
     "pkv_shrink_block_tables": ([_vp, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp], ctypes.c_int),
@@ -258,11 +258,12 @@ def pkv_grow_block_tables(block_tables, starts, ends, ref_counts, block_size: in
     _want(out, torch.int32, "out")
     if cu_new.numel() != B + 1 or out.numel() != num_new_tokens:
         raise ValueError("cu_new needs num_seqs + 1 entries and out num_new_tokens")
-    if workspace is None:
-        workspace = _empty(_lib.pkv_grow_block_tables_workspace_size(B, nb), torch.uint8, dev, stream)
+    ws = 0 if workspace is not None else _lib.pkv_grow_block_tables_workspace_size(B, nb, num_new_tokens)
+    if ws:
+        workspace = _empty(ws, torch.uint8, dev, stream)
     _call(dev, _lib.pkv_grow_block_tables, _addr(block_tables), max_blocks, _addr(starts), _addr(ends), B, block_size,
           _addr(ref_counts), nb, _addr(cu_new), _addr(out), num_new_tokens, _addr(workspace),
-          workspace.numel() * workspace.element_size(), _flag(err_flag), _raw_stream(dev, stream))
+          0 if workspace is None else workspace.numel() * workspace.element_size(), _flag(err_flag), _raw_stream(dev, stream))
     return cu_new, out
 
 

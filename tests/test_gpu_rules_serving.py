@@ -127,7 +127,7 @@ def test_buffers_belong_to_the_stream_given(pkv, cuda_dev, monkeypatch):
     monkeypatch.setattr(torch, "empty", spy)
     got = (pkv.pkv_paged_attention_prefill_mod(q, kc, vc, t, lens, cu, 0.1, 3, stream=side, **args),
            pkv.pkv_paged_attention_decode_mod(q[:2], kc, vc, t, lens, 0.1, 1600, stream=side, **args))
-    pkv.pkv_grow_block_tables(grown, zero, lens, ref_counts, bs, num_new_tokens=2400, stream=side)
+    pkv.pkv_grow_block_tables(grown, zero, lens, ref_counts, bs, num_new_tokens=20000, stream=side)
     monkeypatch.undo()
     side.synchronize()
     assert len(seen) == 7 and all(seen)

@@ -26,8 +26,9 @@ def _grow(lib, **kw):
     (dict(num_blocks=-1), "INVALID_ARG"), (dict(num_blocks=1 << 28), "INVALID_ARG"),
     (dict(num_new=-1), "INVALID_ARG"), (dict(num_seqs=65536), "UNSUPPORTED"), (dict(starts=None), "INVALID_ARG"),
     (dict(ends=None), "INVALID_ARG"), (dict(cu_new=None), "INVALID_ARG"), (dict(block_tables=None), "INVALID_ARG"),
-    (dict(ref_counts=None), "INVALID_ARG"), (dict(slots=None), "INVALID_ARG"), (dict(workspace=None), "WORKSPACE"),
-    (dict(ws_bytes=100), "WORKSPACE"), (dict(workspace=_p((1 << 20) + 16)), "WORKSPACE")])
+    (dict(ref_counts=None), "INVALID_ARG"), (dict(slots=None), "INVALID_ARG"),
+    (dict(num_blocks=40000, workspace=None), "WORKSPACE"), (dict(num_seqs=2000, ws_bytes=100), "WORKSPACE"),
+    (dict(num_new=1 << 20, workspace=_p((1 << 20) + 16)), "WORKSPACE")])
 def test_grow_refuses(pkv, bad, status):
     assert _grow(pkv._lib, **bad) == getattr(pkv, "PKV_ERR_" + status)
     assert b"grow" in pkv._lib.pkv_last_error_string()
@@ -35,8 +36,9 @@ def test_grow_refuses(pkv, bad, status):
 
 def test_grow_of_nothing(pkv):
     assert _grow(pkv._lib, num_seqs=0, workspace=None, ws_bytes=0) == pkv.PKV_OK
-    assert pkv._lib.pkv_grow_block_tables_workspace_size(0, 10) == 0
-    assert pkv._lib.pkv_grow_block_tables_workspace_size(3, 10) > 0
+    size = pkv._lib.pkv_grow_block_tables_workspace_size
+    assert size(0, 10, 5) == 0 and size(3, 10, 5) == 0  # nothing, and one launch without a workspace
+    assert min(size(2000, 10, 5), size(3, 40000, 5), size(3, 10, 1 << 20)) > 0
 
 
 @pytest.mark.parametrize("bad,status", [
