@@ -157,12 +157,11 @@ def _device_of(first, *others):
     index = first.get_device()
     if index < 0:
         raise ValueError("tensors must be CUDA tensors (no CPU path exists)")
-    for t in (first, *others):
-        if t is not None:
-            if t.get_device() != index:
-                raise ValueError("all tensors must be on one CUDA device")
-            if not t.is_contiguous():
-                raise ValueError("tensors must be contiguous")
+    if not first.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    for t in others:
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            raise ValueError("all tensors must be contiguous and on one CUDA device")
     return first.device
 
 
@@ -170,8 +169,12 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _addrs(*tensors):
+    return [None if t is None else t.data_ptr() for t in tensors]
+
+
 def _raw_stream(dev, stream):
-    # the raw handle alone: a Stream object costs a short call 4 of its 24 us
+    # the raw handle alone: a Stream object costs a short call 2 to 4 us
     return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 
@@ -234,11 +237,12 @@ def _table_args(block_tables, a, b, ref_counts, names):
     if not (block_tables.dtype is i32 and a.dtype is i32 and b.dtype is i32 and ref_counts.dtype is i32):
         for t, n in ((block_tables, "block_tables"), (a, names[0]), (b, names[1]), (ref_counts, "ref_counts")):
             _want(t, i32, n)
-    if block_tables.dim() != 2:
+    shape = block_tables.shape
+    if len(shape) != 2:
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
-    if a.numel() != block_tables.shape[0] or b.numel() != block_tables.shape[0]:
+    if a.numel() != shape[0] or b.numel() != shape[0]:
         raise ValueError(f"{names[0]} and {names[1]} need num_seqs entries")
-    return block_tables.shape
+    return shape
 
 
 def pkv_grow_block_tables(block_tables, starts, ends, ref_counts, block_size: int, *, num_new_tokens: int, cu_new=None,
@@ -254,15 +258,14 @@ def pkv_grow_block_tables(block_tables, starts, ends, ref_counts, block_size: in
         cu_new = _empty(B + 1, torch.int32, dev, stream) if B else torch.zeros(1, dtype=torch.int32, device=dev)
     if out is None:
         out = _empty(num_new_tokens, torch.int32, dev, stream)
-    _want(cu_new, torch.int32, "cu_new")
-    _want(out, torch.int32, "out")
+    _want_i32(cu_new=cu_new, out=out)
     if cu_new.numel() != B + 1 or out.numel() != num_new_tokens:
         raise ValueError("cu_new needs num_seqs + 1 entries and out num_new_tokens")
     ws = 0 if workspace is not None else _lib.pkv_grow_block_tables_workspace_size(B, nb, num_new_tokens)
     if ws:
         workspace = _empty(ws, torch.uint8, dev, stream)
-    _call(dev, _lib.pkv_grow_block_tables, _addr(block_tables), max_blocks, _addr(starts), _addr(ends), B, block_size,
-          _addr(ref_counts), nb, _addr(cu_new), _addr(out), num_new_tokens, _addr(workspace),
+    _call(dev, _lib.pkv_grow_block_tables, block_tables.data_ptr(), max_blocks, starts.data_ptr(), ends.data_ptr(), B,
+          block_size, ref_counts.data_ptr(), nb, cu_new.data_ptr(), out.data_ptr(), num_new_tokens, _addr(workspace),
           0 if workspace is None else workspace.numel() * workspace.element_size(), _flag(err_flag), _raw_stream(dev, stream))
     return cu_new, out
 
@@ -272,8 +275,8 @@ def pkv_shrink_block_tables(block_tables, keeps, lens, ref_counts, block_size: i
     past the kept blocks become -1 and their blocks' counts fall (in place)."""
     dev = _device_of(block_tables, keeps, lens, ref_counts, err_flag)
     B, max_blocks = _table_args(block_tables, keeps, lens, ref_counts, ("keeps", "lens"))
-    _call(dev, _lib.pkv_shrink_block_tables, _addr(block_tables), max_blocks, _addr(keeps), _addr(lens), B, block_size,
-          _addr(ref_counts), ref_counts.numel(), _flag(err_flag), _raw_stream(dev, stream))
+    _call(dev, _lib.pkv_shrink_block_tables, block_tables.data_ptr(), max_blocks, keeps.data_ptr(), lens.data_ptr(), B,
+          block_size, ref_counts.data_ptr(), ref_counts.numel(), _flag(err_flag), _raw_stream(dev, stream))
 
 
 def pkv_store_kvcache(key, value, k_cache, v_cache, slot_mapping, *, err_flag=None, stream=None):
@@ -477,14 +480,15 @@ _FORMAT = {torch.uint8: PKV_CACHE_E4M3, torch.int8: PKV_CACHE_INT8}
 
 
 def _cache_format(q, k_cache, v_cache, k_scale, v_scale):
-    """The caches' pkv_cache_format, with their scales checked."""
-    if q.dtype not in _DTYPE or k_cache.dtype != v_cache.dtype:
+    """(pkv_cache_format, q's shape, the caches' shape), with types, shapes and scales checked."""
+    dtype, code, q_shape, shape = q.dtype, k_cache.dtype, q.shape, k_cache.shape
+    if dtype not in _DTYPE or v_cache.dtype is not code:
         raise TypeError("q must be float32/float16/bfloat16 and both caches of one type")
-    if q.dim() != 3 or k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[3] != q.shape[2]:
+    if len(q_shape) != 3 or len(shape) != 4 or v_cache.shape != shape or shape[3] != q_shape[2]:
         raise ValueError("q [rows, Hq, d], caches [num_blocks, bs, Hkv, d]")
-    fmt = _FORMAT.get(k_cache.dtype, PKV_CACHE_DTYPE)
+    fmt = _FORMAT.get(code, PKV_CACHE_DTYPE)
     if fmt == PKV_CACHE_DTYPE:
-        if k_cache.dtype != q.dtype:
+        if code is not dtype:
             raise TypeError("caches must have the type of q, uint8 (E4M3 codes) or int8")
         if k_scale is not None or v_scale is not None:
             raise ValueError("scales belong to 8-bit caches")
@@ -493,18 +497,28 @@ def _cache_format(q, k_cache, v_cache, k_scale, v_scale):
             if t is None:
                 raise ValueError(f"{name} is required for an 8-bit cache")
             _want(t, torch.float32, name)
-            if t.shape != (k_cache.shape[0], k_cache.shape[2]):
+            if t.shape != (shape[0], shape[2]):
                 raise ValueError(f"{name} must be [num_blocks, num_kv_heads]")
-    return fmt
+    return fmt, q_shape, shape
+
+
+def _want_i32(**tensors):
+    for name, t in tensors.items():
+        if t.dtype is not torch.int32:
+            raise TypeError(f"{name} must be torch.int32")
 
 
 def _score_mod(softcap, alibi_slopes, key_starts, prefix_lens, Hq, rows, B):
-    for t, dtype, n, name in ((alibi_slopes, torch.float32, Hq, "alibi_slopes"),
-                              (key_starts, torch.int32, rows, "key_starts"),
-                              (prefix_lens, torch.int32, B, "prefix_lens")):
-        if t is not None and (t.dtype != dtype or t.numel() != n):
-            raise ValueError(f"{name}: {n} entries of {dtype}")
-    return _ScoreMod(softcap, _addr(alibi_slopes), _addr(key_starts), _addr(prefix_lens))
+    """A pkv_score_mod by reference, None for plain causal attention."""
+    if alibi_slopes is not None and (alibi_slopes.dtype is not torch.float32 or alibi_slopes.numel() != Hq):
+        raise ValueError(f"alibi_slopes: {Hq} entries of torch.float32")
+    if key_starts is not None and (key_starts.dtype is not torch.int32 or key_starts.numel() != rows):
+        raise ValueError(f"key_starts: {rows} entries of torch.int32")
+    if prefix_lens is not None and (prefix_lens.dtype is not torch.int32 or prefix_lens.numel() != B):
+        raise ValueError(f"prefix_lens: {B} entries of torch.int32")
+    if softcap == 0 and alibi_slopes is None and key_starts is None and prefix_lens is None:
+        return None
+    return ctypes.byref(_ScoreMod(softcap, *_addrs(alibi_slopes, key_starts, prefix_lens)))
 
 
 def pkv_paged_attention_decode_mod(q, k_cache, v_cache, block_tables, context_lens, scale: float,
@@ -517,12 +531,10 @@ def pkv_paged_attention_decode_mod(q, k_cache, v_cache, block_tables, context_le
     key_starts[b] on.  With key / value the step's new row is appended first."""
     dev = _device_of(q, key, value, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, alibi_slopes, key_starts,
                out, workspace, err_flag)
-    fmt = _cache_format(q, k_cache, v_cache, k_scale, v_scale)
-    _want(block_tables, torch.int32, "block_tables")
-    _want(context_lens, torch.int32, "context_lens")
-    B, Hq, d = q.shape
-    nb, bs, Hkv, _ = k_cache.shape
-    if context_lens.numel() != B or block_tables.dim() != 2 or block_tables.shape[0] != B:
+    fmt, (B, Hq, d), (nb, bs, Hkv, _) = _cache_format(q, k_cache, v_cache, k_scale, v_scale)
+    _want_i32(block_tables=block_tables, context_lens=context_lens)
+    tables = block_tables.shape
+    if context_lens.numel() != B or len(tables) != 2 or tables[0] != B:
         raise ValueError("inconsistent shapes")
     if (key is None) != (value is None):
         raise ValueError("key and value go together")
@@ -530,16 +542,17 @@ def pkv_paged_attention_decode_mod(q, k_cache, v_cache, block_tables, context_le
         raise ValueError("key, value: [num_seqs, num_kv_heads, head_dim] of the q dtype")
     mod = _score_mod(softcap, alibi_slopes, key_starts, None, Hq, B, B)
     if out is None:
-        out = _empty(q.shape, q.dtype, dev, stream)
+        out = _empty((B, Hq, d), q.dtype, dev, stream)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have the shape and type of q")
-    ws = pkv_paged_attention_decode_workspace_size(B, Hq, Hkv, d, bs, max_context_len, q.dtype) if B else 0
+    dtype = _DTYPE[q.dtype]
+    ws = _lib.pkv_paged_attention_decode_workspace_size(B, Hq, Hkv, d, bs, max_context_len, dtype) if B else 0
     if ws and workspace is None:
         workspace = _empty(ws, torch.uint8, dev, stream)
-    _call(dev, _lib.pkv_paged_attention_decode_mod, _addr(out), _addr(q), _addr(key), _addr(value), _addr(k_cache),
-          _addr(v_cache), _addr(k_scale), _addr(v_scale), fmt, _addr(block_tables), block_tables.shape[1],
-          _addr(context_lens), B, Hq, Hkv, d, bs, nb, max_context_len, scale, ctypes.byref(mod), _DTYPE[q.dtype],
-          _addr(workspace) if ws else None, workspace.numel() * workspace.element_size() if ws else 0,
+    _call(dev, _lib.pkv_paged_attention_decode_mod,
+          *_addrs(out, q, key, value, k_cache, v_cache, k_scale, v_scale), fmt, block_tables.data_ptr(), tables[1],
+          context_lens.data_ptr(), B, Hq, Hkv, d, bs, nb, max_context_len, scale, mod, dtype,
+          workspace.data_ptr() if ws else None, workspace.numel() * workspace.element_size() if ws else 0,
           _flag(err_flag), _raw_stream(dev, stream))
     return out
 
@@ -559,26 +572,22 @@ def pkv_paged_attention_prefill_mod(q, k_cache, v_cache, block_tables, starts, c
     those below prefix_lens[b]."""
     dev = _device_of(q, k_cache, v_cache, k_scale, v_scale, block_tables, starts, cu_q, alibi_slopes, key_starts,
                prefix_lens, out, workspace, err_flag)
-    fmt = _cache_format(q, k_cache, v_cache, k_scale, v_scale)
-    _want(block_tables, torch.int32, "block_tables")
-    _want(starts, torch.int32, "starts")
-    _want(cu_q, torch.int32, "cu_q")
-    rows, Hq, d = q.shape
-    nb, bs, Hkv, _ = k_cache.shape
-    B = starts.numel()
-    if cu_q.numel() != B + 1 or block_tables.dim() != 2 or block_tables.shape[0] != B:
+    fmt, (rows, Hq, d), (nb, bs, Hkv, _) = _cache_format(q, k_cache, v_cache, k_scale, v_scale)
+    _want_i32(block_tables=block_tables, starts=starts, cu_q=cu_q)
+    B, tables = starts.numel(), block_tables.shape
+    if cu_q.numel() != B + 1 or len(tables) != 2 or tables[0] != B:
         raise ValueError("inconsistent shapes")
     mod = _score_mod(softcap, alibi_slopes, key_starts, prefix_lens, Hq, rows, B)
     if out is None:
-        out = _empty(q.shape, q.dtype, dev, stream)
+        out = _empty((rows, Hq, d), q.dtype, dev, stream)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have the shape and type of q")
-    ws = _lib.pkv_paged_attention_prefill_mod_workspace_size(B, Hq, Hkv, d, bs, max_q_len, block_tables.shape[1])
+    ws = _lib.pkv_paged_attention_prefill_mod_workspace_size(B, Hq, Hkv, d, bs, max_q_len, tables[1])
     if ws and workspace is None:
         workspace = _empty(ws, torch.uint8, dev, stream)
-    _call(dev, _lib.pkv_paged_attention_prefill_mod, _addr(out), _addr(q), _addr(k_cache), _addr(v_cache),
-          _addr(k_scale), _addr(v_scale), fmt, _addr(block_tables), block_tables.shape[1], _addr(starts), _addr(cu_q), B,
-          max_q_len, Hq, Hkv, d, bs, nb, scale, ctypes.byref(mod), _DTYPE[q.dtype], _addr(workspace) if ws else None,
+    _call(dev, _lib.pkv_paged_attention_prefill_mod, *_addrs(out, q, k_cache, v_cache, k_scale, v_scale), fmt,
+          block_tables.data_ptr(), tables[1], starts.data_ptr(), cu_q.data_ptr(), B, max_q_len, Hq, Hkv, d, bs, nb, scale,
+          mod, _DTYPE[q.dtype], workspace.data_ptr() if ws else None,
           workspace.numel() * workspace.element_size() if ws else 0, _flag(err_flag), _raw_stream(dev, stream))
     return out
 
