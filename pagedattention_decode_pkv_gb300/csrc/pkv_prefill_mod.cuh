@@ -98,6 +98,7 @@ enum { kNoCap = 0, kCap = 1, kCapBounded = 2 };
 constexpr float kFreeCap = 73.f;
 constexpr float kTanhLimit = 0.7f;    // |score / cap| up to which the polynomial stands for tanh
 constexpr double kTanhFit[5] = {0.9999996973, -0.3333021287, 0.1328111218, -0.05083622068, 0.0137736928};
+constexpr int kMaxGridPairs = 32768;  // grid.y
 constexpr int kMinSplitBlocks = 2;    // blocks of a split at least
 
 // Scores of a block of keys as every consumer needs them.
@@ -149,6 +150,7 @@ struct ModArgs {
     const float *slopes;
     const int32_t *key_starts, *prefix_lens;
     int32_t max_blocks, Hq, Hkv, lg_g, bs, num_blocks, box_lg, max_q_len, pairs, nsplit;
+    int32_t pair_grids;  // grids of kMaxGridPairs items that hold pairs * nsplit
     float sl;     // scale log2 e: raw score -> log2 units
     float sa;     // softcap: raw score -> scale / c
     float su;     // softcap: raw score -> 2 log2 e scale / c
@@ -184,8 +186,13 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     constexpr bool kFree = CAP == kCapBounded;
     static_assert(!kFree || (kBf16 && !ALIBI), "P = 2^s needs bf16's range and bounded scores");
     constexpr int kRing = L::kRing;
-    const int b = blockIdx.z, kh = blockIdx.y;
-    const int pair = A.nsplit == 1 ? blockIdx.x : blockIdx.x / A.nsplit, split = blockIdx.x - pair * A.nsplit;
+    // CTAs start in grid order: every KV head's last pair of a sequence first, the shortest pairs
+    // last, so that the launch's end is short (heads slower than pairs: 8 prompts
+    // of 4k, cap 50, 1049 us against 1037, packed documents 155 against 150)
+    const int kh = blockIdx.x, b = A.pair_grids == 1 ? blockIdx.z : blockIdx.z / A.pair_grids;
+    const int item = (blockIdx.z - b * A.pair_grids) * kMaxGridPairs + blockIdx.y;
+    if (item >= A.pairs * A.nsplit) return;
+    const int pair = A.nsplit == 1 ? item : item / A.nsplit, split = item - pair * A.nsplit;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int lg_g = A.lg_g, G = 1 << lg_g, Hq = A.Hq, bs = A.bs;
     extern __shared__ uint8_t smem_raw[];
@@ -1068,8 +1075,12 @@ pkv_status prefill_mod_launch(const PrefillCall &c) {
     a.ml_part = reinterpret_cast<float2 *>(c.workspace + c.plan.o_bytes);
     a.split_used = reinterpret_cast<int32_t *>(c.workspace + c.plan.o_bytes + c.plan.ml_bytes);
     a.err_flag = c.err_flag;
+    const int items = a.pairs * a.nsplit;
+    a.pair_grids = (items + kMaxGridPairs - 1) / kMaxGridPairs;
+    if (static_cast<int64_t>(c.num_seqs) * a.pair_grids > 65535)
+        return set_error(PKV_ERR_UNSUPPORTED, "prefill: max_q_len is too long for so many sequences");
     cudaError_t e = launch_pdl(kPdlDecode, prefill_mod_kernel<T, FMT, CAP, ALIBI>,
-                               dim3(a.pairs * a.nsplit, c.Hkv, c.num_seqs), dim3(kModThreads<FMT != kCode16>),
+                               dim3(c.Hkv, items < kMaxGridPairs ? items : kMaxGridPairs, c.num_seqs * a.pair_grids), dim3(kModThreads<FMT != kCode16>),
                                ModLayout<FMT != kCode16>::kAlloc, c.stream, mk, mv, a);
     if (e == cudaSuccess && a.nsplit > 1) {
         const int64_t rows = static_cast<int64_t>(c.num_seqs) * c.max_q_len * c.Hq;
