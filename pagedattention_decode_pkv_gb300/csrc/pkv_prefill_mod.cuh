@@ -758,29 +758,27 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             if constexpr (ALIBI) {
                 // bias nslope |k - c|, c the row's own key in the half's coordinates
                 const float c = static_cast<float>(pos - h * kHalfKeys);
-                // on one side of every row's own key the bias is linear
+                // On one side of every row's own key the bias is linear: by (c - k).  The seldom
+                // half with keys on both sides is corrected afterwards: |c - k| in a branch of its own
+                // lengthened the loop (8 prompts of 4k 1330 us against 1235).
                 const bool past = __all_sync(0xffffffffu, pos - h * kHalfKeys >= kHalfKeys - 1);
                 const bool ahead = __all_sync(0xffffffffu, pos - h * kHalfKeys <= 0);
                 const float by = ahead ? -nslope : nslope;
+                const uint64_t on = splat2(-2.f * by);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const uint64_t sl = splat2(CAP ? 1.f : C8 ? A.sl * f->ks[g0 + g] * rq : A.sl);
-                    if (past || ahead) {  // by (c - k), two keys on by one addition
-                        uint64_t bias = pack2(by * (c - 16 * g), by * (c - 16 * g - 1));
-                        const uint64_t on = splat2(-2.f * by);
+                    uint64_t bias = pack2(by * (c - 16 * g), by * (c - 16 * g - 1));  // two keys on by one addition
 #pragma unroll
-                        for (int k = 16 * g; k < 16 * g + 16; k += 2) {
-                            const uint64_t s = pack2(x[k], x[k + 1]);
-                            unpack2(CAP ? add2(s, bias) : fma2(s, sl, bias), x[k], x[k + 1]);
-                            bias = add2(bias, on);
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 16 * g; k < 16 * g + 16; ++k) {
-                            const float bias = nslope * fabsf(static_cast<float>(k) - c);
-                            x[k] = CAP ? x[k] + bias : fmaf(x[k], C8 ? A.sl * f->ks[g0 + g] * rq : A.sl, bias);
-                        }
+                    for (int k = 16 * g; k < 16 * g + 16; k += 2) {
+                        const uint64_t s = pack2(x[k], x[k + 1]);
+                        unpack2(CAP ? add2(s, bias) : fma2(s, sl, bias), x[k], x[k + 1]);
+                        bias = add2(bias, on);
                     }
+                }
+                if (!past && !ahead) {  // keys behind the row's own: from nslope (c - k) to nslope (k - c)
+#pragma unroll
+                    for (int k = 0; k < kHalfKeys; ++k) x[k] = fmaf(fmaxf(k - c, 0.f), 2.f * nslope, x[k]);
                 }
             }
             // 2. masked keys
