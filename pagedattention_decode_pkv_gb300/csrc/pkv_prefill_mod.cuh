@@ -39,16 +39,16 @@
 // QK_{h+2} follows PV_h into the buffer that P_h leaves, so that S_{h+1} is there when
 // the softmax of h ends and its warps never wait for the tensor core's round trip.
 //
-// What bounds it.  Plain scores, 8 prompts of 4k (32 heads, 8 KV heads): 923 us, 1075
+// What bounds it.  Plain scores, 8 prompts of 4k (32 heads, 8 KV heads): 907 us, 1095
 // TFLOP/s.  A step of 64 keys of both tiles is 1240 clk of products alone: Q K^T at 64
 // keys reads its operands from shared memory at 386 clk where the arithmetic takes 256
 // (128 keys at once, one S buffer a tile, read less and ran 976 us: both tiles then sit
 // in their softmax together).  With the copies into the ring the step is 1534, with the
-// softmax warps beside it 1834.  Cap 50: 1046 us; the polynomial's operations come on
-// top.  E4M3 and int8: 1300 and 1334; widening writes every tile once more.  Short
+// softmax warps beside it 1834.  Cap 50: 1038 us; the polynomial's operations come on
+// top.  With a bias 1235.  E4M3 and int8: 1267 and 1305; widening writes every tile once more.  Short
 // spans: of a CTA's ~13k clk of setup, first products and output nothing overlaps, for
-// both tiles do them together (2 x 8k rows of packed documents of 60 to 2500 rows: 155
-// us, 645 TFLOP/s).
+// both tiles do them together (2 x 8k rows of packed documents of 60 to 2500 rows: 150
+// us, 664 TFLOP/s).
 //
 // Few rows over a long context (a small chunk, few sequences) leave most SMs idle,
 // so the blocks of a tile pair are cut into up to nsplit runs, one CTA each, whose
@@ -93,7 +93,7 @@ constexpr float kModRescale = 8.f;    // log2 units a block may exceed the refer
 // maximum is needed: P = 2^s itself, |s| <= kFreeCap, is in bf16's range with all its
 // bits, and its sums times V are in f32's as long as keys x max |V| < 2^54. Without the
 // maximum and the rescaling 8 prompts of 4096 rows (32 heads, 8 KV heads, cap 50) take
-// 1051 us; f16 ones, with both, 1203.
+// 1038 us; f16 ones, with both, 1186.
 enum { kNoCap = 0, kCap = 1, kCapBounded = 2 };
 constexpr float kFreeCap = 73.f;
 constexpr float kTanhLimit = 0.7f;    // |score / cap| up to which the polynomial stands for tanh
