@@ -45,10 +45,10 @@
 // (128 keys at once, one S buffer a tile, read less and ran 976 us: both tiles then sit
 // in their softmax together).  With the copies into the ring the step is 1534, with the
 // softmax warps beside it 1834.  Cap 50: 1038 us; the polynomial's operations come on
-// top.  With a bias 1235.  E4M3 and int8: 1267 and 1305; widening writes every tile once more.  Short
-// spans: of a CTA's ~13k clk of setup, first products and output nothing overlaps, for
-// both tiles do them together (2 x 8k rows of packed documents of 60 to 2500 rows: 150
-// us, 664 TFLOP/s).
+// top.  With a bias 1235.  E4M3 and int8: 1267 and 1305; widening writes every tile once
+// more.  Short spans: of a CTA's ~13k clk of setup, first products and output nothing
+// overlaps, for both tiles do them together (2 x 8k rows of packed documents of 60 to
+// 2500 rows: 150 us, 664 TFLOP/s).
 //
 // Few rows over a long context (a small chunk, few sequences) leave most SMs idle,
 // so the blocks of a tile pair are cut into up to nsplit runs, one CTA each, whose
