@@ -68,8 +68,8 @@ typedef enum pkv_cache_format { PKV_CACHE_DTYPE = 0, PKV_CACHE_E4M3 = 1, PKV_CAC
 /*
  * Score rules of the _mod attention calls.  For the query at position p and key t,
  * with s = scale * q . K_t, in this order:
- *   softcap > 0      s = softcap * tanh(s / softcap); 0: none.  0, or finite and
- *                    at least 1e-30.
+ *   softcap > 0      s = softcap * tanh(s / softcap); 0: none.  0, or from 1e-30 to
+ *                    1e30.
  *   alibi_slopes     device float32 [num_q_heads] or NULL: s -= slope_h * |p - t|
  *   key_starts       device int32, one per query (prefill: in the order of q's rows;
  *                    decode: one per sequence) or NULL: keys t < key_starts are not

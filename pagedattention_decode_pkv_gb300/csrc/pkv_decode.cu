@@ -778,8 +778,8 @@ extern "C" pkv_status pkv_paged_attention_decode_mod(
         return set_error(PKV_ERR_UNSUPPORTED, "decode: q/out over 8-bit caches must be fp16 or bf16");
     DecodeMod m;
     if (mod) {
-        if (!(mod->softcap >= 0.f) || std::isinf(mod->softcap) || (mod->softcap > 0.f && mod->softcap < 1e-30f))
-            return set_error(PKV_ERR_INVALID_ARG, "decode: softcap must be 0, or finite and at least 1e-30");
+        if (!(mod->softcap >= 0.f) || mod->softcap > 1e30f || (mod->softcap > 0.f && mod->softcap < 1e-30f))
+            return set_error(PKV_ERR_INVALID_ARG, "decode: softcap must be 0, or from 1e-30 to 1e30");
         m.softcap = mod->softcap;
         m.slopes = mod->alibi_slopes;
         m.key_starts = mod->key_starts;

@@ -1060,10 +1060,16 @@ decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         float y[4] = {sc[0] * sl, sc[1] * sl, sc[2] * sl, sc[3] * sl};  // log2 units
         if constexpr (MOD) {
             if (mod.softcap > 0.f) {
-                // c tanh(s / c) = c - 2 c / (1 + e^(2 s / c)): off by a few 2^-23 c
-                const float cap = mod.softcap * kLog2e, u = 2.f / mod.softcap;
+                // c tanh(s / c) = s P((s / c)^2) where |s / c| is small (relative 3e-7), else
+                // c - 2 c / (1 + e^(2 s / c)), off by a few 2^-23 c: of a small s nothing would be left
+                const float cap = mod.softcap * kLog2e, inv = 1.f / cap, u2 = 2.f / mod.softcap;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = fmaf(fast_rcp(1.f + fast_exp2(y[e] * u)), -2.f * cap, cap);
+                for (int e = 0; e < 4; ++e) {
+                    const float u = y[e] * inv, z = u * u;
+                    constexpr float f0 = kTanhFit[0], f1 = kTanhFit[1], f2 = kTanhFit[2], f3 = kTanhFit[3], f4 = kTanhFit[4];
+                    const float p = fmaf(fmaf(fmaf(fmaf(f4, z, f3), z, f2), z, f1), z, f0);
+                    y[e] = fabsf(u) > kTanhLimit ? fmaf(fast_rcp(1.f + fast_exp2(y[e] * u2)), -2.f * cap, cap) : y[e] * p;
+                }
             }
             const float d0 = static_cast<float>(dist[slot] - g), d8 = static_cast<float>(dist[slot] - g - 8);
             y[0] = fmaf(-slope0, d0, y[0]);

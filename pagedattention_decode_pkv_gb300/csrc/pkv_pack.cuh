@@ -26,6 +26,10 @@ template <> __device__ __forceinline__ void pair_acc<__half>(uint32_t w, float &
         : "r"(w));
 }
 
+// tanh(u) = u (f0 + f1 u^2 + .. + f4 u^8) for |u| <= kTanhLimit: the minimax fit in relative error, 3e-7
+constexpr float kTanhLimit = 0.7f;
+constexpr double kTanhFit[5] = {0.9999996973, -0.3333021287, 0.1328111218, -0.05083622068, 0.0137736928};
+
 // max(a, b, c) in one instruction (three-input max; NaN operands are ignored
 // as by fmaxf).
 __device__ __forceinline__ float max3f(float a, float b, float c) {

@@ -78,8 +78,8 @@ extern "C" pkv_status pkv_paged_attention_prefill_mod(
         return set_error(PKV_ERR_INVALID_ARG, "prefill: num_blocks * block_size >= 2^31");
     const pkv_score_mod none{};
     const pkv_score_mod m = mod ? *mod : none;
-    if (!(m.softcap >= 0.f) || std::isinf(m.softcap) || (m.softcap > 0.f && m.softcap < 1e-30f))
-        return set_error(PKV_ERR_INVALID_ARG, "prefill: softcap must be 0, or finite and at least 1e-30");
+    if (!(m.softcap >= 0.f) || m.softcap > 1e30f || (m.softcap > 0.f && m.softcap < 1e-30f))
+        return set_error(PKV_ERR_INVALID_ARG, "prefill: softcap must be 0, or from 1e-30 to 1e30");
     if (num_seqs > 65535 || num_kv_heads > 65535)
         return set_error(PKV_ERR_UNSUPPORTED, "prefill: more than 65535 sequences or KV heads");
     if (num_seqs == 0 || max_q_len == 0) return ok();

@@ -11,11 +11,11 @@
 // hold a boundary; blocks that no row of the CTA sees are never loaded.  Then the
 // softmax and the sum over V_t; a row that sees nothing is zero.
 //
-// tanh(u), |u| <= 0.7 in every score of a warp's 64-key step (35 of a cap of 50), is
-// u times a polynomial of degree 4 in u^2, the minimax fit in relative error (linear
-// programming on a Chebyshev grid): 3e-7, at seven packed FMA-unit operations a pair
-// of scores.  Larger scores take c tanh(u) = c - 2 c / (1 + e^{2u}), one exponential and
-// one reciprocal, off by a few 2^-23 c: two more trips through the special-function
+// tanh(u), |u| <= 0.7 (35 of a cap of 50), is u times a polynomial of degree 4 in u^2,
+// the minimax fit in relative error (linear programming on a Chebyshev grid): 3e-7, at
+// seven packed FMA-unit operations a pair of scores.  Larger scores take c tanh(u) =
+// c - 2 c / (1 + e^{2u}), one exponential and one reciprocal, off by a few 2^-23 c, in
+// the 64-key steps of a warp that have one: two more trips through the special-function
 // unit, which the softmax needs as well (8 prompts of 4k, cap 50: 1432 us with that
 // alone, 1279 with the polynomial, at that step of the kernel).  Both errors are far
 // below the rounding of P; the one-instruction tanh (relative 2^-11) is not.  A capped
@@ -96,8 +96,6 @@ constexpr float kModRescale = 8.f;    // log2 units a block may exceed the refer
 // 1038 us; f16 ones, with both, 1186.
 enum { kNoCap = 0, kCap = 1, kCapBounded = 2 };
 constexpr float kFreeCap = 73.f;
-constexpr float kTanhLimit = 0.7f;    // |score / cap| up to which the polynomial stands for tanh
-constexpr double kTanhFit[5] = {0.9999996973, -0.3333021287, 0.1328111218, -0.05083622068, 0.0137736928};
 constexpr int kMaxGridPairs = 32768;  // grid.y
 constexpr int kMinSplitBlocks = 2;    // blocks of a split at least
 
@@ -733,24 +731,18 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         unpack2(mul2(u, fma2(u2, fma2(u2, fma2(u2, fma2(u2, c[4], c[3]), c[2]), c[1]), c[0])), x[k], x[k + 1]);
                     }
                 }
-                if (!__all_sync(0xffffffffu, top <= kTanhLimit * kTanhLimit)) {  // S is still there: once more
+                if (!__all_sync(0xffffffffu, top <= kTanhLimit * kTanhLimit)) {  // S is still there: once more for the large ones
 #pragma unroll
                     for (int c0 = 0; c0 < kHalfKeys; c0 += 32) {
                         uint32_t v[32];
                         tmem_ld32(scol + c0, v);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[c0 + i] = __uint_as_float(v[i]);
-                    }
-                    const uint64_t one = splat2(1.f), c2 = splat2(A.capl2), m2c = splat2(-2.f * A.capl2);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const uint64_t su = splat2(C8 ? A.su * f->ks[g0 + g] * rq : A.su);
-#pragma unroll
-                        for (int k = 16 * g; k < 16 * g + 16; k += 2) {
-                            float e0, e1;
-                            unpack2(mul2(pack2(x[k], x[k + 1]), su), e0, e1);
-                            unpack2(add2(pack2(fast_exp2(e0), fast_exp2(e1)), one), e0, e1);
-                            unpack2(fma2(pack2(fast_rcp(e0), fast_rcp(e1)), m2c, c2), x[k], x[k + 1]);
+                        for (int i = 0; i < 32; ++i) {
+                            const float su = C8 ? A.su * f->ks[g0 + (c0 + i) / 16] * rq : A.su;
+                            const float e = __uint_as_float(v[i]) * su;  // 2 log2 e score / cap
+                            const float big = fmaf(fast_rcp(1.f + fast_exp2(e)), -2.f * A.capl2, A.capl2);
+                            // (under a small cap those bits are there for small scores too)
+                            x[c0 + i] = kFree || fabsf(e) > kTanhLimit * 2.8853900817779268f ? big : x[c0 + i];
                         }
                     }
                 }

@@ -89,6 +89,13 @@ def test_other_shapes(pkv, cuda_dev, dtype, Hq, Hkv, d, bs, rule):
     _check(pkv, _batch(dtype, Hq, Hkv, d, bs, CTX, d + bs, cuda_dev), CTX, _rules(rule, CTX, Hq, cuda_dev))
 
 
+@pytest.mark.parametrize("softcap", [1e-30, 0.01, 300.0, 1e30])
+@pytest.mark.parametrize("dtype,d,bs", [(torch.bfloat16, 128, 16), (torch.float16, 128, 16), (torch.float32, 64, 4)])
+def test_caps_of_any_size(pkv, cuda_dev, softcap, dtype, d, bs):
+    ctx = [1, 100, 700]
+    _check(pkv, _batch(dtype, 8, 8, d, bs, ctx, 12, cuda_dev), ctx, {"softcap": softcap})
+
+
 @pytest.mark.parametrize("ctx", [[4096] * 8, [3000, 9, 8192, 1], [16384]])
 @pytest.mark.parametrize("rule", ["plain", "cap", "window", "all"])
 def test_long_contexts(pkv, cuda_dev, ctx, rule):

@@ -124,7 +124,7 @@ def test_split_keys(pkv, cuda_dev, rule, fmt, spans):
            _codes(pkv, fmt, batch, 8, cuda_dev) if fmt else None, max_q=max(ns) + 300)
 
 
-@pytest.mark.parametrize("softcap", [0.01, 3.0, 50.5, 51.0, 300.0])
+@pytest.mark.parametrize("softcap", [1e-30, 0.01, 3.0, 50.5, 51.0, 300.0, 1e30])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("q_gain", [0.1, 30.0])
 def test_caps_of_any_size(pkv, cuda_dev, softcap, dtype, q_gain):
@@ -134,6 +134,23 @@ def test_caps_of_any_size(pkv, cuda_dev, softcap, dtype, q_gain):
     batch, q, starts, cu, ns = _case(dtype, 8, 8, 16, spans, 11, cuda_dev, q_gain)
     q[::7] = -q_gain * batch.k_cache[batch.block_tables[0, 0].item(), 0].to(dtype)  # against key 0
     _check(pkv, batch, q, starts, cu, ns, spans, {"softcap": softcap}, batch.scale)
+
+
+@pytest.mark.parametrize("fmt", [None, "fp8"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_small_scores_beside_large_ones(pkv, cuda_dev, dtype, fmt):
+    """Rows whose scores pass a large cap do not cost the rows beside them their precision."""
+    spans = [(200, 120)]
+    batch, q, starts, cu, ns = _case(dtype, 8, 8, 16, spans, 31, cuda_dev)
+    q[::2] *= 3e3  # scores of 6000 in standard deviation
+    rules = {"softcap": 2e4}
+    caches = _codes(pkv, fmt, batch, 3, cuda_dev) if fmt else None
+    (kc, ks), (vc, vs) = caches or ((batch.k_cache, None), (batch.v_cache, None))
+    out = pkv.pkv_paged_attention_prefill_mod(q, kc, vc, batch.block_tables, starts, cu, batch.scale, 120, k_scale=ks,
+                                              v_scale=vs, **rules)
+    ref = sr.prefill(q, sr.dequantize(kc, ks), sr.dequantize(vc, vs), batch.block_tables, [200], ns, batch.scale, 2e4)
+    assert torch.isfinite(out).all()
+    sr.assert_within(out[1::2], tuple(x[1::2] for x in ref), vc, vs)
 
 
 def test_plain_rule_equals_the_plain_call(pkv, cuda_dev):

@@ -82,7 +82,8 @@ def _prefill(pkv, lib, **kw):
     (dict(max_q=-1), "INVALID_ARG"), (dict(Hq=0), "INVALID_ARG"), (dict(Hq=12), "INVALID_ARG"),
     (dict(bs=0), "INVALID_ARG"), (dict(nb=1 << 28), "INVALID_ARG"), (dict(nb=0), "INVALID_ARG"),
     (dict(mod=(-1.0,)), "INVALID_ARG"), (dict(mod=(float("nan"),)), "INVALID_ARG"),
-    (dict(mod=(float("inf"),)), "INVALID_ARG"), (dict(mod=(1e-33,)), "INVALID_ARG"), (dict(num_seqs=65536), "UNSUPPORTED"), (dict(d=64), "UNSUPPORTED"),
+    (dict(mod=(float("inf"),)), "INVALID_ARG"), (dict(mod=(1e-33,)), "INVALID_ARG"), (dict(mod=(1e31,)), "INVALID_ARG"),
+    (dict(num_seqs=65536), "UNSUPPORTED"), (dict(d=64), "UNSUPPORTED"),
     (dict(Hq=24), "UNSUPPORTED"), (dict(Hq=128), "UNSUPPORTED"), (dict(bs=24), "UNSUPPORTED"), (dict(dtype=0), "UNSUPPORTED"),
     (dict(out=None), "INVALID_ARG"), (dict(q=None), "INVALID_ARG"), (dict(k=None), "INVALID_ARG"),
     (dict(v=None), "INVALID_ARG"), (dict(tables=None), "INVALID_ARG"), (dict(starts=None), "INVALID_ARG"),
@@ -123,7 +124,8 @@ def _decode(pkv, lib, **kw):
     (dict(dtype=7), "INVALID_ARG"), (dict(fmt=-1), "INVALID_ARG"), (dict(num_seqs=-1), "INVALID_ARG"),
     (dict(Hq=12), "INVALID_ARG"), (dict(max_ctx=-1), "INVALID_ARG"), (dict(nb=1 << 28), "INVALID_ARG"),
     (dict(mod=(-0.5,)), "INVALID_ARG"), (dict(mod=(float("nan"),)), "INVALID_ARG"),
-    (dict(mod=(float("inf"),)), "INVALID_ARG"), (dict(mod=(1e-33,)), "INVALID_ARG"), (dict(key=_p()), "INVALID_ARG"), (dict(value=_p()), "INVALID_ARG"),
+    (dict(mod=(float("inf"),)), "INVALID_ARG"), (dict(mod=(1e-33,)), "INVALID_ARG"), (dict(mod=(1e31,)), "INVALID_ARG"),
+    (dict(key=_p()), "INVALID_ARG"), (dict(value=_p()), "INVALID_ARG"),
     (dict(out=None), "INVALID_ARG"), (dict(ctx=None), "INVALID_ARG"), (dict(fmt=1), "INVALID_ARG"),
     (dict(fmt=1, ks=_p(), vs=_p(), dtype=0), "UNSUPPORTED"), (dict(fmt=2, ks=_p(), vs=_p(), d=64), "UNSUPPORTED"),
     (dict(num_seqs=65536), "UNSUPPORTED"), (dict(d=2048), "UNSUPPORTED"), (dict(ws=None), "WORKSPACE"),
