@@ -234,10 +234,12 @@ table_assign_kernel(int32_t *__restrict__ block_tables, int32_t max_blocks, cons
             e_len[mine] = static_cast<int32_t>(min(static_cast<int64_t>(bs), g.end - j * bs));
         }
         __syncthreads();
-        const int32_t taken = static_cast<int32_t>(min(found, granted - base));
-        // taken * bs <= num_blocks * bs < 2^31
-        for (int32_t x = threadIdx.x; x < taken * bs; x += kTabThreads) {
-            const int32_t e = x / bs, o = x - e * bs;
+        // Positions of a block as far as the slot map can hold any.  taken * span <= num_blocks * bs
+        // < 2^31, and one step past it is in 32 unsigned bits.
+        const uint32_t taken = static_cast<uint32_t>(min(found, granted - base));
+        const uint32_t span = static_cast<uint32_t>(min(static_cast<int64_t>(bs), num_slots_out));
+        for (uint32_t x = threadIdx.x; x < taken * span; x += kTabThreads) {
+            const int32_t e = x / span, o = x - e * span;
             const int64_t k = e_out[e] + o;
             if (o < e_len[e] && k < num_slots_out) slots[k] = e_id[e] * bs + o;
         }
@@ -343,8 +345,9 @@ table_grow_one_kernel(int32_t *__restrict__ block_tables, int32_t max_blocks, co
             bits |= PKV_ERRBIT_NO_BLOCKS;
         }
         const int64_t stop = min(upto, g.start + max(num_slots_out - out0, static_cast<int64_t>(0)));
-        int o = static_cast<int>(g.start - (g.held - 1) * bs);  // in that block, where it is partly filled
-        for (int64_t p = g.start; p < stop; ++p, ++o) slots[out0 + p - g.start] = id < 0 ? -1 : id * bs + o;
+        // the start's slot, where id is a block
+        uint32_t at = static_cast<uint32_t>(id * static_cast<int64_t>(bs) + g.start - (g.held - 1) * bs);
+        for (int64_t p = g.start; p < stop; ++p, ++at) slots[out0 + p - g.start] = id < 0 ? -1 : static_cast<int32_t>(at);
         if (bits && err_flag) atomicOr(err_flag, bits);
     }
     for (int64_t k = tokens + b; k < num_slots_out; k += kOneThreads) slots[k] = -1;  // padding
@@ -354,7 +357,7 @@ table_grow_one_kernel(int32_t *__restrict__ block_tables, int32_t max_blocks, co
         for (; free_bits && rank < min(r0 + kOneThreads, granted); ++rank, free_bits &= free_bits - 1)
             e_id[rank - r0] = 32 * b + __ffs(free_bits) - 1;
         __syncthreads();
-        const int32_t taken = min(kOneThreads, granted - r0);
+        const int32_t taken = min(kOneThreads, granted - r0), span = min(bs, num_slots_out);
         if (b < taken) {
             const int32_t r = r0 + b, id = e_id[b], to = last_at_most(s_prefix, B, r);
             const Growth h = growth_of(s_start[to], s_end[to], bs, max_blocks);
@@ -366,8 +369,8 @@ table_grow_one_kernel(int32_t *__restrict__ block_tables, int32_t max_blocks, co
             e_len[b] = static_cast<int32_t>(min(static_cast<int64_t>(bs), h.end - j * bs));
         }
         __syncthreads();
-        for (int32_t x = b; x < taken * bs; x += kOneThreads) {  // taken * bs <= num_blocks * bs < 2^31
-            const int32_t e = x / bs, o = x - e * bs;
+        for (int32_t x = b; x < taken * span; x += kOneThreads) {  // span: what the slot map can hold, at most kOneTokens
+            const int32_t e = x / span, o = x - e * span;
             if (o < e_len[e] && o < num_slots_out - e_out[e]) slots[e_out[e] + o] = e_id[e] * bs + o;
         }
         __syncthreads();  // the entries are read before the next ones overwrite them

@@ -1,0 +1,25 @@
+"""Growth of block tables at its limits: lengths and sizes near 2^31."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("B", [1, 2000])
+def test_grow_with_blocks_near_2_31_positions(pkv, cuda_dev, B):
+    """One block of 2^31 - 1 positions: the last block of the pool's numbering space."""
+    bs = 2 ** 31 - 1
+    t = torch.full((B, 1), -1, dtype=torch.int32, device=cuda_dev)
+    starts = torch.zeros(B, dtype=torch.int32, device=cuda_dev)
+    ends = torch.zeros(B, dtype=torch.int32, device=cuda_dev)
+    ends[B // 2] = 5
+    ref = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+    cu, slots = pkv.pkv_grow_block_tables(t, starts, ends, ref, bs, num_new_tokens=8, err_flag=err)
+    assert slots.tolist() == [0, 1, 2, 3, 4, -1, -1, -1] and int(cu[-1]) == 5 and int(cu[B // 2]) == 0
+    assert ref.tolist() == [1] and int(t[B // 2]) == 0 and int((t == -1).sum()) == B - 1
+    again = pkv.pkv_grow_block_tables(t, ends, (ends + 2 * (ends > 0)).int(), ref, bs, num_new_tokens=3, err_flag=err)
+    assert again[1].tolist() == [5, 6, -1] and int(err.item()) == 0
+    t2, two = torch.full((B, 3), -1, dtype=torch.int32, device=cuda_dev), torch.zeros(2, dtype=torch.int32, device=cuda_dev)
+    cu, slots = pkv.pkv_grow_block_tables(t2, starts, ends, two, 2 ** 30 - 1, num_new_tokens=20000, err_flag=err)
+    assert slots[:5].tolist() == [0, 1, 2, 3, 4] and bool((slots[5:] == -1).all()) and two.tolist() == [1, 0]
