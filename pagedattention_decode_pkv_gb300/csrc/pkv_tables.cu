@@ -198,10 +198,10 @@ table_assign_kernel(int32_t *__restrict__ block_tables, int32_t max_blocks, cons
             for (int64_t j = g.held + lane; j < g.grown; j += 32) row[j] = -1;
             if (lane == 0 && err_flag) atomicOr(err_flag, PKV_ERRBIT_NO_BLOCKS);
         }
-        for (int64_t p = g.start + lane; p < upto; p += 32) {
-            const int64_t k = out0 + p - g.start;
-            if (k < num_slots_out) slots[k] = id < 0 ? -1 : static_cast<int32_t>(id * static_cast<int64_t>(bs) + p % bs);
-        }
+        // as far as the slot map goes: the span of lengths that are not valid may be 2^32
+        const int64_t stop = min(upto, g.start + max(num_slots_out - out0, static_cast<int64_t>(0)));
+        for (int64_t p = g.start + lane; p < stop; p += 32)
+            slots[out0 + p - g.start] = id < 0 ? -1 : static_cast<int32_t>(id * static_cast<int64_t>(bs) + p % bs);
         if (lane == 0 && err_flag && out0 + max(g.end - g.start, static_cast<int64_t>(0)) > num_slots_out)
             atomicOr(err_flag, PKV_ERRBIT_SPAN);
         return;

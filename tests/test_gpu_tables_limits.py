@@ -23,3 +23,17 @@ def test_grow_with_blocks_near_2_31_positions(pkv, cuda_dev, B):
     t2, two = torch.full((B, 3), -1, dtype=torch.int32, device=cuda_dev), torch.zeros(2, dtype=torch.int32, device=cuda_dev)
     cu, slots = pkv.pkv_grow_block_tables(t2, starts, ends, two, 2 ** 30 - 1, num_new_tokens=20000, err_flag=err)
     assert slots[:5].tolist() == [0, 1, 2, 3, 4] and bool((slots[5:] == -1).all()) and two.tolist() == [1, 0]
+
+
+@pytest.mark.parametrize("B", [3, 2000])
+def test_grow_lengths_that_span_2_32(pkv, cuda_dev, B):
+    """Garbage lengths, each span as long as 32 bits allow: no slots, the tables as they were, at once."""
+    t = torch.full((B, 4), 3, dtype=torch.int32, device=cuda_dev)
+    starts = torch.full((B,), -2 ** 31, dtype=torch.int32, device=cuda_dev)
+    ends = torch.full((B,), 2 ** 31 - 1, dtype=torch.int32, device=cuda_dev)
+    ref = torch.zeros(9, dtype=torch.int32, device=cuda_dev)
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+    cu, slots = pkv.pkv_grow_block_tables(t, starts, ends, ref, 16, num_new_tokens=1000, err_flag=err)
+    assert cu.tolist() == [0] + [2 ** 31 - 1] * B and bool((slots == -1).all())
+    assert bool((t == 3).all()) and not bool(ref.any())
+    assert int(err.item()) == pkv.ERRBIT_CONTEXT | pkv.ERRBIT_SPAN
