@@ -192,7 +192,8 @@ PKV_API pkv_status pkv_compute_slot_mapping(const int32_t *block_tables, int32_t
  *   outside [0, num_blocks) becomes -1, PKV_ERRBIT_BLOCK_RANGE; a count that is
  *   not positive stays, PKV_ERRBIT_REF_COUNT.
  *
- * num_blocks * block_size < 2^31, at most 65535 sequences per call.
+ * num_blocks * block_size < 2^31, at most 65535 sequences per call.  num_seqs == 0
+ * enqueues nothing: cu_new and slot_mapping stay as they are, for the caller to fill.
  */
 PKV_API size_t pkv_grow_block_tables_workspace_size(int32_t num_seqs, int32_t num_blocks, int64_t num_new_tokens);
 PKV_API pkv_status pkv_grow_block_tables(int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *starts,

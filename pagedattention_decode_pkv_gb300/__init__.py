@@ -250,12 +250,13 @@ def pkv_grow_block_tables(block_tables, starts, ends, ref_counts, block_size: in
     """Sequence b grows from starts[b] to ends[b] positions: its new blocks (the
     lowest free ones, sequences in order) go into block_tables and ref_counts in
     place.  Returns (cu_new [num_seqs + 1], slot_mapping [num_new_tokens]);
-    num_new_tokens may be an upper bound (slots past the last position are -1)."""
+    num_new_tokens may be an upper bound (slots past the last position are -1, all
+    of them for an empty batch)."""
     dev = _device_of(block_tables, starts, ends, ref_counts, cu_new, out, workspace, err_flag)
     B, max_blocks = _table_args(block_tables, starts, ends, ref_counts, ("starts", "ends"))
     nb = ref_counts.numel()
     if cu_new is None:
-        cu_new = _empty(B + 1, torch.int32, dev, stream) if B else torch.zeros(1, dtype=torch.int32, device=dev)
+        cu_new = _empty(B + 1, torch.int32, dev, stream)
     if out is None:
         out = _empty(num_new_tokens, torch.int32, dev, stream)
     _want_i32(cu_new=cu_new, out=out)
@@ -267,6 +268,10 @@ def pkv_grow_block_tables(block_tables, starts, ends, ref_counts, block_size: in
     _call(dev, _lib.pkv_grow_block_tables, block_tables.data_ptr(), max_blocks, starts.data_ptr(), ends.data_ptr(), B,
           block_size, ref_counts.data_ptr(), nb, cu_new.data_ptr(), out.data_ptr(), num_new_tokens, _addr(workspace),
           0 if workspace is None else workspace.numel() * workspace.element_size(), _flag(err_flag), _raw_stream(dev, stream))
+    if not B:  # the library enqueues nothing for an empty batch
+        with torch.cuda.stream(stream):  # None: the current one
+            cu_new.zero_()
+            out.fill_(-1)
     return cu_new, out
 
 

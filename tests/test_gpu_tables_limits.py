@@ -1,8 +1,26 @@
-"""Growth of block tables at its limits: lengths and sizes near 2^31."""
+"""Growth of block tables at its limits: no sequences, lengths and sizes near 2^31."""
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("nb", [0, 10, 300000])
+@pytest.mark.parametrize("cap", [0, 5, 20000])
+def test_grow_of_no_sequences(pkv, cuda_dev, nb, cap):
+    """An empty batch: the offset 0, and a slot map of -1 that a store skips."""
+    i32 = lambda v, *shape: torch.full(shape, v, dtype=torch.int32, device=cuda_dev)  # noqa: E731
+    none, ref, cu, slots = i32(0, 0), i32(0, nb), i32(7, 1), i32(5, cap)
+    err = i32(0, 1)
+    got = pkv.pkv_grow_block_tables(i32(0, 0, 6), none, none, ref, 16, num_new_tokens=cap, cu_new=cu, out=slots, err_flag=err)
+    assert got[0] is cu and got[1] is slots
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for cu, slots in (got, pkv.pkv_grow_block_tables(i32(0, 0, 6), none, none, ref, 16, num_new_tokens=cap),
+                      pkv.pkv_grow_block_tables(i32(0, 0, 6), none, none, ref, 16, num_new_tokens=cap, stream=side)):
+        torch.cuda.synchronize()
+        assert cu.tolist() == [0] and slots.numel() == cap and bool((slots == -1).all())
+    assert int(err.item()) == 0 and not bool(ref.any())
 
 
 @pytest.mark.parametrize("B", [1, 2000])
