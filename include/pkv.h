@@ -534,9 +534,11 @@ PKV_API pkv_status pkv_paged_attention_decode_mod(
  * f32 scores, softmax and accumulators.  P enters its product rounded to dtype (f16
  * over 8-bit caches, whose codes are widened exactly; bf16 queries become f16 under
  * one power of two per row).  Shapes and alignment as pkv_paged_attention_prefill.
- * K and V of masked keys may hold anything in rows of other sequences, past the span,
- * or in front of every visible key; a non-finite V value that one query of a 256-row
- * tile pair sees may reach queries of that pair that do not.  Over bf16 caches a
+ * Masked keys may hold anything in K.  Rows go in pairs of tiles, 256 / G consecutive
+ * positions (G = num_q_heads / num_kv_heads) counted from a sequence's last one down:
+ * V may hold anything in front of the lowest key that a query of the pair sees and
+ * behind the highest; between the two a non-finite value of V may reach queries of
+ * that pair which do not see it, and no others.  Over bf16 caches a
  * softcap of 50.5 and less keeps 2^(s log2 e) itself, so max |V| times the number of
  * keys must stay below 2^54.
  * Device errors: starts[b] < 0 or a span needing more than max_blocks_per_seq blocks

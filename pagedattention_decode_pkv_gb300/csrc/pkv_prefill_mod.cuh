@@ -388,9 +388,10 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             int fix_jj = -1;  // a block whose V rows are still to be zeroed
             unsigned fix_miss = 0;
             uint32_t lands = 0;  // blocks that went through kVLand
-            // V rows that no row sees, past the sequence or of a missing page read as
-            // zero (0 x NaN would stay): such a tile lands on a barrier of its own, and
-            // its full barrier is arrived on when the rows are zero.
+            // V rows that no row of the CTA sees (in front of the lowest key, from the highest
+            // on: later tokens, past the sequence) or of a missing page read as zero (0 x NaN
+            // would stay): such a tile lands on a barrier of its own, and its full barrier is
+            // arrived on when the rows are zero.
             auto zero_v = [&]() -> bool {
                 if (!wait_bar(L::kVLand, lands & 1)) return false;
                 ++lands;
@@ -399,7 +400,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const uint32_t vt = sRing + static_cast<uint32_t>(slot) * kModTile;
                 for (int i = lane; i < kModKeys * 16; i += 32) {
                     const int rr = i >> 4, c = i & 15, key = (j0 + fix_jj) * kModKeys + rr;
-                    if (key < key_lo || key >= total || (fix_miss >> (rr >> 4) & 1))
+                    if (key < key_lo || key >= key_hi || (fix_miss >> (rr >> 4) & 1))
                         st_shared_v4(vt + (c >> 3) * kModHalf + rr * 128 + (c & 7) * 16, 0, 0, 0, 0);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -431,7 +432,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const int slot_row = mine ? id * bs + key % bs : 0;
                 int next_id = -1;
                 float next_ks = 1.f, next_vs = 1.f;
-                const bool fix = miss || (j0 + jj) * kModKeys < key_lo || (j0 + jj + 1) * kModKeys > total;
+                const bool fix = miss || (j0 + jj) * kModKeys < key_lo || (j0 + jj + 1) * kModKeys > key_hi;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     const int item = 2 * jj + kv, slot = item % kSlots;
@@ -602,7 +603,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     for (int e = 0; e < 4; ++e) codes4_to_f16x4<FMT, false>(x[e], y[2 * e], y[2 * e + 1]);
                     if (fix) {
                         const int key = key0 + rr;
-                        if (key < key_lo || key >= total || (miss >> (rr >> 4) & 1)) {
+                        if (key < key_lo || key >= key_hi || (miss >> (rr >> 4) & 1)) {
 #pragma unroll
                             for (int e = 0; e < 8; ++e) y[e] = 0;
                         }
