@@ -544,7 +544,9 @@ PKV_API pkv_status pkv_paged_attention_decode_mod(
  * Device errors: starts[b] < 0 or a span needing more than max_blocks_per_seq blocks
  * gives zero rows and PKV_ERRBIT_CONTEXT; n_b < 0 or n_b > max_q_len leaves the
  * sequence's rows as they were and sets PKV_ERRBIT_CONTEXT; a used block id outside
- * [0, num_blocks) drops that block's tokens and sets PKV_ERRBIT_BLOCK_RANGE.
+ * [0, num_blocks) drops that block's tokens and sets PKV_ERRBIT_BLOCK_RANGE.  Blocks
+ * in front of every visible key or behind all of them are not used: their entries and
+ * scales may hold anything.
  */
 PKV_API size_t pkv_paged_attention_prefill_mod_workspace_size(int32_t num_seqs, int32_t num_q_heads,
                                                               int32_t num_kv_heads, int32_t head_dim,

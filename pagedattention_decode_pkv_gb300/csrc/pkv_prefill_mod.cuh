@@ -286,11 +286,16 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             qv[i] = up < left ? __ldg(src + (up * Hq + ((2 * i) & (G - 1))) * 16) : make_uint4(0, 0, 0, 0);
         }
     };
-    // The sequence's table entry for this lane's 16 keys of block j (0: none)
+    // The sequence's table entry for this lane's 16 keys of block j (0: none).  Only a chunk of
+    // 2^box_lg keys (all of one page) that reaches the CTA's keys [lo, hi) is looked up: pages that
+    // nobody sees may be missing.
     const int32_t *table = A.block_tables + static_cast<int64_t>(b) * A.max_blocks;
-    auto owned = [&](int j) { return lane < 8 && j * kModKeys + 16 * lane < total; };
-    auto entry = [&](int j) -> int {  // key / bs < ceil(total / bs) <= max_blocks
-        return owned(j) ? table[(j * kModKeys + 16 * lane) / bs] : 0;
+    auto owned = [&](int j, int lo, int hi) {
+        const int box = 1 << A.box_lg, last = (j * kModKeys + 16 * lane) | (box - 1);
+        return lane < 8 && last >= lo && last - box < hi - 1;
+    };
+    auto entry = [&](int j, int lo, int hi) -> int {  // hi <= total: key / bs < ceil(total / bs) <= max_blocks
+        return owned(j, lo, hi) ? table[(j * kModKeys + 16 * lane) / bs] : 0;
     };
     if (t < 2) {
         if constexpr (!C8) load_q();
@@ -326,8 +331,8 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             cta[2] = q_begin;
             cta[3] = n;
         }
-        raw0 = entry(key_lo / kModKeys);
-        raw1 = entry(key_lo / kModKeys + 1);
+        raw0 = entry(key_lo / kModKeys, key_lo, key_hi);
+        raw1 = entry(key_lo / kModKeys + 1, key_lo, key_hi);
     }
     tc_fence_before();
     __syncthreads();  // the barriers, the range and the TMEM address are there
@@ -364,9 +369,9 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             // loaded two blocks ahead and scales one, so that no copy waits for them.
             const int box_rows = 1 << A.box_lg;
             bool bad = false;
-            // a page id, -1 past the sequence, -2 out of range
+            // a page id, -1 where nobody sees a key, -2 out of range
             auto page = [&](int j, int raw) -> int {
-                if (!owned(j)) return -1;
+                if (!owned(j, key_lo, key_hi)) return -1;
                 if (raw >= 0 && raw < A.num_blocks) return raw;
                 bad = true;
                 return -2;
@@ -413,8 +418,8 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             float ks = 1.f, vs = 1.f;
             if (nb > 0) {
                 if (split != 0) {  // the first split starts at the lowest key's block
-                    raw0 = entry(j0);
-                    raw1 = entry(j0 + 1);
+                    raw0 = entry(j0, key_lo, key_hi);
+                    raw1 = entry(j0 + 1, key_lo, key_hi);
                 }
                 id = page(j0, raw0);
                 next_raw = raw1;
@@ -423,10 +428,9 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             }
             for (int jj = 0; jj < nb && !timed_out; ++jj) {
                 const int key = (j0 + jj) * kModKeys + 16 * lane;
-                const bool copied = lane < 8 && id >= 0 && (key | (box_rows - 1)) >= key_lo;  // the chunk reaches key_lo
                 const unsigned miss = __ballot_sync(0xffffffffu, id == -2);
                 const unsigned neg = __ballot_sync(0xffffffffu, C8 && id >= 0 && !(ks >= 0.f));
-                const unsigned chunks = __ballot_sync(0xffffffffu, copied && (key & (box_rows - 1)) == 0);
+                const unsigned chunks = __ballot_sync(0xffffffffu, id >= 0 && (key & (box_rows - 1)) == 0);
                 const uint32_t chunk_bytes = static_cast<uint32_t>(box_rows) * (C8 ? 128 : 256);
                 const bool mine = (chunks >> lane) & 1;
                 const int slot_row = mine ? id * bs + key % bs : 0;
@@ -475,7 +479,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         next_id = page(j0 + jj + 1, next_raw);
                         next_ks = scale_of(A.k_scale, next_id);
                         next_vs = scale_of(A.v_scale, next_id);
-                        next_raw = entry(j0 + jj + 2);
+                        next_raw = entry(j0 + jj + 2, key_lo, key_hi);
                     }
                     if (!C8 && kv == 0 && fix_jj >= 0 && !zero_v()) {
                         timed_out = true;

@@ -54,3 +54,33 @@ def test_nonfinite_in_later_tokens(pkv, cuda_dev, fmt, rule, start, at):
     out, err = _call(pkv, q, caches, batch.block_tables, starts, cu, batch.scale, 200, rules)
     assert err == 0
     sr.assert_within(out[:at], ref, clean, caches[1][1])
+
+
+@pytest.mark.parametrize("fmt", [None, "fp8", "int8"])
+@pytest.mark.parametrize("rule", ["plain", "bounded", "alibi"])
+@pytest.mark.parametrize("bs", [16, 48, 256])
+def test_entries_that_nobody_sees(pkv, cuda_dev, fmt, rule, bs):
+    """Table entries in front of every row's window, or behind the last row that sees anything, are not
+    used: they may be missing or wrong without an error, and their blocks' scales are not read."""
+    spans = [(300, 60), (0, 90), (700, 20)]
+    batch, q, starts, cu, ns = _case(torch.bfloat16, 16, 8, bs, spans, 8, cuda_dev)
+    caches = _caches(pkv, fmt, batch, cuda_dev)
+    ks = [p - 69 for p in range(300, 360)] + [0 if p < 70 else 10 ** 6 for p in range(90)] + [690] * 20
+    rules = {**_rules(rule, 16, cuda_dev), "key_starts": torch.tensor(ks, dtype=torch.int32, device=cuda_dev)}
+    ref = _reference(q, caches, batch.block_tables, [300, 0, 700], ns, batch.scale, rules)
+    tables = batch.block_tables.clone()
+    unused = [(0, j) for j in range(231 // bs)] + [(1, j) for j in range(sr.cdiv(70, bs), sr.cdiv(90, bs))]
+    unused += [(2, j) for j in range(690 // bs)]
+    for i, (b, j) in enumerate(unused):
+        tables[b, j] = -1 if i % 2 else 77_777
+    out, err = _call(pkv, q, caches, tables, starts, cu, batch.scale, 60 + 30, rules)
+    assert err == 0
+    sr.assert_within(out, ref, caches[1][0], caches[1][1])
+    if fmt:
+        scales = caches[1][1].clone()
+        for b, j in unused:
+            for _, s in caches:
+                s[batch.block_tables[b, j]] = float("nan") if b else float("inf")
+        out, err = _call(pkv, q, caches, batch.block_tables, starts, cu, batch.scale, 60 + 30, rules)
+        assert err == 0
+        sr.assert_within(out, ref, caches[1][0], scales)
