@@ -958,7 +958,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 
 // Joins the splits of a row: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
 // One warp per (sequence, query, head), lanes over the dims.  Splits without a
-// visible key carry m = -inf and weight 0, and their O is not read.
+// visible key carry m = -inf and l = 0, and their O is not read.
 constexpr int kModMergeThreads = 256;
 
 template <typename T>
@@ -985,7 +985,7 @@ prefill_mod_merge_kernel(const __grid_constant__ ModArgs A, int64_t rows) {
     float l = 0.f;
     for (int s = 0; s < used; ++s) {
         const float2 v = ml[s];
-        if (v.x == -INFINITY) continue;
+        if (v.x == -INFINITY && v.y == 0.f) continue;  // (scores that are all NaN leave the maximum there, and a NaN sum)
         const float w = exp2f(v.x - M);
         const float4 o = __ldg(reinterpret_cast<const float4 *>(A.o_part + (row * A.nsplit + s) * kFastHeadDim) + lane);
         acc.x = fmaf(w, o.x, acc.x);

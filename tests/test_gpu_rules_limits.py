@@ -84,3 +84,18 @@ def test_entries_that_nobody_sees(pkv, cuda_dev, fmt, rule, bs):
         out, err = _call(pkv, q, caches, batch.block_tables, starts, cu, batch.scale, 60 + 30, rules)
         assert err == 0
         sr.assert_within(out, ref, caches[1][0], scales)
+
+
+@pytest.mark.parametrize("fmt", [None, "fp8"])
+@pytest.mark.parametrize("rule", ["plain", "cap", "alibi"])
+@pytest.mark.parametrize("upto", [256, 2001])
+def test_nan_in_visible_keys(pkv, cuda_dev, fmt, rule, upto):
+    """Visible NaN keys make the row NaN, also where they are all that one CTA of a split span sees."""
+    spans = [(2000, 1)]
+    batch, q, starts, cu, ns = _case(torch.bfloat16, 8, 2, 16, spans, 5, cuda_dev)
+    caches = _caches(pkv, fmt, batch, cuda_dev)
+    for t in range(upto):
+        caches[0][0][int(batch.block_tables[0, t // 16]), t % 16] = 0x7F if fmt else float("nan")
+    assert pkv.pkv_paged_attention_prefill_mod_workspace_size(1, 8, 2, 128, 16, 1, batch.block_tables.shape[1]) > 0
+    out, _ = _call(pkv, q, caches, batch.block_tables, starts, cu, batch.scale, 1, _rules(rule, 8, cuda_dev))
+    assert bool(out.isnan().all())
