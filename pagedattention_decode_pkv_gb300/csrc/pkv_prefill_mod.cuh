@@ -746,8 +746,8 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                             const float su = C8 ? A.su * f->ks[g0 + (c0 + i) / 16] * rq : A.su;
                             const float e = __uint_as_float(v[i]) * su;  // 2 log2 e score / cap
                             const float big = fmaf(fast_rcp(1.f + fast_exp2(e)), -2.f * A.capl2, A.capl2);
-                            // (under a small cap those bits are there for small scores too)
-                            x[c0 + i] = kFree || fabsf(e) > kTanhLimit * 2.8853900817779268f ? big : x[c0 + i];
+                            // each score by its own size: a row's bits are its own
+                            x[c0 + i] = fabsf(e) > kTanhLimit * 2.8853900817779268f ? big : x[c0 + i];
                         }
                     }
                 }

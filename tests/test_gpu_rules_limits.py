@@ -86,6 +86,27 @@ def test_entries_that_nobody_sees(pkv, cuda_dev, fmt, rule, bs):
         sr.assert_within(out, ref, caches[1][0], scales)
 
 
+@pytest.mark.parametrize("softcap", [8.0, 50.0, 60.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("fmt", [None, "fp8"])
+def test_rows_do_not_depend_on_their_neighbours(pkv, cuda_dev, softcap, dtype, fmt):
+    """A row's bits are the same whatever the scores of the rows beside it and of keys that it does not see."""
+    spans = [(200, 120)]
+    batch, q, starts, cu, ns = _case(dtype, 8, 8, 16, spans, 31, cuda_dev)
+    caches = _caches(pkv, fmt, batch, cuda_dev)
+    args = (batch.block_tables, starts, cu, batch.scale, 120, {"softcap": softcap})
+    want, _ = _call(pkv, q, caches, *args)
+    loud = q.clone()
+    loud[::2] *= 100
+    got, _ = _call(pkv, loud, caches, *args)
+    assert torch.equal(got[1::2], want[1::2])
+    if not fmt:
+        for t in range(316, 320):
+            batch.k_cache[int(batch.block_tables[0, t // 16]), t % 16] *= 1000
+        got, _ = _call(pkv, q, caches, *args)
+        assert torch.equal(got[:116], want[:116])
+
+
 @pytest.mark.parametrize("fmt", [None, "fp8"])
 @pytest.mark.parametrize("rule", ["plain", "cap", "alibi"])
 @pytest.mark.parametrize("upto", [256, 2001])
