@@ -174,8 +174,11 @@ def _addrs(*tensors):
 
 
 def _raw_stream(dev, stream):
+    if stream is not None:
+        return stream.cuda_stream
     # the raw handle alone: a Stream object costs a short call 2 to 4 us
-    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(dev).cuda_stream if current is None else current(dev.index)
 
 
 def _empty(n, dtype, dev, stream):

@@ -142,3 +142,18 @@ def test_error_flag_type(pkv, cuda_dev):
         pkv.pkv_grow_block_tables(t, i, i, r, 16, num_new_tokens=0, err_flag=byte)
     with pytest.raises(TypeError):
         pkv.pkv_shrink_block_tables(t, i, i, r, 16, err_flag=byte)
+
+
+def test_current_stream_without_the_raw_handle(pkv, cuda_dev, monkeypatch):
+    """Where torch has no raw stream handle to give, the calls still run on the current stream."""
+    t, lens = torch.full((2, 3), -1, dtype=torch.int32, device=cuda_dev), torch.tensor([5, 20], dtype=torch.int32, device=cuda_dev)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    with torch.cuda.stream(side):
+        assert pkv._raw_stream(cuda_dev, None) == side.cuda_stream
+        ref_counts = torch.zeros(9, dtype=torch.int32, device=cuda_dev)
+        cu, _ = pkv.pkv_grow_block_tables(t, torch.zeros_like(lens), lens, ref_counts, 16, num_new_tokens=25)
+    side.synchronize()
+    assert cu.tolist() == [0, 5, 25] and t.tolist() == [[0, -1, -1], [1, 2, -1]]
+    assert pkv._raw_stream(cuda_dev, side) == side.cuda_stream
