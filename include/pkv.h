@@ -524,8 +524,9 @@ PKV_API pkv_status pkv_paged_attention_decode_mod(
  * prefix, and over 8-bit caches.
  *
  *   k_scale, v_scale  device float32 [num_blocks, num_kv_heads] for PKV_CACHE_E4M3
- *                     and PKV_CACHE_INT8 pools, not negative, V scales at
- *                     most 2^90 (NULL for PKV_CACHE_DTYPE)
+ *                     and PKV_CACHE_INT8 pools, not negative; V scales 0, or
+ *                     from 2^-100 (smaller ones lose bits of the output) to
+ *                     2^90 (NULL for PKV_CACHE_DTYPE)
  *   max_q_len         host bound on n_b; the exact maximum gives the best schedule
  *   workspace         pkv_paged_attention_prefill_mod_workspace_size bytes (may be
  *                     0), 256-byte aligned, needed during the call only; calls that
@@ -539,8 +540,8 @@ PKV_API pkv_status pkv_paged_attention_decode_mod(
  * V may hold anything in front of the lowest key that a query of the pair sees and
  * behind the highest; between the two a non-finite value of V may reach queries of
  * that pair which do not see it, and no others.  Over bf16 caches a
- * softcap of 50.5 and less keeps 2^(s log2 e) itself, so max |V| times the number of
- * keys must stay below 2^54.
+ * softcap of 50.5 and less keeps 2^(s log2 e) itself as P, so max |V| times the number
+ * of keys must stay below 2^54, and values of V below 2^-53 may count as zero.
  * Device errors: starts[b] < 0 or a span needing more than max_blocks_per_seq blocks
  * gives zero rows and PKV_ERRBIT_CONTEXT; n_b < 0 or n_b > max_q_len leaves the
  * sequence's rows as they were and sets PKV_ERRBIT_CONTEXT; a used block id outside

@@ -34,6 +34,25 @@ def _reference(q, caches, tables, starts, ns, scale, rules):
                       rules.get("softcap", 0.0), rules.get("alibi_slopes"), rules.get("key_starts"))
 
 
+def _dropping(q, caches, table, start, n, gone, scale, rules):
+    """The definition with the scores of the keys in the 16-token blocks `gone` at minus infinity."""
+    Hq, G = q.shape[1], q.shape[1] // caches[0][0].shape[2]
+    total = start + n
+    k, v = (sr.rows_of(sr.dequantize(c, x), table, total) for c, x in caches)
+    pos, t = torch.arange(start, total), torch.arange(total)
+    seen = (t <= pos[:, None]) & ~torch.isin(t // 16, torch.tensor(gone))
+    want, mag = torch.zeros(q.shape, dtype=torch.float64), torch.zeros(q.shape, dtype=torch.float64)
+    for h in range(Hq):
+        x = scale * (q[:, h].cpu().double() @ k[:, h // G].T)
+        if "softcap" in rules:
+            x = rules["softcap"] * torch.tanh(x / rules["softcap"])
+        if "alibi_slopes" in rules:
+            x = x - rules["alibi_slopes"][h].cpu().double() * (pos[:, None] - t)
+        w = torch.softmax(x.masked_fill(~seen, float("-inf")), -1)
+        want[:, h], mag[:, h] = w @ v[:, h // G], w @ v[:, h // G].abs()
+    return want, mag, seen.sum(1).double()[:, None, None]
+
+
 @pytest.mark.parametrize("rule", ["plain", "bounded", "cap", "cap-alibi"])
 @pytest.mark.parametrize("fmt", [None, "fp8"])
 @pytest.mark.parametrize("start", [10, 1034])
@@ -86,6 +105,54 @@ def test_entries_that_nobody_sees(pkv, cuda_dev, fmt, rule, bs):
         sr.assert_within(out, ref, caches[1][0], scales)
 
 
+@pytest.mark.parametrize("fmt", [None, "fp8", "int8"])
+@pytest.mark.parametrize("rule", list(RULES))
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("spans", [[(100, 90), (0, 40)], [(1500, 40)]])
+def test_missing_blocks(pkv, cuda_dev, fmt, rule, dtype, spans):
+    """Table entries out of range among the used ones: their tokens are dropped, whether they are a
+    part of a 64-key step or all of it, in a span whose keys are split too."""
+    batch, q, starts, cu, ns = _case(dtype, 16, 8, 16, spans, 72, cuda_dev)
+    caches = _caches(pkv, fmt, batch, cuda_dev)
+    rules = _rules(rule, 16, cuda_dev)
+    tables = batch.block_tables.clone()
+    gone = [1] + list(range(4, 8))  # positions 16 .. 31 and 64 .. 127
+    for j in gone:
+        tables[0, j] = -1 if j % 2 else 10_000
+    out, err = _call(pkv, q, caches, tables, starts, cu, batch.scale, max(ns), rules)
+    assert err == pkv.ERRBIT_BLOCK_RANGE
+    s, n = spans[0]
+    ref = _dropping(q[:n], caches, batch.block_tables[0], s, n, gone, batch.scale, rules)
+    sr.assert_within(out[:n], ref, caches[1][0], caches[1][1])
+    if len(spans) > 1:  # the other sequence is whole
+        ref = _reference(q[n:], caches, batch.block_tables[1:], [0], ns[1:], batch.scale, rules)
+        sr.assert_within(out[n:], ref, caches[1][0], caches[1][1])
+
+
+@pytest.mark.parametrize("fmt", [None, "fp8", "int8"])
+@pytest.mark.parametrize("rule", list(RULES))
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_missing_blocks_of_a_decode_step(pkv, cuda_dev, fmt, rule, dtype):
+    """The same for a decode call: whole stages of 16 tokens are dropped, one of them the last."""
+    batch, q, _, _, _ = _case(dtype, 16, 8, 16, [(199, 1), (77, 1)], 72, cuda_dev)
+    caches = _caches(pkv, fmt, batch, cuda_dev)
+    rules = _rules(rule, 16, cuda_dev)
+    tables = batch.block_tables.clone()
+    gone = [1] + list(range(4, 8)) + [12]
+    for j in gone:
+        tables[0, j] = -1 if j % 2 else 10_000
+    (kc, ks), (vc, vs) = caches
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+    ctx = torch.tensor([200, 78], dtype=torch.int32, device=cuda_dev)
+    out = pkv.pkv_paged_attention_decode_mod(q, kc, vc, tables, ctx, batch.scale, 200, k_scale=ks, v_scale=vs,
+                                             err_flag=err, **rules)
+    assert int(err.item()) == pkv.ERRBIT_BLOCK_RANGE
+    ref = _dropping(q[:1], caches, batch.block_tables[0], 199, 1, gone, batch.scale, rules)
+    sr.assert_within(out[:1], ref, vc, vs)
+    ref = _reference(q[1:], caches, batch.block_tables[1:], [77], [1], batch.scale, rules)
+    sr.assert_within(out[1:], ref, vc, vs)
+
+
 @pytest.mark.parametrize("softcap", [8.0, 50.0, 60.0])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("fmt", [None, "fp8"])
@@ -120,3 +187,57 @@ def test_nan_in_visible_keys(pkv, cuda_dev, fmt, rule, upto):
     assert pkv.pkv_paged_attention_prefill_mod_workspace_size(1, 8, 2, 128, 16, 1, batch.block_tables.shape[1]) > 0
     out, _ = _call(pkv, q, caches, batch.block_tables, starts, cu, batch.scale, 1, _rules(rule, 8, cuda_dev))
     assert bool(out.isnan().all())
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "int8"])
+@pytest.mark.parametrize("softcap", [0.0, 10.0])
+def test_smallest_scales(pkv, cuda_dev, fmt, softcap):
+    """V scales from 2^-100 to 2^-97 everywhere, and zero blocks: no bits are lost.  The comparison is at
+    2^100 times the values, exact in bf16 and in the reference."""
+    spans = [(100, 60), (0, 300)]
+    batch, q, starts, cu, ns = _case(torch.bfloat16, 8, 8, 16, spans, 8, cuda_dev)
+    (kc, ks), (vc, vs) = _codes(pkv, fmt, batch, 3, cuda_dev)
+    g = torch.Generator().manual_seed(2)
+    vs.copy_((1 + 7 * torch.rand(vs.shape, generator=g)).to(cuda_dev) * 2.0 ** -100)
+    for b in range(2):
+        i = int(batch.block_tables[b, 2])
+        vc[i], vs[i] = 0, 0
+    rules = {"softcap": softcap}
+    out, err = _call(pkv, q, ((kc, ks), (vc, vs)), batch.block_tables, starts, cu, batch.scale, 300, rules)
+    up = vs * 2.0 ** 100
+    ref = _reference(q, ((kc, ks), (vc, up)), batch.block_tables, [100, 0], ns, batch.scale, rules)
+    assert err == 0
+    sr.assert_within(out * 2.0 ** 100, ref, vc, up)
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("gain", [2.0 ** -44, 2.0 ** 42])
+def test_bounded_cap_with_values_of_extreme_size(pkv, cuda_dev, sign, gain):
+    """Every score at one end of a cap of 50, where P is 2^-72 or 2^72 without a reference maximum, times V
+    whose values are near the ends of what stays in f32's range (below 2^54 / keys; above 2^-53)."""
+    spans = [(0, 300)]
+    batch, q, starts, cu, ns = _case(torch.bfloat16, 8, 8, 16, spans, 8, cuda_dev)
+    g = torch.Generator().manual_seed(4)
+    base = torch.randn(128, generator=g)
+    base *= 128 ** 0.5 / base.norm()
+    rows = torch.randn(batch.k_cache.shape, generator=g)
+    batch.k_cache.copy_((base + 0.05 * rows).to(torch.bfloat16))
+    q.copy_((sign * 40 * base).to(torch.bfloat16).expand_as(q))  # scores near +-450
+    batch.v_cache.mul_(gain)
+    caches, rules = ((batch.k_cache, None), (batch.v_cache, None)), {"softcap": 50.0}
+    out, err = _call(pkv, q, caches, batch.block_tables, starts, cu, batch.scale, 300, rules)
+    assert err == 0
+    sr.assert_within(out, _reference(q, caches, batch.block_tables, [0], ns, batch.scale, rules), batch.v_cache)
+
+
+@pytest.mark.parametrize("fmt", [None, "int8"])
+def test_generous_bound_on_the_rows(pkv, cuda_dev, fmt):
+    """A bound so far above the rows that a sequence's tile pairs take several grids."""
+    spans = [(37, 64), (0, 1), (127, 130)]
+    batch, q, starts, cu, ns = _case(torch.bfloat16, 8, 1, 16, spans, 8, cuda_dev)
+    caches = _caches(pkv, fmt, batch, cuda_dev)
+    rules = _rules("cap-alibi", 8, cuda_dev)
+    out, err = _call(pkv, q, caches, batch.block_tables, starts, cu, batch.scale, 1 << 21, rules)
+    assert err == 0  # 16 positions a tile: 65536 pairs
+    ref = _reference(q, caches, batch.block_tables, [s for s, _ in spans], ns, batch.scale, rules)
+    sr.assert_within(out, ref, caches[1][0], caches[1][1])
