@@ -521,7 +521,9 @@ PKV_API pkv_status pkv_paged_attention_decode_mod(
  * pkv_paged_attention_prefill_mod -- pkv_paged_attention_prefill with score rules
  * (`mod`, may be NULL) and over any cache format: chunked prefill of a model with
  * capped scores, a distance bias, packed documents, local windows or a bidirectional
- * prefix, and over 8-bit caches.
+ * prefix, and over 8-bit caches.  Without a rule it gives what the plain call gives up
+ * to the order of its sums, in less time (8 prompts of 4096 tokens, 32 heads over 8
+ * KV heads, bf16: 908 us, the plain call 1158).
  *
  *   k_scale, v_scale  device float32 [num_blocks, num_kv_heads] for PKV_CACHE_E4M3
  *                     and PKV_CACHE_INT8 pools, not negative; V scales 0, or
@@ -534,7 +536,7 @@ PKV_API pkv_status pkv_paged_attention_decode_mod(
  *   other arguments as pkv_paged_attention_prefill.
  * f32 scores, softmax and accumulators.  P enters its product rounded to dtype (f16
  * over 8-bit caches, whose codes are widened exactly; bf16 queries become f16 under
- * one power of two per row).  Shapes and alignment as pkv_paged_attention_prefill.
+ * one power of two per row, which rounds elements below 2^-30 of the row's largest).  Shapes and alignment as pkv_paged_attention_prefill.
  * Masked keys may hold anything in K.  Rows go in pairs of tiles, 256 / G consecutive
  * positions (G = num_q_heads / num_kv_heads) counted from a sequence's last one down:
  * V may hold anything in front of the lowest key that a query of the pair sees and

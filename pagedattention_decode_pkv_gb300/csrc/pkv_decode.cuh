@@ -5,9 +5,9 @@
 //
 // The rules cost the tensor-core kernel arithmetic only, which hides behind the K and V
 // stream; keys in front of a window are not read.  With rules against without: 64
-// sequences of 1 .. 4096 tokens, 32 heads, fp16, bias: 275.8 us (7.2 TB/s) / 274.9; 128
-// sequences of 256 .. 8192 tokens, E4M3, 8 KV heads, cap 50: 159.8 us (6.4 TB/s) / 157.8;
-// 4 of up to 500 tokens, cap 50: 9.7 us / 9.3.
+// sequences of 1 .. 4096 tokens, 32 heads, fp16, bias: 281 us (7.1 TB/s) / 279; 128
+// sequences of 256 .. 8192 tokens, E4M3, 8 KV heads, cap 50: 164 us (6.3 TB/s) / 161;
+// 4 of up to 500 tokens, cap 50: 10.1 us / 9.5.
 #pragma once
 
 #include <cuda.h>

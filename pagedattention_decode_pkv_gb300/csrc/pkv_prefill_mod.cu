@@ -16,9 +16,10 @@ constexpr int kMaxSplits = 32;
 // Splits: one CTA runs per SM, so a launch of fewer than half as many CTAs as SMs
 // cuts its key blocks until it fills one wave, in runs of kMinSplitBlocks blocks at
 // least; longer launches gain nothing from it.  Cap 50, 32 heads over 8 KV heads, bf16,
-// with the joining kernel against one CTA a pair: 16 rows over 512 keys 11.6 us / 11.9,
-// over 2048 13.8 / 33.4; 64 over 8k 32 / 142; 4 x 16 over 32k 128 / 470; 8 x 64 over 4k
-// 53 / 76; 512 over 64k 568 / 1096.
+// with the joining kernel against one CTA a pair, on the GPU: 16 rows over 512 keys
+// 11.6 us / 11.9 (from Python, with the workspace and the second launch, 24 / 18), over
+// 2048 13.8 / 33.5 (24 / 34); 64 over 8k 33 / 145; 4 x 16 over 32k 128 / 472; 8 x 64 over
+// 4k 53 / 78; 512 over 64k 581 / 1127.
 PrefillPlan prefill_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_q_len, int32_t max_blocks, int32_t bs) {
     PrefillPlan p;
     const int G = Hq / Hkv, positions = kModRows / G;

@@ -26,8 +26,9 @@
 // converter warps and never rounded; ks multiplies the score, in f32.  P enters
 // its product as f16(p vs), and the row's reference maximum follows s + log2 vs,
 // which keeps p vs in f16's range whatever the scales; the row sum adds p itself.
-// bf16 queries become f16 under a power of two per row (exact; undone in the
-// score's factor), so no bf16 magnitude overflows.
+// bf16 queries become f16 under a power of two per row (undone in the score's factor), so
+// no bf16 magnitude overflows; elements from 2^-30 of their row's largest on are exact,
+// smaller ones off by at most 2^-38 of it.
 //
 // The CTA.  Two tiles of 128 query rows (128 / G positions x G heads) of one KV
 // head, accumulators in tensor memory: eight softmax warps hold one query row per
@@ -39,13 +40,13 @@
 // QK_{h+2} follows PV_h into the buffer that P_h leaves, so that S_{h+1} is there when
 // the softmax of h ends and its warps never wait for the tensor core's round trip.
 //
-// What bounds it.  Plain scores, 8 prompts of 4k (32 heads, 8 KV heads): 907 us, 1095
+// What bounds it.  Plain scores, 8 prompts of 4k (32 heads, 8 KV heads): 908 us, 1093
 // TFLOP/s.  A step of 64 keys of both tiles is 1240 clk of products alone: Q K^T at 64
 // keys reads its operands from shared memory at 386 clk where the arithmetic takes 256
 // (128 keys at once, one S buffer a tile, read less and ran 976 us: both tiles then sit
 // in their softmax together).  With the copies into the ring the step is 1534, with the
-// softmax warps beside it 1834.  Cap 50: 1038 us; the polynomial's operations come on
-// top.  With a bias 1235.  E4M3 and int8: 1267 and 1305; widening writes every tile once
+// softmax warps beside it 1834.  Cap 50: 1049 us; the polynomial's operations come on
+// top.  With a bias 1236.  E4M3 and int8: 1264 and 1297; widening writes every tile once
 // more.  Short spans: of a CTA's ~13k clk of setup, first products and output nothing
 // overlaps, for both tiles do them together (2 x 8k rows of packed documents of 60 to
 // 2500 rows: 150 us, 664 TFLOP/s).
@@ -91,9 +92,10 @@ constexpr uint64_t kModDeadlineNs = 2000000000ull;
 constexpr float kModRescale = 8.f;    // log2 units a block may exceed the reference maximum by before O is rescaled
 // CAP: no cap, a cap, or a cap that bounds the scores so far that no reference
 // maximum is needed: P = 2^s itself, |s| <= kFreeCap, is in bf16's range with all its
-// bits, and its sums times V are in f32's as long as keys x max |V| < 2^54. Without the
+// bits, and its sums times V are in f32's as long as keys x max |V| < 2^54 (at the other
+// end, V below 2^-53 under P = 2^-73, products leave f32's normal range). Without the
 // maximum and the rescaling 8 prompts of 4096 rows (32 heads, 8 KV heads, cap 50) take
-// 1038 us; f16 ones, with both, 1186.
+// 1049 us; with both (f16, or a cap of 51) 1180.
 enum { kNoCap = 0, kCap = 1, kCapBounded = 2 };
 constexpr float kFreeCap = 73.f;
 constexpr int kMaxGridPairs = 32768;  // grid.y

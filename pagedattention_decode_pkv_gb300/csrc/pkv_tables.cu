@@ -20,7 +20,7 @@
 // the earlier chunks' free counts.  The CTA that takes a block writes its
 // count, its table entry and the slots of its positions, so nothing waits for
 // another CTA's writes and the result does not depend on their order.  (512 prompts of up
-// to 4096 tokens, 262144 blocks: 17 us with the return of the blocks, of which the million
+// to 4096 tokens, 262144 blocks: 16 us with the return of the blocks, of which the million
 // slots are 4 MB.)  A small growth is one CTA that does both steps.
 #include <cuda_runtime.h>
 
@@ -38,9 +38,11 @@ constexpr int kTabSmemSeqs = 4096;       // need prefixes kept in shared memory 
 
 // Up to these sizes one CTA grows the tables alone, in one launch and without a workspace
 // to allocate.  A grow and a shrink, us, one launch / two, on the GPU in a graph and from
-// Python: 64 sequences by a token each, 20000 blocks: 6.3 / 8.1, 21.6 / 27; 1024 by 8,
-// 32768 blocks: 12.4 / 12.3, 21.5 / 28.  By 16 tokens each the one CTA takes 15.7 / 11.7
-// on the GPU: it writes the slots alone.
+// Python: 64 sequences by a token each, 20000 blocks: 6.2 / 7.3, 21 / 25; 1024 by up to 8,
+// 32768 blocks: 9.5 / 10.9, 22 / 25.  At the limits themselves (1024 by 8) the GPU times
+// tie, 12.7 / 12.1, and what is gained is a launch and an allocation on the host, 21 / 25:
+// nothing in a captured step.  By 16 tokens each the one CTA takes 18.1 / 13.6 on the GPU:
+// it writes the slots alone.
 constexpr int kOneThreads = 1024, kOneWarps = kOneThreads / 32;
 constexpr int kOneSeqs = kOneThreads;           // a thread per sequence
 constexpr int kOneBlocks = 32 * kOneThreads;    // a thread keeps 32 free bits
