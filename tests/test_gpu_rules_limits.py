@@ -241,3 +241,36 @@ def test_generous_bound_on_the_rows(pkv, cuda_dev, fmt):
     assert err == 0  # 16 positions a tile: 65536 pairs
     ref = _reference(q, caches, batch.block_tables, [s for s, _ in spans], ns, batch.scale, rules)
     sr.assert_within(out, ref, caches[1][0], caches[1][1])
+
+
+@pytest.mark.parametrize("fmt", [None, "fp8", "int8"])
+@pytest.mark.parametrize("bs", [16, 48, 256])
+@pytest.mark.parametrize("append", [False, True])
+def test_entries_in_front_of_a_decode_window(pkv, cuda_dev, fmt, bs, append):
+    """Released blocks in front of the window: no error, and their scales are not read."""
+    ctx, first = [400, 78, 700, 64], [231, 70, 699, 64]
+    batch, q, _, _, _ = _case(torch.bfloat16, 16, 8, bs, [(c - 1, 1) for c in ctx], 8, cuda_dev)
+    caches = _caches(pkv, fmt, batch, cuda_dev)
+    (kc, ks), (vc, vs) = caches
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=cuda_dev)  # noqa: E731
+    rules = {"softcap": 20.0, "key_starts": i32(first)}
+    row = {}
+    if append:
+        key, value = (torch.randn(4, 8, 128, device=cuda_dev).to(torch.bfloat16) for _ in range(2))
+        pkv.pkv_paged_attention_decode_mod(q, kc, vc, batch.block_tables, i32(ctx), batch.scale, 700, key=key, value=value,
+                                           k_scale=ks, v_scale=vs, **rules)  # the same row twice: the caches as they will be
+        row = {"key": key, "value": value}
+    ref = _reference(q, caches, batch.block_tables, [c - 1 for c in ctx], [1] * 4, batch.scale, rules)
+    tables, scales = batch.block_tables.clone(), None if vs is None else vs.clone()
+    for b, (c, f) in enumerate(zip(ctx, first)):
+        for j in range(min(f // bs, (c - 1) // bs)):
+            tables[b, j] = -1 if j % 2 else 77_777
+            for s in (ks, vs):
+                if s is not None:
+                    s[batch.block_tables[b, j]] = float("nan")
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+    for entries in (tables, batch.block_tables):
+        out = pkv.pkv_paged_attention_decode_mod(q, kc, vc, entries, i32(ctx), batch.scale, 700, k_scale=ks, v_scale=vs,
+                                                 err_flag=err, **row, **rules)
+        assert int(err.item()) == 0
+        sr.assert_within(out, ref, vc, scales)
