@@ -675,6 +675,109 @@ PKV_API pkv_status pkv_paged_attention_decode_append_int8(void *out, const void 
                                                           int32_t *err_flag, void *stream);
 
 /*
+ * 4-bit paged caches.  k_cache / v_cache hold codes, [num_blocks, num_kv_heads,
+ * block_size, head_dim / 2] bytes, and k_scale / v_scale one float16 per 32 dims of a
+ * row (a token of a KV head), [num_blocks, num_kv_heads, block_size, head_dim / 32]
+ * (passed as uint16_t bits).  A nibble u stands for scale * (u - 8).  Eight dims are one
+ * little-endian 32-bit word, nibbles from the lowest: dims 0 2 4 6 1 3 5 7.  Unlike the
+ * 8-bit caches a row carries its own scales, so rows are written one by one as they come,
+ * and 72 bytes hold what takes 256 in 16 bits (head_dim 128).
+ *   Writing x: scale = max|x| / 7 over the 32 dims (NaN ignored), rounded to bf16, then to
+ *   float16 (both to nearest even), at most 9344, so that scale * code is exact in
+ *   float16; code = x / scale rounded to the nearest integer, ties to even, within +-7
+ *   (NaN: 0), both from exact values; u = code + 8.  A zero scale stores zeros.  Values
+ *   beyond 65408 saturate; groups whose largest magnitude is below 2^-22 become zero, and
+ *   below 2^-11 the scale has fewer bits.
+ *
+ * pkv_store_kvcache_int4: "Step 1" into a 4-bit cache: row slot_mapping[i] <- key[i] /
+ *   value[i] (dtype any).  key_stride / value_stride: elements from one token to the next
+ *   (num_kv_heads * head_dim when contiguous; heads and dims are contiguous), so that both
+ *   may be parts of one projection's output.  Slot -1 is skipped; other slots outside the
+ *   pool are skipped and set PKV_ERRBIT_SLOT_RANGE.  Distinct slots are a precondition, as
+ *   in pkv_store_kvcache.
+ * pkv_load_kvcache_int4: the rows of both caches at slot_mapping read back, key / value
+ *   [num_tokens, num_kv_heads, head_dim] of dtype (outputs, 16-byte aligned): exact in
+ *   float32 and float16, rounded once in bf16.  Slots may repeat.  Slot -1 gives a zero
+ *   row, another slot outside the pool as well and PKV_ERRBIT_SLOT_RANGE.
+ * Both need head_dim a multiple of 32 (PKV_ERR_UNSUPPORTED otherwise; store: at most 1024)
+ * and codes 4-byte aligned; num_blocks * block_size < 2^31.
+ */
+PKV_API pkv_status pkv_store_kvcache_int4(const void *key, int64_t key_stride, const void *value, int64_t value_stride,
+                                          void *k_cache, void *v_cache, uint16_t *k_scale, uint16_t *v_scale,
+                                          const int32_t *slot_mapping, int64_t num_tokens, int32_t num_kv_heads,
+                                          int32_t head_dim, int32_t block_size, int32_t num_blocks, pkv_dtype dtype,
+                                          int32_t *err_flag, void *stream);
+PKV_API pkv_status pkv_load_kvcache_int4(void *key, void *value, const void *k_cache, const void *v_cache,
+                                         const uint16_t *k_scale, const uint16_t *v_scale, const int32_t *slot_mapping,
+                                         int64_t num_tokens, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                         int32_t num_blocks, pkv_dtype dtype, int32_t *err_flag, void *stream);
+
+/*
+ * Rotary positions with the cache write.  The first rotary_dim dims of a head are pairs
+ * (x_a, x_b): dims (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when interleaved.  At
+ * position p pair i becomes
+ *   amplitude * (x_a cos t - x_b sin t, x_b cos t + x_a sin t),   t = p * f_i radians;
+ * the other dims stay.  Frequencies are given to the device as turns per position in
+ * 64-bit fixed point, frac(f_i / 2 pi) * 2^64, so that far (and negative) positions lose
+ * nothing; a negated table turns back.
+ */
+typedef enum pkv_rope_scaling { PKV_ROPE_NONE = 0, PKV_ROPE_LINEAR = 1, PKV_ROPE_NTK = 2, PKV_ROPE_YARN = 3 } pkv_rope_scaling;
+typedef struct pkv_rope {
+    const uint64_t *turns; /* device [rotary_dim / 2] */
+    double amplitude;
+    int32_t rotary_dim;    /* even, 0 .. head_dim; 0: nothing is rotated */
+    int32_t interleaved;   /* 0 or 1 */
+} pkv_rope;
+
+/*
+ * pkv_rope_frequencies (host): the table and amplitude of f_i = base^(-2 i / rotary_dim),
+ * scaled for contexts `factor` times the trained length:
+ *   PKV_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *   PKV_ROPE_NTK     base * factor^(rotary_dim / (rotary_dim - 2)) in place of base
+ *   PKV_ROPE_YARN    with the turns n_i = original_len f_i / 2 pi and
+ *                    k_i = clamp((n_i - beta_slow) / (beta_fast - beta_slow), 0, 1):
+ *                    f_i k_i + f_i / factor (1 - k_i), amplitude 0.1 ln(factor) + 1
+ * The amplitude of the others is 1.  pkv_rope_turns (host): the table of any other
+ * frequencies, inv_freq in radians per position.
+ *   turns  host uint64 [rotary_dim / 2] (output), to be copied to the device
+ */
+PKV_API pkv_status pkv_rope_frequencies(int32_t rotary_dim, double base, pkv_rope_scaling scaling, double factor,
+                                        double original_len, double beta_fast, double beta_slow, uint64_t *turns,
+                                        double *amplitude);
+PKV_API pkv_status pkv_rope_turns(const double *inv_freq, int32_t num_pairs, uint64_t *turns);
+
+/*
+ * pkv_rope_store_kvcache: the step's queries rotated into q_out, its keys rotated into the
+ * paged cache, its values beside them, in one launch: what pkv_store_kvcache would store
+ * of rotated keys.  Arithmetic is f32, each output rounded once to dtype.
+ *   q            device, token i's heads at q + i * q_stride elements; q_out device
+ *                [num_tokens, num_q_heads, head_dim], may be q itself when q is contiguous,
+ *                and overlaps nothing otherwise.  num_q_heads may be 0.
+ *   key, value   as in pkv_store_kvcache_int4 (token strides)
+ *   positions    device int32 [num_tokens]
+ *   rope         NULL: nothing is rotated (positions may be NULL)
+ *   caches, slot_mapping, num_slots, errors as in pkv_store_kvcache; a token whose slot is
+ *                not stored has its query rotated all the same.
+ * pkv_rope_store_kvcache_int4: the same into 4-bit caches, quantised from the rotated
+ *   values without a rounding in between.
+ * head_dim at most 1024.  16-byte aligned buffers and strides, head_dim a multiple of 16
+ * up to 512, and rotary_dim a multiple of 16 (interleaved: 8; halves into 4-bit caches:
+ * rotary_dim and head_dim multiples of 64) take the vector kernel, others a scalar one.
+ */
+PKV_API pkv_status pkv_rope_store_kvcache(void *q_out, const void *q, int64_t q_stride, const void *key, int64_t key_stride,
+                                          const void *value, int64_t value_stride, const int32_t *positions,
+                                          const pkv_rope *rope, void *k_cache, void *v_cache, const int32_t *slot_mapping,
+                                          int64_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                          int64_t num_slots, pkv_dtype dtype, int32_t *err_flag, void *stream);
+PKV_API pkv_status pkv_rope_store_kvcache_int4(void *q_out, const void *q, int64_t q_stride, const void *key,
+                                               int64_t key_stride, const void *value, int64_t value_stride,
+                                               const int32_t *positions, const pkv_rope *rope, void *k_cache, void *v_cache,
+                                               uint16_t *k_scale, uint16_t *v_scale, const int32_t *slot_mapping,
+                                               int64_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                               int32_t head_dim, int32_t block_size, int32_t num_blocks, pkv_dtype dtype,
+                                               int32_t *err_flag, void *stream);
+
+/*
  * Host block allocator -- which physical block of the pool each sequence
  * owns ("Paged KV Cache - AI infra interview lesson": Walk the Shapes First;
  * Append slots during decode; Separate allocation, sharing and release).

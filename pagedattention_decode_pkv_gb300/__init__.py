@@ -33,12 +33,14 @@ PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA, PKV_ERR_OUT_OF_R
 PKV_F32, PKV_F16, PKV_BF16 = 0, 1, 2
 PKV_U32, PKV_U64 = 0, 1
 PKV_CACHE_DTYPE, PKV_CACHE_E4M3, PKV_CACHE_INT8 = 0, 1, 2
+PKV_ROPE_NONE, PKV_ROPE_LINEAR, PKV_ROPE_NTK, PKV_ROPE_YARN = 0, 1, 2, 3
 ERRBIT_SLOT_RANGE, ERRBIT_BLOCK_RANGE, ERRBIT_CONTEXT, ERRBIT_CSR_PAGE, ERRBIT_CSR_PHYS, \
     ERRBIT_SPAN, ERRBIT_TIMEOUT, ERRBIT_NO_BLOCKS, ERRBIT_REF_COUNT = \
     0x01, 0x02, 0x04, 0x08, 0x10, 0x20, 0x40, 0x80, 0x100
 _DTYPE = {torch.float32: PKV_F32, torch.float16: PKV_F16, torch.bfloat16: PKV_BF16}
 
 _vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+_f64 = ctypes.c_double
 _SIGS = {
     "pkv_last_error_string": ([], ctypes.c_char_p),
     "pkv_version": ([], ctypes.c_char_p),
@@ -90,6 +92,16 @@ _SIGS = {
     "pkv_grow_block_tables": ([_vp, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _i64, _vp, _sz, _vp, _vp],
                               ctypes.c_int),
     "pkv_shrink_block_tables": ([_vp, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp], ctypes.c_int),
+    "pkv_store_kvcache_int4": ([_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, ctypes.c_int,
+                                _vp, _vp], ctypes.c_int),
+    "pkv_load_kvcache_int4": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, ctypes.c_int, _vp, _vp],
+                              ctypes.c_int),
+    "pkv_rope_frequencies": ([_i32, _f64, ctypes.c_int, _f64, _f64, _f64, _f64, _vp, _vp], ctypes.c_int),
+    "pkv_rope_turns": ([_vp, _i32, _vp], ctypes.c_int),
+    "pkv_rope_store_kvcache": ([_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i64,
+                                ctypes.c_int, _vp, _vp], ctypes.c_int),
+    "pkv_rope_store_kvcache_int4": ([_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32,
+                                     _i32, _i32, _i32, _i32, ctypes.c_int, _vp, _vp], ctypes.c_int),
     "pkv_selftest_wait_timeout": ([_vp, ctypes.c_uint32, _vp], ctypes.c_int),
     "pkv_allocator_create": ([_i32, _i32, _vp], ctypes.c_int),
     "pkv_allocator_destroy": ([_vp], None),
@@ -111,6 +123,12 @@ class _ScoreMod(ctypes.Structure):
     """pkv_score_mod"""
 
     _fields_ = [("softcap", _f32), ("alibi_slopes", _vp), ("key_starts", _vp), ("prefix_lens", _vp)]
+
+
+class _Rope(ctypes.Structure):
+    """pkv_rope"""
+
+    _fields_ = [("turns", _vp), ("amplitude", _f64), ("rotary_dim", _i32), ("interleaved", _i32)]
 
 
 class PkvError(RuntimeError):
@@ -726,6 +744,158 @@ def pkv_paged_attention_decode_append_int8(q, key, value, k_cache, v_cache, k_sc
     """One decode step over int8 code caches (see pkv_paged_attention_decode_append_fp8)."""
     return _attention_codes("int8", q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
                             max_context_len, out, workspace, err_flag, stream, key, value)
+
+
+# ----------------------------------------------------------------------------- rotary positions, 4-bit caches
+class RopeFrequencies:
+    """What a model's rotary positions are computed from: `turns`, int64 [rotary_dim / 2] on
+    the device (turns per position, 64-bit fixed point), and `amplitude`."""
+
+    def __init__(self, turns, amplitude: float = 1.0):
+        _want(turns, torch.int64, "turns")
+        if turns.dim() != 1:
+            raise ValueError("turns must be [rotary_dim / 2]")
+        self.turns, self.amplitude, self.rotary_dim = turns, float(amplitude), 2 * turns.numel()
+
+    def inverse(self):
+        """Frequencies that turn back."""
+        return RopeFrequencies(-self.turns, 1 / self.amplitude)
+
+
+_ROPE_SCALING = {None: PKV_ROPE_NONE, "linear": PKV_ROPE_LINEAR, "ntk": PKV_ROPE_NTK, "yarn": PKV_ROPE_YARN}
+
+
+def pkv_rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling=None, factor: float = 1.0, original_len=0,
+                         beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda") -> RopeFrequencies:
+    """Frequencies base^(-2 i / rotary_dim); `scaling` "linear", "ntk" or "yarn" stretches them
+    for contexts `factor` times as long (yarn: as `original_len`)."""
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {list(_ROPE_SCALING)}")
+    turns, amplitude = torch.empty(max(rotary_dim, 0) // 2, dtype=torch.int64), ctypes.c_double()
+    _check(_lib.pkv_rope_frequencies(rotary_dim, base, _ROPE_SCALING[scaling], factor, original_len, beta_fast, beta_slow,
+                                     _ptr(turns), ctypes.byref(amplitude)))
+    return RopeFrequencies(turns.to(device), amplitude.value)
+
+
+def pkv_rope_turns(inv_freq, *, amplitude: float = 1.0, device="cuda") -> RopeFrequencies:
+    """Frequencies given as radians per position (a sequence or a tensor, [rotary_dim / 2])."""
+    f = torch.as_tensor(inv_freq, dtype=torch.float64).detach().cpu().contiguous()
+    turns = torch.empty(f.shape, dtype=torch.int64)
+    _check(_lib.pkv_rope_turns(_ptr(f), f.numel(), _ptr(turns)))
+    return RopeFrequencies(turns.to(device), amplitude)
+
+
+def _heads(x, dtype, dev_index, name):
+    """A [tokens, heads, head_dim] tensor whose heads and dims are contiguous: elements between tokens."""
+    if x.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.get_device() != dev_index:
+        raise ValueError("all tensors must be on one CUDA device")
+    n, h, d = x.shape
+    s = x.stride()
+    if n and h and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s[0] if n > 1 else h * d
+
+
+def _int4_cache(k_cache, v_cache, k_scale, v_scale):
+    """(num_blocks, Hkv, block_size, d) of 4-bit caches, checked."""
+    shape = k_cache.shape
+    if k_cache.dtype is not torch.uint8 or v_cache.dtype is not torch.uint8:
+        raise TypeError("k_cache and v_cache must be torch.uint8 (two codes a byte)")
+    if k_scale.dtype is not torch.float16 or v_scale.dtype is not torch.float16:
+        raise TypeError("k_scale and v_scale must be torch.float16")
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache, v_cache: [num_blocks, Hkv, bs, head_dim / 2]")
+    if k_scale.shape != (*shape[:3], shape[3] // 16) or v_scale.shape != k_scale.shape:
+        raise ValueError("k_scale, v_scale: [num_blocks, Hkv, bs, head_dim / 32]")
+    return shape[0], shape[1], shape[2], 2 * shape[3]
+
+
+def _rope_store(fn, geometry, tail, q, key, value, positions, rope, caches, slot_mapping, interleaved, out, err_flag, stream):
+    """The marshalling of the store calls; q and rope may be absent.  `geometry` is (num_blocks, Hkv, bs, d)."""
+    dev = _device_of(*caches, slot_mapping, positions, None if rope is None else rope.turns, out, err_flag)
+    _, H, _, d = geometry
+    n, dtype, index = slot_mapping.numel(), key.dtype, dev.index
+    if dtype not in _DTYPE:
+        raise TypeError("key and value must be float32/float16/bfloat16")
+    if slot_mapping.dtype is not torch.int32:
+        raise TypeError("slot_mapping must be torch.int32")
+    if key.shape != (n, H, d) or value.shape != (n, H, d):
+        raise ValueError(f"key/value must be [{n}, {H}, {d}]")
+    ks, vs = _heads(key, dtype, index, "key"), _heads(value, dtype, index, "value")
+    if q is None:
+        front = (key.data_ptr(), ks, value.data_ptr(), vs)
+    else:
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != n or shape[2] != d:
+            raise ValueError(f"q must be [{n}, Hq, {d}]")
+        qs = _heads(q, dtype, index, "q")
+        if positions.dtype is not torch.int32 or positions.numel() != n:
+            raise ValueError(f"positions: {n} entries of torch.int32")
+        if out is None:
+            out = _empty(shape, dtype, dev, stream)
+        elif out.shape != shape or out.dtype is not dtype:
+            raise ValueError("out must have the shape and type of q")
+        c = ctypes.byref(_Rope(rope.turns.data_ptr(), rope.amplitude, rope.rotary_dim, 1 if interleaved else 0))
+        front = (out.data_ptr(), q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs, positions.data_ptr(), c)
+        tail = (shape[1], *tail)
+    _call(dev, fn, *front, *_addrs(*caches), slot_mapping.data_ptr(), n, *tail, _DTYPE[dtype], _flag(err_flag),
+          _raw_stream(dev, stream))
+    return out
+
+
+def pkv_rope_store_kvcache(q, key, value, positions, rope: RopeFrequencies, k_cache, v_cache, slot_mapping, *,
+                           interleaved: bool = False, out=None, err_flag=None, stream=None):
+    """Rotates q and key by their positions: the queries are returned (into `out`, which may be
+    q itself), row slot_mapping[i] of the caches receives the rotated key[i] and value[i] (slot
+    -1 skipped).  q, key and value may be parts of one projection's output."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("caches must be [num_blocks, block_size, num_kv_heads, head_dim]")
+    if k_cache.dtype is not key.dtype or v_cache.dtype is not key.dtype:
+        raise TypeError("key, value and caches must share one type")
+    nb, bs, H, d = shape
+    return _rope_store(_lib.pkv_rope_store_kvcache, (nb, H, bs, d), (H, d, nb * bs), q, key, value, positions, rope,
+                       (k_cache, v_cache), slot_mapping, interleaved, out, err_flag, stream)
+
+
+def pkv_rope_store_kvcache_int4(q, key, value, positions, rope: RopeFrequencies, k_cache, v_cache, k_scale, v_scale,
+                                slot_mapping, *, interleaved: bool = False, out=None, err_flag=None, stream=None):
+    """pkv_rope_store_kvcache into 4-bit caches (uint8 [num_blocks, Hkv, bs, head_dim / 2] with
+    float16 scales [num_blocks, Hkv, bs, head_dim / 32])."""
+    geometry = nb, H, bs, d = _int4_cache(k_cache, v_cache, k_scale, v_scale)
+    return _rope_store(_lib.pkv_rope_store_kvcache_int4, geometry, (H, d, bs, nb), q, key, value, positions, rope,
+                       (k_cache, v_cache, k_scale, v_scale), slot_mapping, interleaved, out, err_flag, stream)
+
+
+def pkv_store_kvcache_int4(key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping, *, err_flag=None, stream=None):
+    """Row slot_mapping[i] of the 4-bit caches <- key[i] / value[i], each 32 dims under their own
+    scale (in place; slot -1 skipped)."""
+    geometry = nb, H, bs, d = _int4_cache(k_cache, v_cache, k_scale, v_scale)
+    _rope_store(_lib.pkv_store_kvcache_int4, geometry, (H, d, bs, nb), None, key, value, None, None,
+                (k_cache, v_cache, k_scale, v_scale), slot_mapping, False, None, err_flag, stream)
+
+
+def pkv_load_kvcache_int4(k_cache, v_cache, k_scale, v_scale, slot_mapping, dtype=torch.float16, *, out=None, err_flag=None,
+                          stream=None):
+    """(key, value) [num_tokens, Hkv, head_dim] of `dtype`: the rows slot_mapping of the 4-bit
+    caches read back (slot -1: zeros)."""
+    nb, H, bs, d = _int4_cache(k_cache, v_cache, k_scale, v_scale)
+    if dtype not in _DTYPE:
+        raise TypeError("dtype must be float32/float16/bfloat16")
+    if slot_mapping.dtype is not torch.int32:
+        raise TypeError("slot_mapping must be torch.int32")
+    n = slot_mapping.numel()
+    key, value = out if out is not None else (None, None)
+    dev = _device_of(k_cache, v_cache, k_scale, v_scale, slot_mapping, key, value, err_flag)
+    if out is None:
+        key, value = _empty((n, H, d), dtype, dev, stream), _empty((n, H, d), dtype, dev, stream)
+    elif not (key.shape == value.shape == (n, H, d) and key.dtype == value.dtype == dtype):
+        raise ValueError(f"out must be two tensors [{n}, {H}, {d}] of dtype")
+    _call(dev, _lib.pkv_load_kvcache_int4, key.data_ptr(), value.data_ptr(), *_addrs(k_cache, v_cache, k_scale, v_scale),
+          slot_mapping.data_ptr(), n, H, d, bs, nb, _DTYPE[dtype], _flag(err_flag), _raw_stream(dev, stream))
+    return key, value
 
 
 # ----------------------------------------------------------------------------- failure detection
