@@ -778,6 +778,30 @@ PKV_API pkv_status pkv_rope_store_kvcache_int4(void *q_out, const void *q, int64
                                                int32_t *err_flag, void *stream);
 
 /*
+ * pkv_paged_attention_decode_int4 -- "Step 2" over 4-bit caches, with score rules (`mod`, may
+ * be NULL; key_starts [num_seqs]): pkv_paged_attention_decode of the values that the codes
+ * stand for.  fp16 or bf16; q enters its product in f16 under a power of two per head, K and V
+ * as what is stored, exactly (V as float16(scale * code): exact for the scales that the store
+ * writes); P is rounded to f16 once; f32 sums.
+ *   caches, scales   16-byte aligned, as are q and out
+ *   workspace        pkv_paged_attention_decode_int4_workspace_size bytes, 256-byte aligned,
+ *                    needed during the call only; calls that may overlap need one each
+ *   other arguments, zero rows and device errors as in pkv_paged_attention_decode_mod.
+ * head_dim 64, 128 or 256, block_size a multiple of 16, any num_q_heads / num_kv_heads (more
+ * than 8 read the cache once for every 8 query heads); others return PKV_ERR_UNSUPPORTED.  Of
+ * a block that is partly seen, rows that are not seen may hold anything, codes and scales.
+ * More than 512 sequences run as consecutive launches over groups of at most 512.
+ */
+PKV_API size_t pkv_paged_attention_decode_int4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                                              int32_t head_dim);
+PKV_API pkv_status pkv_paged_attention_decode_int4(
+    void *out, const void *q, const void *k_cache, const void *v_cache, const uint16_t *k_scale, const uint16_t *v_scale,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+    int32_t max_context_len, float scale, const pkv_score_mod *mod, pkv_dtype dtype, void *workspace,
+    size_t workspace_bytes, int32_t *err_flag, void *stream);
+
+/*
  * Host block allocator -- which physical block of the pool each sequence
  * owns ("Paged KV Cache - AI infra interview lesson": Walk the Shapes First;
  * Append slots during decode; Separate allocation, sharing and release).

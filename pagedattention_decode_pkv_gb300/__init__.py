@@ -102,6 +102,9 @@ _SIGS = {
                                 ctypes.c_int, _vp, _vp], ctypes.c_int),
     "pkv_rope_store_kvcache_int4": ([_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32,
                                      _i32, _i32, _i32, _i32, ctypes.c_int, _vp, _vp], ctypes.c_int),
+    "pkv_paged_attention_decode_int4_workspace_size": ([_i32] * 4, _sz),
+    "pkv_paged_attention_decode_int4": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                         _i32, _f32, _vp, ctypes.c_int, _vp, _sz, _vp, _vp], ctypes.c_int),
     "pkv_selftest_wait_timeout": ([_vp, ctypes.c_uint32, _vp], ctypes.c_int),
     "pkv_allocator_create": ([_i32, _i32, _vp], ctypes.c_int),
     "pkv_allocator_destroy": ([_vp], None),
@@ -896,6 +899,41 @@ def pkv_load_kvcache_int4(k_cache, v_cache, k_scale, v_scale, slot_mapping, dtyp
     _call(dev, _lib.pkv_load_kvcache_int4, key.data_ptr(), value.data_ptr(), *_addrs(k_cache, v_cache, k_scale, v_scale),
           slot_mapping.data_ptr(), n, H, d, bs, nb, _DTYPE[dtype], _flag(err_flag), _raw_stream(dev, stream))
     return key, value
+
+
+def pkv_paged_attention_decode_int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim) -> int:
+    return int(_lib.pkv_paged_attention_decode_int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim))
+
+
+def pkv_paged_attention_decode_int4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale: float,
+                                    max_context_len: int, *, softcap: float = 0.0, alibi_slopes=None, key_starts=None,
+                                    out=None, workspace=None, err_flag=None, stream=None):
+    """Decode attention over 4-bit caches (as pkv_store_kvcache_int4 writes them), with the score
+    rules of pkv_paged_attention_decode_mod."""
+    nb, Hkv, bs, d = _int4_cache(k_cache, v_cache, k_scale, v_scale)
+    dev = _device_of(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, alibi_slopes, key_starts, out,
+                     workspace, err_flag)
+    dtype, shape, tables = q.dtype, q.shape, block_tables.shape
+    if dtype not in _DTYPE:
+        raise TypeError("q must be float16/bfloat16")
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError(f"q must be [num_seqs, Hq, {d}]")
+    B, Hq = shape[0], shape[1]
+    _want_i32(block_tables=block_tables, context_lens=context_lens)
+    if context_lens.numel() != B or len(tables) != 2 or tables[0] != B:
+        raise ValueError("inconsistent shapes")
+    mod = _score_mod(softcap, alibi_slopes, key_starts, None, Hq, B, B)
+    if out is None:
+        out = _empty(shape, dtype, dev, stream)
+    elif out.shape != shape or out.dtype is not dtype:
+        raise ValueError("out must have the shape and type of q")
+    if workspace is None:
+        workspace = _empty(_lib.pkv_paged_attention_decode_int4_workspace_size(B, Hq, Hkv, d), torch.uint8, dev, stream)
+    _call(dev, _lib.pkv_paged_attention_decode_int4, *_addrs(out, q, k_cache, v_cache, k_scale, v_scale),
+          block_tables.data_ptr(), tables[1], context_lens.data_ptr(), B, Hq, Hkv, d, bs, nb, max_context_len, scale, mod,
+          _DTYPE[dtype], workspace.data_ptr(), workspace.numel() * workspace.element_size(), _flag(err_flag),
+          _raw_stream(dev, stream))
+    return out
 
 
 # ----------------------------------------------------------------------------- failure detection

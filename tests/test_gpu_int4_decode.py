@@ -1,0 +1,177 @@
+"""Decode attention over the 4-bit cache, against the definition in binary64 over the values
+that the codes stand for.
+
+Tolerance: score_reference.py's, with P in float16, and a larger score error.  K's codes enter
+their products as 1024 + u and 1024 + 16 u (under q / 16), their offset taken back by the start
+of the f32 accumulator.  A group of 32 dims is two instructions; each may cut its sum to 2^-22
+of its largest term or partial sum, at most 1200 sum |q| over the group: together 2 x 1200 x
+2^-22 < 2^-10 sum |q|, in code steps.  With scales up to s the score is off by at most
+scale s 2^-10 sum |q| more.
+"""
+import pytest
+import torch
+
+import int4_reference as ref
+import score_reference as sr
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+CTX = [1, 15, 16, 17, 31, 32, 33, 0, 63, 64, 65, 100, 255, 256, 300, 511, 700, 1025]
+
+
+def batch(Hq, Hkv, d, bs, ctx, dtype, seed, spare=2, hole=None):
+    """(q, caches, tables): a permuted pool whose unused rows hold NaN scales."""
+    g = torch.Generator().manual_seed(seed)
+    used = [sr.cdiv(c, bs) for c in ctx]
+    nb = sum(used) + spare
+    perm = torch.randperm(nb, generator=g).to(torch.int32)
+    x = torch.randn(2, nb, Hkv, bs, d, generator=g).double() * torch.exp(0.5 * torch.randn(Hkv, 1, d, generator=g)).double()
+    s = ref.scales(x)
+    codes = ref.pack(ref.codes(x, s))
+    width = max(max(used), 1) + 1
+    tables = torch.full((len(ctx), width), -1, dtype=torch.int32)
+    seen = torch.zeros(nb, bs, dtype=torch.bool)
+    at = 0
+    for b, (u, c) in enumerate(zip(used, ctx)):
+        tables[b, :u] = perm[at:at + u]
+        for j in range(u):
+            seen[perm[at + j], :min(bs, c - j * bs)] = True
+        at += u
+    s = torch.where(seen[None, :, None, :, None], s, float("nan"))
+    q = torch.randn(len(ctx), Hq, d, generator=g).to(dtype).cuda()
+    return q, (codes[0].cuda(), codes[1].cuda(), s[0].contiguous().cuda(), s[1].contiguous().cuda()), tables.cuda()
+
+
+def check(got, q, caches, want, scale):
+    s_max = float(torch.nan_to_num(caches[2].float()).abs().max())
+    score = sr.SCORE + scale * s_max * 2.0 ** -10 * q.double().abs().sum(-1).max().item()
+    out, mag, keys = want
+    v_max = 8 * float(torch.nan_to_num(caches[3].float()).abs().max())
+    tol = sr.tolerance(want, got.dtype, F16, v_max) + 2 * (score - sr.SCORE) * mag
+    err = (got.cpu().double() - out).abs()
+    assert torch.isfinite(got).all()
+    assert bool((err <= tol).all()), f"worst error / tolerance {(err / tol).max().item():.3g}, max abs {err.max().item():.3g}"
+
+
+def reference(q, caches, tables, ctx, scale, softcap=0.0, slopes=None, key_starts=None):
+    k, v = ref.token_major(caches[0], caches[2]), ref.token_major(caches[1], caches[3])
+    some = [b for b, c in enumerate(ctx) if c > 0]
+    starts = None if key_starts is None else key_starts[some]
+    parts = sr.prefill(q[some], k, v, tables[some], [ctx[b] - 1 for b in some], [1] * len(some), scale, softcap, slopes, starts)
+    whole = [torch.zeros(len(ctx), *p.shape[1:], dtype=torch.float64) for p in parts]
+    for w, p in zip(whole, parts):
+        w[some] = p
+    return tuple(whole)
+
+
+def rules(name, ctx, Hq):
+    first = torch.tensor([max(-3, c - 70) if i % 5 else c + 3 for i, c in enumerate(ctx)], dtype=torch.int32).cuda()
+    slopes = torch.exp2(-8 * torch.arange(1, Hq + 1) / Hq).float().cuda()
+    return {"plain": {}, "cap": {"softcap": 3.0}, "alibi": {"alibi_slopes": slopes}, "window": {"key_starts": first},
+            "all": {"softcap": 30.0, "alibi_slopes": slopes, "key_starts": first}}[name]
+
+
+@pytest.mark.parametrize("rule", ["plain", "cap", "alibi", "window", "all"])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("Hq,Hkv,d,bs", [(8, 8, 128, 16), (16, 8, 128, 256), (32, 8, 128, 48), (64, 8, 128, 16), (4, 1, 128, 64),
+                                         (6, 2, 64, 16), (8, 2, 256, 32), (12, 1, 128, 16), (40, 2, 64, 32), (9, 1, 256, 16)])
+def test_decode(pkv, cuda_dev, Hq, Hkv, d, bs, dtype, rule):
+    q, caches, tables = batch(Hq, Hkv, d, bs, CTX, dtype, Hq + d + bs)
+    kw = rules(rule, CTX, Hq)
+    scale = d ** -0.5
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+    out = torch.full_like(q, float("nan"))
+    ctx = torch.tensor(CTX, dtype=torch.int32, device=cuda_dev)
+    pkv.pkv_paged_attention_decode_int4(q, *caches, tables, ctx, scale, max(CTX), out=out, err_flag=err, **kw)
+    assert int(err) == 0
+    check(out, q, caches, reference(q, caches, tables, CTX, scale, kw.get("softcap", 0.0), kw.get("alibi_slopes"),
+                                    kw.get("key_starts")), scale)
+
+
+@pytest.mark.parametrize("ctx", [[1], [40000], [3] * 600, [17000, 1, 0, 9]], ids=["one", "long", "many", "mixed"])
+def test_lengths(pkv, cuda_dev, ctx):
+    q, caches, tables = batch(8, 2, 128, 16, ctx, BF16, 5)
+    out = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, torch.tensor(ctx, dtype=torch.int32).cuda(), 128 ** -0.5, max(ctx))
+    check(out, q, caches, reference(q, caches, tables, ctx, 128 ** -0.5), 128 ** -0.5)
+
+
+def test_errors_and_holes(pkv, cuda_dev):
+    """Bad lengths give zero rows, missing blocks count as masked; both set their bits."""
+    ctx = [100, 100, 100, 64]
+    q, caches, tables = batch(4, 2, 128, 16, ctx, F16, 6)
+    want = reference(q, caches, tables, ctx, 0.1)
+    given = torch.tensor([100, -4, 300, 64], dtype=torch.int32).cuda()
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+    out = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, given, 0.1, 128, err_flag=err)
+    assert int(err) == pkv.ERRBIT_CONTEXT and not bool(out[1:3].any())
+    check(out[[0, 3]], q[[0, 3]], caches, tuple(w[[0, 3]] for w in want), 0.1)
+    # blocks 0 and 2 of sequence 0 missing: the rest alone, blocks in front of the window never looked at
+    holes = tables.clone()
+    holes[0, 0], holes[0, 2] = -1, 10 ** 6
+    given = torch.tensor(ctx, dtype=torch.int32).cuda()
+    err.zero_()
+    out = pkv.pkv_paged_attention_decode_int4(q, *caches, holes, given, 0.1, 128, err_flag=err)
+    assert int(err) == pkv.ERRBIT_BLOCK_RANGE
+    k, v = (ref.token_major(caches[i], caches[2 + i]) for i in (0, 1))
+    rows = [torch.cat([x[tables[0, j].item()] for j in (1, 3, 4, 5, 6)])[:68] for x in (k, v)]
+    pos = torch.tensor([67])
+    alone = sr.attention(q[:1].cpu(), rows[0], rows[1], pos, torch.tensor([0]), torch.tensor([68]), 0.1)
+    check(out[:1], q[:1], caches, alone, 0.1)
+    err.zero_()
+    first = torch.tensor([48, 0, 0, 0], dtype=torch.int32).cuda()
+    pkv.pkv_paged_attention_decode_int4(q, *caches, holes, given, 0.1, 128, key_starts=first, err_flag=err)
+    assert int(err) == 0
+
+
+@pytest.mark.parametrize("gain", [2.0 ** -30, 1e-3, 1.0, 3e4])
+def test_magnitudes(pkv, cuda_dev, gain):
+    """Queries far from unit size: the scores, not the queries, decide (the scale makes up for it)."""
+    ctx = [200, 33]
+    q, caches, tables = batch(8, 2, 128, 16, ctx, BF16, 8)
+    q = (q.float() * gain).to(BF16)
+    scale = 128 ** -0.5 / gain
+    out = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, torch.tensor(ctx, dtype=torch.int32).cuda(), scale, 200)
+    check(out, q, caches, reference(q, caches, tables, ctx, scale), scale)
+
+
+def test_empty_batch(pkv, cuda_dev):
+    q, caches, tables = batch(8, 2, 128, 16, [5], BF16, 8)
+    out = pkv.pkv_paged_attention_decode_int4(q[:0], *caches, tables[:0], torch.empty(0, dtype=torch.int32, device=cuda_dev), 0.1, 5)
+    assert out.shape == (0, 8, 128)
+
+
+def test_captured_and_on_another_stream(pkv, cuda_dev):
+    ctx = [700, 33, 2000]
+    q, caches, tables = batch(16, 4, 128, 16, ctx, BF16, 9)
+    lens = torch.tensor(ctx, dtype=torch.int32).cuda()
+    want = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, lens, 0.09, 2000)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    got = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, lens, 0.09, 2000, stream=other)
+    other.synchronize()
+    assert torch.equal(got, want)  # pieces are joined in order: the same bits
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, lens, 0.09, 2000)
+    for step in range(2):
+        q.mul_(-1)
+        lens.sub_(step)
+        graph.replay()
+        assert torch.equal(out, pkv.pkv_paged_attention_decode_int4(q, *caches, tables, lens, 0.09, 2000))
+
+
+def test_offsets_past_32_bits(pkv, cuda_dev):
+    nb, Hkv, bs, d = 20000, 8, 256, 128
+    kc = torch.zeros(nb, Hkv, bs, d // 2, dtype=torch.uint8, device=cuda_dev)
+    ks = torch.zeros(nb, Hkv, bs, d // 32, dtype=F16, device=cuda_dev)
+    caches = (kc, kc.clone(), ks, ks.clone())
+    ctx, ids = 300, [nb - 1, 12345]
+    g = torch.Generator().manual_seed(3)
+    key, value = (torch.randn(ctx, Hkv, d, generator=g).to(BF16).cuda() for _ in range(2))
+    slots = torch.tensor([ids[p // bs] * bs + p % bs for p in range(ctx)], dtype=torch.int32).cuda()
+    pkv.pkv_store_kvcache_int4(key, value, *caches, slots)
+    q = torch.randn(1, 32, d, generator=g).to(BF16).cuda()
+    tables = torch.tensor([ids], dtype=torch.int32).cuda()
+    out = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, torch.tensor([ctx], dtype=torch.int32).cuda(), d ** -0.5, ctx)
+    near = tuple(c[ids].contiguous() for c in caches)
+    check(out, q, near, reference(q, near, torch.tensor([[0, 1]]), [ctx], d ** -0.5), d ** -0.5)
