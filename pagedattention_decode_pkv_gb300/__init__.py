@@ -105,6 +105,8 @@ _SIGS = {
     "pkv_paged_attention_decode_int4_workspace_size": ([_i32] * 4, _sz),
     "pkv_paged_attention_decode_int4": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
                                          _i32, _f32, _vp, ctypes.c_int, _vp, _sz, _vp, _vp], ctypes.c_int),
+    "pkv_paged_attention_prefill_int4": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                                          _i32, _i32, _f32, _vp, ctypes.c_int, _vp, _sz, _vp, _vp], ctypes.c_int),
     "pkv_selftest_wait_timeout": ([_vp, ctypes.c_uint32, _vp], ctypes.c_int),
     "pkv_allocator_create": ([_i32, _i32, _vp], ctypes.c_int),
     "pkv_allocator_destroy": ([_vp], None),
@@ -933,6 +935,38 @@ def pkv_paged_attention_decode_int4(q, k_cache, v_cache, k_scale, v_scale, block
           block_tables.data_ptr(), tables[1], context_lens.data_ptr(), B, Hq, Hkv, d, bs, nb, max_context_len, scale, mod,
           _DTYPE[dtype], workspace.data_ptr(), workspace.numel() * workspace.element_size(), _flag(err_flag),
           _raw_stream(dev, stream))
+    return out
+
+
+def pkv_paged_attention_prefill_int4(q, k_cache, v_cache, k_scale, v_scale, block_tables, starts, cu_q, scale: float,
+                                     max_q_len: int, *, softcap: float = 0.0, alibi_slopes=None, key_starts=None,
+                                     prefix_lens=None, out=None, workspace=None, err_flag=None, stream=None):
+    """Prefill attention over 4-bit caches (as pkv_store_kvcache_int4 writes them), with the score
+    rules and workspace of pkv_paged_attention_prefill_mod."""
+    nb, Hkv, bs, d = _int4_cache(k_cache, v_cache, k_scale, v_scale)
+    dev = _device_of(q, k_cache, v_cache, k_scale, v_scale, block_tables, starts, cu_q, alibi_slopes, key_starts,
+                     prefix_lens, out, workspace, err_flag)
+    dtype, shape, tables, B = q.dtype, q.shape, block_tables.shape, starts.numel()
+    if dtype not in _DTYPE:
+        raise TypeError("q must be float16/bfloat16")
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError(f"q must be [rows, Hq, {d}]")
+    _want_i32(block_tables=block_tables, starts=starts, cu_q=cu_q)
+    if cu_q.numel() != B + 1 or len(tables) != 2 or tables[0] != B:
+        raise ValueError("inconsistent shapes")
+    rows, Hq = shape[0], shape[1]
+    mod = _score_mod(softcap, alibi_slopes, key_starts, prefix_lens, Hq, rows, B)
+    if out is None:
+        out = _empty(shape, dtype, dev, stream)
+    elif out.shape != shape or out.dtype is not dtype:
+        raise ValueError("out must have the shape and type of q")
+    ws = _lib.pkv_paged_attention_prefill_mod_workspace_size(B, Hq, Hkv, d, bs, max_q_len, tables[1])
+    if ws and workspace is None:
+        workspace = _empty(ws, torch.uint8, dev, stream)
+    _call(dev, _lib.pkv_paged_attention_prefill_int4, *_addrs(out, q, k_cache, v_cache, k_scale, v_scale),
+          block_tables.data_ptr(), tables[1], starts.data_ptr(), cu_q.data_ptr(), B, max_q_len, Hq, Hkv, d, bs, nb, scale,
+          mod, _DTYPE[dtype], workspace.data_ptr() if ws else None,
+          workspace.numel() * workspace.element_size() if ws else 0, _flag(err_flag), _raw_stream(dev, stream))
     return out
 
 

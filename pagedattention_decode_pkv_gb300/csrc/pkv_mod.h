@@ -19,6 +19,7 @@ struct PrefillCall {
     void *out;
     const void *q, *k_cache, *v_cache;
     const float *k_scale, *v_scale;  // 8-bit caches
+    const uint16_t *k_scale4, *v_scale4;  // 4-bit caches, f16 bits
     const int32_t *block_tables;
     int32_t max_blocks;
     const int32_t *starts, *cu_q;
@@ -36,5 +37,9 @@ struct PrefillCall {
 pkv_status prefill_mod_16bit(const PrefillCall &c);
 pkv_status prefill_mod_e4m3(const PrefillCall &c);
 pkv_status prefill_mod_int8(const PrefillCall &c);
+pkv_status prefill_mod_int4(const PrefillCall &c);
+
+// Checks the call (whose plan and workspace are still to be set) and enqueues it; `format` is a CacheCode.
+pkv_status prefill_mod_run(PrefillCall c, int format, int32_t head_dim, void *workspace, size_t workspace_bytes);
 
 }  // namespace pkv

@@ -1,5 +1,5 @@
-// Entry points of the score-rule and 8-bit prefill, and its kernels over 16-bit
-// caches (pkv_prefill_mod.cuh has the method).
+// Entry points of the score-rule and 8-bit prefill, the checks of every call, and the
+// kernels over 16-bit caches (pkv_prefill_mod.cuh has the method).
 #include "pkv_prefill_mod.cuh"
 
 #include <cmath>
@@ -60,44 +60,59 @@ extern "C" size_t pkv_paged_attention_prefill_mod_workspace_size(int32_t num_seq
     return prefill_plan(num_seqs, num_q_heads, num_kv_heads, max_q_len, max_blocks_per_seq, block_size).ws_bytes;
 }
 
+pkv_status pkv::prefill_mod_run(PrefillCall c, int format, int32_t head_dim, void *workspace, size_t workspace_bytes) {
+    if (dtype_bytes(c.dtype) == 0) return set_error(PKV_ERR_INVALID_ARG, "prefill: unknown dtype %d", (int)c.dtype);
+    if (format != kCode16 && format != kCodeE4M3 && format != kCodeInt8 && format != kCodeInt4)
+        return set_error(PKV_ERR_INVALID_ARG, "prefill: unknown cache format %d", format);
+    if (c.num_seqs < 0 || c.max_q_len < 0 || c.Hq <= 0 || c.Hkv <= 0 || head_dim <= 0 || c.block_size <= 0 ||
+        c.num_blocks < 0 || c.max_blocks < 0)
+        return set_error(PKV_ERR_INVALID_ARG, "prefill: bad sizes");
+    if (c.Hq % c.Hkv)
+        return set_error(PKV_ERR_INVALID_ARG, "prefill: num_q_heads (%d) is not a multiple of num_kv_heads (%d)", c.Hq, c.Hkv);
+    if (static_cast<int64_t>(c.num_blocks) * c.block_size > INT32_MAX)
+        return set_error(PKV_ERR_INVALID_ARG, "prefill: num_blocks * block_size >= 2^31");
+    const float cap = c.mod.softcap;
+    if (!(cap >= 0.f) || cap > 1e30f || (cap > 0.f && cap < 1e-30f))
+        return set_error(PKV_ERR_INVALID_ARG, "prefill: softcap must be 0, or from 1e-30 to 1e30");
+    if (c.num_seqs > 65535 || c.Hkv > 65535)
+        return set_error(PKV_ERR_UNSUPPORTED, "prefill: more than 65535 sequences or KV heads");
+    if (c.num_seqs == 0 || c.max_q_len == 0) return ok();
+    if ((c.dtype != PKV_F16 && c.dtype != PKV_BF16) || !supported_shape(c.Hq, c.Hkv, head_dim, c.block_size))
+        return set_error(PKV_ERR_UNSUPPORTED, "prefill: needs fp16/bf16, head_dim 128, Hq/Hkv in {1, 2, 4, 8} and "
+                                              "block_size a multiple of 16");
+    if (!c.out || !c.q || !c.starts || !c.cu_q || !c.block_tables || !c.k_cache || !c.v_cache || c.num_blocks == 0)
+        return set_error(PKV_ERR_INVALID_ARG, "prefill: NULL pointer or empty pool");
+    if (!aligned(c.k_cache, 16) || !aligned(c.v_cache, 16) || !aligned(c.q, 16) || !aligned(c.out, 16))
+        return set_error(PKV_ERR_UNSUPPORTED, "prefill: pools, q and out must be 16-byte aligned");
+    if ((format == kCodeE4M3 || format == kCodeInt8) &&
+        (!c.k_scale || !c.v_scale || !aligned(c.k_scale, 4) || !aligned(c.v_scale, 4)))
+        return set_error(PKV_ERR_INVALID_ARG, "prefill: scales of an 8-bit cache NULL or not 4-byte aligned");
+    if (format == kCodeInt4) {
+        if (!c.k_scale4 || !c.v_scale4) return set_error(PKV_ERR_INVALID_ARG, "prefill: scales of a 4-bit cache NULL");
+        if (!aligned(c.k_scale4, 16) || !aligned(c.v_scale4, 16))
+            return set_error(PKV_ERR_UNSUPPORTED, "prefill: scales of a 4-bit cache must be 16-byte aligned");
+    }
+    c.plan = prefill_plan(c.num_seqs, c.Hq, c.Hkv, c.max_q_len, c.max_blocks, c.block_size);
+    if (c.plan.ws_bytes > 0 && (!workspace || workspace_bytes < c.plan.ws_bytes || !aligned(workspace, 256)))
+        return set_error(PKV_ERR_WORKSPACE, "prefill: workspace needs %zu bytes (256-byte aligned), got %zu",
+                         c.plan.ws_bytes, workspace_bytes);
+    c.workspace = static_cast<char *>(workspace);
+    const pkv_status st = format == kCodeE4M3   ? prefill_mod_e4m3(c)
+                          : format == kCodeInt8 ? prefill_mod_int8(c)
+                          : format == kCodeInt4 ? prefill_mod_int4(c)
+                                                : prefill_mod_16bit(c);
+    return st == PKV_OK ? ok() : st;
+}
+
 extern "C" pkv_status pkv_paged_attention_prefill_mod(
     void *out, const void *q, const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
     pkv_cache_format format, const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *starts,
     const int32_t *cu_q, int32_t num_seqs, int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
     int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale, const pkv_score_mod *mod, pkv_dtype dtype,
     void *workspace, size_t workspace_bytes, int32_t *err_flag, void *stream) {
-    if (dtype_bytes(dtype) == 0) return set_error(PKV_ERR_INVALID_ARG, "prefill: unknown dtype %d", (int)dtype);
     if (format != PKV_CACHE_DTYPE && format != PKV_CACHE_E4M3 && format != PKV_CACHE_INT8)
         return set_error(PKV_ERR_INVALID_ARG, "prefill: unknown cache format %d", (int)format);
-    if (num_seqs < 0 || max_q_len < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 ||
-        num_blocks < 0 || max_blocks_per_seq < 0)
-        return set_error(PKV_ERR_INVALID_ARG, "prefill: bad sizes");
-    if (num_q_heads % num_kv_heads)
-        return set_error(PKV_ERR_INVALID_ARG, "prefill: num_q_heads (%d) is not a multiple of num_kv_heads (%d)",
-                         num_q_heads, num_kv_heads);
-    if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX)
-        return set_error(PKV_ERR_INVALID_ARG, "prefill: num_blocks * block_size >= 2^31");
-    const pkv_score_mod none{};
-    const pkv_score_mod m = mod ? *mod : none;
-    if (!(m.softcap >= 0.f) || m.softcap > 1e30f || (m.softcap > 0.f && m.softcap < 1e-30f))
-        return set_error(PKV_ERR_INVALID_ARG, "prefill: softcap must be 0, or from 1e-30 to 1e30");
-    if (num_seqs > 65535 || num_kv_heads > 65535)
-        return set_error(PKV_ERR_UNSUPPORTED, "prefill: more than 65535 sequences or KV heads");
-    if (num_seqs == 0 || max_q_len == 0) return ok();
-    if ((dtype != PKV_F16 && dtype != PKV_BF16) || !supported_shape(num_q_heads, num_kv_heads, head_dim, block_size))
-        return set_error(PKV_ERR_UNSUPPORTED, "prefill: needs fp16/bf16, head_dim 128, Hq/Hkv in {1, 2, 4, 8} and "
-                                              "block_size a multiple of 16");
-    if (!out || !q || !starts || !cu_q || !block_tables || !k_cache || !v_cache || num_blocks == 0)
-        return set_error(PKV_ERR_INVALID_ARG, "prefill: NULL pointer or empty pool");
-    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(q, 16) || !aligned(out, 16))
-        return set_error(PKV_ERR_UNSUPPORTED, "prefill: pools, q and out must be 16-byte aligned");
-    if (format != PKV_CACHE_DTYPE && (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4)))
-        return set_error(PKV_ERR_INVALID_ARG, "prefill: scales of an 8-bit cache NULL or not 4-byte aligned");
     PrefillCall c{};
-    c.plan = prefill_plan(num_seqs, num_q_heads, num_kv_heads, max_q_len, max_blocks_per_seq, block_size);
-    if (c.plan.ws_bytes > 0 && (!workspace || workspace_bytes < c.plan.ws_bytes || !aligned(workspace, 256)))
-        return set_error(PKV_ERR_WORKSPACE, "prefill: workspace needs %zu bytes (256-byte aligned), got %zu",
-                         c.plan.ws_bytes, workspace_bytes);
     c.out = out;
     c.q = q;
     c.k_cache = k_cache;
@@ -115,13 +130,9 @@ extern "C" pkv_status pkv_paged_attention_prefill_mod(
     c.block_size = block_size;
     c.num_blocks = num_blocks;
     c.scale = scale;
-    c.mod = m;
+    if (mod) c.mod = *mod;
     c.dtype = dtype;
-    c.workspace = static_cast<char *>(workspace);
     c.err_flag = err_flag;
     c.stream = static_cast<cudaStream_t>(stream);
-    const pkv_status st = format == PKV_CACHE_E4M3   ? prefill_mod_e4m3(c)
-                          : format == PKV_CACHE_INT8 ? prefill_mod_int8(c)
-                                                     : prefill_mod_16bit(c);
-    return st == PKV_OK ? ok() : st;
+    return prefill_mod_run(c, format, head_dim, workspace, workspace_bytes);
 }

@@ -64,6 +64,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "pkv_int4.cuh"
 #include "pkv_internal.h"
 #include "pkv_mod.h"
 #include "pkv_pack.cuh"
@@ -87,7 +88,8 @@ constexpr int kConvWarps = 4;
 constexpr int kHalfKeys = kModKeys / 2;  // keys per step of the softmax and the products
 constexpr int kModTile = 32768;       // a 128 x 128 tile of 16-bit values: two 64-column halves
 constexpr int kModHalf = kModTile / 2;
-constexpr int kModCodeTile = 16384;   // the same tile in codes
+constexpr int kModCodeTile = 16384;   // the same tile in codes (4-bit ones and their scales: 9216 bytes of it)
+constexpr int kModScales4 = kModKeys * 64;  // where a 4-bit tile's scales begin, 8 bytes a key
 constexpr uint64_t kModDeadlineNs = 2000000000ull;
 constexpr float kModRescale = 8.f;    // log2 units a block may exceed the reference maximum by before O is rescaled
 // CAP: no cap, a cap, or a cap that bounds the scores so far that no reference
@@ -147,6 +149,8 @@ struct ModArgs {
     const void *q;
     const int32_t *block_tables, *starts, *cu_q;
     const float *k_scale, *v_scale;
+    const uint8_t *codes[2];    // 4-bit caches: K, V
+    const uint16_t *scales[2];
     const float *slopes;
     const int32_t *key_starts, *prefix_lens;
     int32_t max_blocks, Hq, Hkv, lg_g, bs, num_blocks, box_lg, max_q_len, pairs, nsplit;
@@ -177,7 +181,9 @@ template <typename T, int FMT, int CAP, bool ALIBI>
 __global__ void __launch_bounds__(kModThreads<FMT != kCode16>, 1)
 prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ ModArgs A) {
-    constexpr bool C8 = FMT != kCode16;
+    constexpr bool C8 = FMT != kCode16;    // codes, which converter warps widen
+    constexpr bool C4 = FMT == kCodeInt4;  // with their scales, row by row
+    constexpr bool BS = C8 && !C4;         // a scale per block, kept out of the tiles
     constexpr bool RAW = !CAP && !ALIBI;  // the score's factor goes into the exponent's FMA
     using L = ModLayout<C8>;
     using M16 = typename std::conditional<C8, __half, T>::type;  // operand type of the products
@@ -227,8 +233,10 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         mbar_init(bar(L::kVLand), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        prefetch_tensormap(&tm_k);
-        prefetch_tensormap(&tm_v);
+        if constexpr (!C4) {
+            prefetch_tensormap(&tm_k);
+            prefetch_tensormap(&tm_v);
+        }
     }
     pdl_wait();
     pdl_trigger();
@@ -379,7 +387,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 return -2;
             };
             auto scale_of = [&](const float *scales, int page_id) -> float {
-                if constexpr (!C8) return 1.f;
+                if constexpr (!BS) return 1.f;
                 return page_id >= 0 ? __ldg(scales + static_cast<int64_t>(page_id) * A.Hkv + kh) : 1.f;
             };
             auto wait_bar = [&](int i, uint32_t parity) -> bool {
@@ -431,9 +439,9 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             for (int jj = 0; jj < nb && !timed_out; ++jj) {
                 const int key = (j0 + jj) * kModKeys + 16 * lane;
                 const unsigned miss = __ballot_sync(0xffffffffu, id == -2);
-                const unsigned neg = __ballot_sync(0xffffffffu, C8 && id >= 0 && !(ks >= 0.f));
+                const unsigned neg = __ballot_sync(0xffffffffu, BS && id >= 0 && !(ks >= 0.f));
                 const unsigned chunks = __ballot_sync(0xffffffffu, id >= 0 && (key & (box_rows - 1)) == 0);
-                const uint32_t chunk_bytes = static_cast<uint32_t>(box_rows) * (C8 ? 128 : 256);
+                const uint32_t chunk_bytes = static_cast<uint32_t>(box_rows) * (C4 ? 72 : C8 ? 128 : 256);
                 const bool mine = (chunks >> lane) & 1;
                 const int slot_row = mine ? id * bs + key % bs : 0;
                 int next_id = -1;
@@ -455,7 +463,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                             f->fix = fix;
                             f->neg = neg != 0;
                         }
-                        if (C8 && lane < 8) {
+                        if (BS && lane < 8) {
                             f->ks[lane] = ks;
                             f->vs[lane] = vs;
                             f->lv[lane] = fmaxf(__log2f(vs), -100.f);  // also a scale of 0
@@ -468,8 +476,13 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     __syncwarp();
                     if (mine) {
                         const CUtensorMap *tm = kv ? &tm_v : &tm_k;
-                        const uint32_t dst = sDst + static_cast<uint32_t>(slot) * kSlotBytes + (16 * lane) * 128;
-                        if constexpr (C8) {
+                        const uint32_t dst = sDst + static_cast<uint32_t>(slot) * kSlotBytes + (16 * lane) * (C4 ? 64 : 128);
+                        if constexpr (C4) {
+                            const int64_t row = (static_cast<int64_t>(id) * A.Hkv + kh) * bs + key % bs;
+                            bulk_load(dst, A.codes[kv] + row * 64, box_rows * 64, landed);
+                            bulk_load(sDst + static_cast<uint32_t>(slot) * kSlotBytes + kModScales4 + 16 * lane * 8,
+                                      A.scales[kv] + row * 4, box_rows * 8, landed);
+                        } else if constexpr (C8) {
                             tma_load_3d(dst, tm, 0, slot_row, kh, landed);
                         } else {
                             tma_load_3d(dst, tm, 0, slot_row, 2 * kh, landed);
@@ -598,26 +611,58 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const int miss = f->miss, key0 = (j0 + (item >> 1)) * kModKeys;
                 const uint32_t src = sStage + static_cast<uint32_t>(st) * kModCodeTile;
                 const uint32_t dst = sRing + static_cast<uint32_t>(slot) * kModTile;
-#pragma unroll 2  // more (4: -6 % with int8) costs the other warps their instruction cache
-                for (int i = 0; i < 8; ++i) {
-                    const int rr = row0 + 8 * (i >> 1), c4 = l8 & 3;
-                    const int c = c4 + 4 * (i & 1);
-                    uint32_t x[4];
-                    ld_shared_v4(src + rr * 128 + ((c ^ (rr & 7)) << 4), x);
-                    uint32_t y[8];
+                if constexpr (C4) {
+                    // A lane takes a group: 16 bytes of codes, one scale, four chunks of eight
+                    // dims.  Eight lanes are two rows of four groups (their reads are 128
+                    // consecutive bytes), and groups 2 and 3 write their chunks in the order 2 3 0 1,
+                    // so that the eight writes of a step are in eight different places.
+                    const int c = lane & 3, flip = c & 2;
+                    const uint32_t d0 = dst + (c >> 1) * kModHalf;
+#pragma unroll 2
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = 32 * w + 8 * i + (lane >> 2);
+                        uint32_t x[4], s;
+                        ld_shared_v4(src + rr * 64 + c * 16, x);
+                        asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tmov.b32 %0, {h, h};\n\t}"
+                                     : "=r"(s)
+                                     : "r"(src + kModScales4 + rr * 8 + c * 2)
+                                     : "memory");
+                        bool none = false;
+                        if (fix) {
+                            const int key = key0 + rr;
+                            none = key < key_lo || key >= key_hi || (miss >> (rr >> 4) & 1);
+                        }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) codes4_to_f16x4<FMT, false>(x[e], y[2 * e], y[2 * e + 1]);
-                    if (fix) {
-                        const int key = key0 + rr;
-                        if (key < key_lo || key >= key_hi || (miss >> (rr >> 4) & 1)) {
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t y[4];
+                            int4_widen(flip ? x[e ^ 2] : x[e], y);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) y[e] = 0;
+                            for (int k = 0; k < 4; ++k) y[k] = none ? 0u : mul_f16x2(y[k], s);
+                            st_shared_v4(d0 + rr * 128 + (((4 * (c & 1) + (e ^ flip)) ^ (rr & 7)) << 4), y[0], y[1], y[2], y[3]);
                         }
                     }
-                    const uint32_t d = dst + (i & 1) * kModHalf + rr * 128;
-                    const uint32_t d0 = d + (((2 * c4 + hi) ^ (rr & 7)) << 4), d1 = d + (((2 * c4 + (hi ^ 1)) ^ (rr & 7)) << 4);
-                    st_shared_v4(d0, hi ? y[4] : y[0], hi ? y[5] : y[1], hi ? y[6] : y[2], hi ? y[7] : y[3]);
-                    st_shared_v4(d1, hi ? y[0] : y[4], hi ? y[1] : y[5], hi ? y[2] : y[6], hi ? y[3] : y[7]);
+                } else {
+#pragma unroll 2  // more (4: -6 % with int8) costs the other warps their instruction cache
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = row0 + 8 * (i >> 1), c4 = l8 & 3;
+                        const int c = c4 + 4 * (i & 1);
+                        uint32_t x[4];
+                        ld_shared_v4(src + rr * 128 + ((c ^ (rr & 7)) << 4), x);
+                        uint32_t y[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) codes4_to_f16x4<FMT, false>(x[e], y[2 * e], y[2 * e + 1]);
+                        if (fix) {
+                            const int key = key0 + rr;
+                            if (key < key_lo || key >= key_hi || (miss >> (rr >> 4) & 1)) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) y[e] = 0;
+                            }
+                        }
+                        const uint32_t d = dst + (i & 1) * kModHalf + rr * 128;
+                        const uint32_t d0 = d + (((2 * c4 + hi) ^ (rr & 7)) << 4), d1 = d + (((2 * c4 + (hi ^ 1)) ^ (rr & 7)) << 4);
+                        st_shared_v4(d0, hi ? y[4] : y[0], hi ? y[5] : y[1], hi ? y[6] : y[2], hi ? y[7] : y[3]);
+                        st_shared_v4(d1, hi ? y[0] : y[4], hi ? y[1] : y[5], hi ? y[2] : y[6], hi ? y[3] : y[7]);
+                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -728,7 +773,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 float top = 0.f;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const uint64_t sa = splat2(C8 ? A.sa * f->ks[g0 + g] * rq : A.sa);
+                    const uint64_t sa = splat2(BS ? A.sa * f->ks[g0 + g] * rq : C4 ? A.sa * rq : A.sa);
 #pragma unroll
                     for (int k = 16 * g; k < 16 * g + 16; k += 2) {
                         const uint64_t u = mul2(pack2(x[k], x[k + 1]), sa), u2 = mul2(u, u);
@@ -745,7 +790,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         tmem_ld32(scol + c0, v);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float su = C8 ? A.su * f->ks[g0 + (c0 + i) / 16] * rq : A.su;
+                            const float su = BS ? A.su * f->ks[g0 + (c0 + i) / 16] * rq : C4 ? A.su * rq : A.su;
                             const float e = __uint_as_float(v[i]) * su;  // 2 log2 e score / cap
                             const float big = fmaf(fast_rcp(1.f + fast_exp2(e)), -2.f * A.capl2, A.capl2);
                             // each score by its own size: a row's bits are its own
@@ -766,7 +811,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const uint64_t on = splat2(-2.f * by);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const uint64_t sl = splat2(CAP ? 1.f : C8 ? A.sl * f->ks[g0 + g] * rq : A.sl);
+                    const uint64_t sl = splat2(CAP ? 1.f : BS ? A.sl * f->ks[g0 + g] * rq : C4 ? A.sl * rq : A.sl);
                     uint64_t bias = pack2(by * (c - 16 * g), by * (c - 16 * g - 1));  // two keys on by one addition
 #pragma unroll
                     for (int k = 16 * g; k < 16 * g + 16; k += 2) {
@@ -781,7 +826,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
             }
             // 2. masked keys
-            if constexpr (RAW && C8) {
+            if constexpr (RAW && BS) {
                 if (!open || f->neg) {
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
@@ -811,7 +856,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             bool moved = false;
             if constexpr (kFree) {
                 mx = 0.f;
-            } else if constexpr (C8) {
+            } else if constexpr (BS) {
                 mx = -INFINITY;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
@@ -827,7 +872,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll
                 for (int k = 0; k < kHalfKeys; k += 2) m4[(k >> 1) & 3] = max3f(m4[(k >> 1) & 3], x[k], x[k + 1]);
                 mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                if (RAW) mx *= A.sl;
+                if (RAW) mx *= C4 ? A.sl * rq : A.sl;
             }
             if (!kFree && mx > m_ref + kModRescale) {  // also the row's first visible key (m_ref = -inf)
                 if (m_ref != -INFINITY) {
@@ -863,8 +908,8 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             uint32_t pk[32];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const uint64_t mul = splat2(RAW ? (C8 ? (scaled ? 1.f : A.sl * f->ks[g0 + g] * rq) : A.sl) : 1.f);
-                const uint64_t sv = splat2(C8 ? f->vs[g0 + g] : 1.f);
+                const uint64_t mul = splat2(RAW ? (BS ? (scaled ? 1.f : A.sl * f->ks[g0 + g] * rq) : C4 ? A.sl * rq : A.sl) : 1.f);
+                const uint64_t sv = splat2(BS ? f->vs[g0 + g] : 1.f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int k = 16 * g + 2 * i, o = 8 * g + i;
@@ -873,7 +918,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     unpack2(RAW ? fma2(s, mul, nb2) : kFree ? s : add2(s, nb2), e0, e1);
                     e0 = fast_exp2(e0);
                     e1 = fast_exp2(e1);
-                    if constexpr (C8) {
+                    if constexpr (BS) {
                         const uint64_t p = pack2(e0, e1);
                         l2[i & 1] = add2(l2[i & 1], p);
                         unpack2(mul2(p, sv), e0, e1);
@@ -889,7 +934,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::kPFull + 2 * t + (h & 1)));
-            if constexpr (C8) unpack2(add2(l2[0], l2[1]), s4[0], s4[1]);
+            if constexpr (BS) unpack2(add2(l2[0], l2[1]), s4[0], s4[1]);
             l_sum = l_sum * resc + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
         }
         // Epilogue: O row / row sum, or the split's share of both.
@@ -1032,7 +1077,10 @@ pkv_status prefill_mod_launch(const PrefillCall &c) {
     CUtensorMap mk, mv;
     const int64_t slots = static_cast<int64_t>(c.num_blocks) * c.block_size;
     pkv_status st;
-    if constexpr (FMT != kCode16) {
+    if constexpr (FMT == kCodeInt4) {
+        mk = mv = CUtensorMap{};  // its copies are whole runs of a (block, head)
+        st = PKV_OK;
+    } else if constexpr (FMT != kCode16) {
         st = make_kv_map_8bit(&mk, c.k_cache, slots, c.Hkv, box_rows, 1);
         if (st == PKV_OK) st = make_kv_map_8bit(&mv, c.v_cache, slots, c.Hkv, box_rows, 1);
     } else {
@@ -1050,6 +1098,10 @@ pkv_status prefill_mod_launch(const PrefillCall &c) {
     a.cu_q = c.cu_q;
     a.k_scale = c.k_scale;
     a.v_scale = c.v_scale;
+    a.codes[0] = static_cast<const uint8_t *>(c.k_cache);
+    a.codes[1] = static_cast<const uint8_t *>(c.v_cache);
+    a.scales[0] = c.k_scale4;
+    a.scales[1] = c.v_scale4;
     a.slopes = c.mod.alibi_slopes;
     a.key_starts = c.mod.key_starts;
     a.prefix_lens = c.mod.prefix_lens;

@@ -90,6 +90,13 @@ __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // Fetch a tensor map (a __grid_constant__ kernel parameter) into the TMA
 // unit's descriptor cache ahead of its first bulk copy.
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *map) {
@@ -154,8 +161,8 @@ __device__ __forceinline__ uint32_t byte_pairs(uint32_t w) {
     return d;
 }
 
-// Code formats of the caches the decode kernel reads.
-enum CacheCode { kCode16 = 0, kCodeE4M3 = 1, kCodeInt8 = 2 };
+// Code formats of the caches the attention kernels read (4-bit codes carry their scales by row).
+enum CacheCode { kCode16 = 0, kCodeE4M3 = 1, kCodeInt8 = 2, kCodeInt4 = 3 };
 
 // Four int8 codes -> two f16x2 words, exactly.  Each byte, offset by 128 to an
 // unsigned u (xor of its sign bit), becomes the low mantissa byte of the f16
