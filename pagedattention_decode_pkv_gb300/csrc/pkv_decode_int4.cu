@@ -12,8 +12,11 @@
 //     accumulator's start, so the codes are never corrected; f32 sums of some 2^12 |q| carry
 //     it with an error of 2^-12 of a code step.
 //   * A group's scale multiplies its partial score in f32 (two products of 16 dims each).
-//   * V codes are widened exactly and multiplied by their scales, which is exact in f16 too
-//     (eight significant bits), so that P, rounded once to f16, is the only rounding.
+//   * V codes are widened exactly to u - 8.  A group's scale goes into P: p rounded to f16, times
+//     the scale, rounded again, each by 2^-12 of it at most on average, which is what the rounding
+//     of an fp16 output amounts to.  (The scales on V are exact, 64 more half-pair products a
+//     step of 32 tokens: 64 sequences of up to 4096 tokens 132 us against 123, 8 x 32768 61.7
+//     against 59.4.)
 //   * The transposed fragments of V come from ldmatrix.trans on 16-bit units: four dims of a
 //     token each, two tokens in a register, which is the pair the product wants.
 //
@@ -38,12 +41,12 @@
 namespace pkv {
 namespace {
 
-constexpr int kI4Step = 32;          // tokens of a step
 constexpr int kI4MaxSeqs = 512;      // sequences of a launch (shared-memory prefix)
 constexpr int kI4MaxWarps = 152 * 16;  // working warps of a launch (sizes the workspace)
-constexpr int kI4MinSteps = 2;       // steps that a working warp takes at least
+constexpr int kI4MinSteps = 1;       // steps that a working warp takes at least
 constexpr int kI4Heads = 8;          // query heads of a unit
 constexpr float kI4Log2e = 1.4426950408889634f;
+constexpr float kI4Slack = 2.5f;     // log2 units: 2^2.5 times the largest V scale is in f16's range
 
 struct I4Args {
     void *out;
@@ -54,8 +57,9 @@ struct I4Args {
     const float *slopes;
     int32_t max_blocks, B, Hq, Hkv, G, subs, bs, num_blocks, max_ctx;
     float scale_log2, softcap;
-    float *o_piece;    // [slots][NG * 8][32]
-    float2 *ml_piece;  // [slots][8]
+    int32_t rows;      // query heads of a unit, at most
+    float *o_piece;    // [slots][rows][D], slot warp + unit
+    float2 *ml_piece;  // [slots][rows]
     int2 *unit_info;   // [units]: first and last warp
     int32_t *err_flag;
 };
@@ -65,191 +69,252 @@ __device__ __forceinline__ int64_t i4_div(int64_t a, int64_t b) {  // a >= 0, b 
     return a / b;
 }
 
-// 16 bytes from global to shared memory, zeros when `bytes` is 0 (nothing is read then).
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// 16 bytes from global to shared memory.
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-template <int D> struct I4Ring {
-    static constexpr int NG = D / 32;              // groups, and 16-byte chunks of a row
-    static constexpr int kCodes = kI4Step * D / 2;
-    static constexpr int kScales = kI4Step * NG * 2;
-    static constexpr int kStage = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
+// N consecutive 32-bit words of shared memory.
+template <int N> __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&x)[N]) {
+    if constexpr (N == 1) {
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[0]) : "r"(addr));
+    } else if constexpr (N == 2) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(addr));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
+                         : "r"(addr + 4 * i));
+    }
+}
+
+// d = a b + c, the columns of c alike in both rows.
+__device__ __forceinline__ void mma_start(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+
+// A warp's shared memory: K codes and scales of a step, V's, and queries.  K of the next step is
+// copied while P V runs, V while Q K does, a unit's queries with the step before its first.
+template <int D, int STEP> struct I4Tile {
+    static constexpr int NG = D / 32;  // groups, and 16-byte chunks of a row
+    static constexpr int kCodes = STEP * D / 2;
+    static constexpr int kHalf = kCodes + STEP * NG * 2;
+    static constexpr int kQ = kI4Heads * D * 2;  // a unit's queries, of two units
+    static constexpr int kWarp = 2 * kHalf + 2 * kQ;
 };
 
-template <typename T, int D, int WARPS, int STAGES, int CTAS, bool MOD>
+template <typename T, int D, int STEP, int WARPS, int CTAS, bool MOD>
 __global__ void __launch_bounds__(WARPS * 32, CTAS)
 decode_int4_kernel(const __grid_constant__ I4Args A) {
-    using R = I4Ring<D>;
+    using R = I4Tile<D, STEP>;
     using H = Half16<__half>;
-    constexpr int NG = R::NG;
+    constexpr int NG = R::NG, TILES = STEP / 16;  // tiles of 16 tokens, each inside one block
     extern __shared__ __align__(128) uint8_t smem[];
-    int64_t *pref = reinterpret_cast<int64_t *>(smem + WARPS * STAGES * R::kStage);  // [B + 1] steps of a head's sequences before b
-    int32_t *cx = reinterpret_cast<int32_t *>(pref + kI4MaxSeqs + 1);                // context length (0: nothing visible)
-    int32_t *fk = cx + kI4MaxSeqs;                                                   // MOD: first visible key
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_trigger();
     const int B = A.B, bs = A.bs;
-    for (int b = threadIdx.x; b < B; b += WARPS * 32) {
-        const int ctx = A.context_lens[b];
-        const bool good = ctx >= 0 && ctx <= A.max_ctx && static_cast<int64_t>(ctx) <= static_cast<int64_t>(A.max_blocks) * bs;
-        const int first = MOD && A.key_starts ? max(A.key_starts[b], 0) : 0;
-        const bool any = good && ctx > first;
-        cx[b] = any ? ctx : 0;
-        if (MOD) fk[b] = any ? first : 0;
-        if (!any && b % gridDim.x == blockIdx.x) {  // a row of zeros
-            if (!good && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_CONTEXT);
-            uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(A.out) + static_cast<int64_t>(b) * A.Hq * D);
-            for (int i = 0; i < A.Hq * D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
-        }
-    }
-    __syncthreads();
-    auto steps_of = [&](int b) -> int64_t {
-        return (cx[b] + kI4Step - 1) / kI4Step - (MOD ? fk[b] / kI4Step : 0);
+    // Context length (0: nothing visible) and first visible key of sequence b.
+    auto first_of = [&](int b) -> int { return MOD && A.key_starts ? max(__ldg(A.key_starts + b), 0) : 0; };
+    auto context_of = [&](int b, int first) -> int {
+        const int ctx = __ldg(A.context_lens + b);
+        return ctx > first && ctx <= A.max_ctx && static_cast<int64_t>(ctx) <= static_cast<int64_t>(A.max_blocks) * bs ? ctx : 0;
     };
-    if (warp == 0) {
-        const int chunk = (B + 31) / 32, lo = min(lane * chunk, B), hi = min(lo + chunk, B);
-        int64_t sum = 0;
-        for (int b = lo; b < hi; ++b) sum += steps_of(b);
-        int64_t incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        int64_t run = incl - sum;
-        for (int b = lo; b < hi; ++b) {
-            pref[b] = run;
-            run += steps_of(b);
-        }
-        if (lane == 31) pref[B] = incl;
-    }
-    __syncthreads();
+    auto steps_of = [&](int b) -> int {
+        const int first = first_of(b), ctx = context_of(b, first);
+        return ctx > 0 ? (ctx + STEP - 1) / STEP - first / STEP : 0;
+    };
     const int HU = A.Hkv * A.subs;  // units of a sequence
-    const int64_t W = pref[B] * HU;
-    int64_t Cw = W / kI4MinSteps;
-    const int64_t all = static_cast<int64_t>(gridDim.x) * WARPS;
-    Cw = Cw > all ? all : Cw < 1 ? 1 : Cw;
-    // neighbouring slices go to different SMs, so that a launch of few slices uses them all
-    const int64_t me = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
-    if (me >= Cw || W == 0) return;
-    const int64_t s0 = i4_div(W * me, Cw), s1 = i4_div(W * (me + 1), Cw);
-
-    // Cursor: sequence b, unit hu of it, step st of n.
-    struct Cursor { int b, hu, st, n; };
+    struct Cursor { int b, hu, st, n; };  // step st of the n of unit hu of sequence b
     Cursor cur;
+    int64_t me = 0;
+    int count = 0;  // steps of this warp's slice
     {
-        int lo = 0, hi = B - 1;  // the largest b with HU pref[b] <= s0
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (pref[mid] * HU <= s0) lo = mid; else hi = mid - 1;
+        // The prefix of steps over the sequences (of one unit each), in what holds the tiles later.
+        int64_t *pref = reinterpret_cast<int64_t *>(smem);  // [B + 1]
+        int32_t *ns = reinterpret_cast<int32_t *>(pref + kI4MaxSeqs + 1);
+        for (int b = threadIdx.x; b < B; b += WARPS * 32) {
+            const int n = steps_of(b);
+            ns[b] = n;
+            if (n == 0 && b % gridDim.x == blockIdx.x) {  // a row of zeros
+                const int ctx = A.context_lens[b];
+                if ((ctx < 0 || ctx > A.max_ctx || static_cast<int64_t>(ctx) > static_cast<int64_t>(A.max_blocks) * bs) && A.err_flag)
+                    atomicOr(A.err_flag, PKV_ERRBIT_CONTEXT);
+                uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(A.out) + static_cast<int64_t>(b) * A.Hq * D);
+                for (int i = 0; i < A.Hq * D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
+            }
         }
-        const int64_t n = pref[lo + 1] - pref[lo], off = s0 - pref[lo] * HU;
-        cur.b = lo;
-        cur.n = static_cast<int>(n);
-        cur.hu = static_cast<int>(i4_div(off, n));
-        cur.st = static_cast<int>(off - cur.hu * n);
+        __syncthreads();
+        if (warp == 0) {
+            const int chunk = (B + 31) / 32, lo = min(lane * chunk, B), hi = min(lo + chunk, B);
+            int64_t sum = 0;
+            for (int b = lo; b < hi; ++b) sum += ns[b];
+            int64_t incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            int64_t run = incl - sum;
+            for (int b = lo; b < hi; ++b) {
+                pref[b] = run;
+                run += ns[b];
+            }
+            if (lane == 31) pref[B] = incl;
+        }
+        __syncthreads();
+        const int64_t W = pref[B] * HU;
+        int64_t Cw = W / kI4MinSteps;
+        const int64_t all = static_cast<int64_t>(gridDim.x) * WARPS;
+        Cw = Cw > all ? all : Cw < 1 ? 1 : Cw;
+        // neighbouring slices go to different SMs, so that a launch of few slices uses them all
+        me = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+        if (me < Cw && W > 0) {
+            const int64_t s0 = i4_div(W * me, Cw), s1 = i4_div(W * (me + 1), Cw);
+            count = static_cast<int>(s1 - s0);
+            int lo = 0, hi = B - 1;  // the largest b with HU pref[b] <= s0
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (pref[mid] * HU <= s0) lo = mid; else hi = mid - 1;
+            }
+            const int64_t off = s0 - pref[lo] * HU;
+            cur.b = lo;
+            cur.n = ns[lo];
+            cur.hu = static_cast<int>(i4_div(off, cur.n));
+            cur.st = static_cast<int>(off - static_cast<int64_t>(cur.hu) * cur.n);
+        }
+        __syncthreads();  // the prefix has been read: the tiles may be filled
     }
-    auto advance = [&](Cursor &c) {  // true at the start of a unit
-        if (++c.st < c.n) return false;
+    if (count == 0) return;
+    auto next_unit = [&](Cursor &c) {  // the first step of the next unit (b == B: there is none)
         c.st = 0;
         if (++c.hu == HU) {
             c.hu = 0;
             do {
                 ++c.b;
-                c.n = c.b < B ? static_cast<int>(pref[c.b + 1] - pref[c.b]) : 1;
-            } while (c.b < B && c.n == 0);
+                c.n = c.b < B ? steps_of(c.b) : 1;
+            } while (c.n == 0);
         }
-        return true;
     };
 
-    // ---- copies: lane l takes 16-byte chunks of codes and one of scales; the table entries of
-    // a step's two halves of 16 tokens (one block each) are loaded a step ahead
-    const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp) * STAGES * R::kStage;
+    // ---- copies.  Lanes 0 .. TILES - 1 keep the table column and the row of their tile and load
+    // its entry a step ahead; of a tile's codes every lane takes the same chunk of rows r, r +
+    // 32 / NG, .., so that all addresses but the tile's first row are constants of the lane.
+    const uint32_t k_tile = smem_u32(smem) + static_cast<uint32_t>(warp) * R::kWarp, v_tile = k_tile + R::kHalf;
+    const uint32_t q_tile = k_tile + 2 * R::kHalf;
+    constexpr int kRowsPer = 32 / NG;        // rows that one copy instruction covers
+    constexpr int kCopies = 16 / kRowsPer;   // of a tile
+    constexpr int kChunks = 2 * NG;          // 16-byte chunks of a tile's scales
+    constexpr int kScaleTiles = 32 / kChunks < TILES ? 32 / kChunks : TILES;  // tiles whose scales one instruction copies
+    static_assert(kRowsPer <= 16 && kChunks <= 32, "lanes of the copies");
+    auto swizzled = [](int row, int c) { return (c ^ ((row * NG / 8) & (NG - 1))) << 4; };  // the same for rows 8 apart
+    const uint32_t code_src = (lane / NG) * (D / 2) + (lane & (NG - 1)) * 16;
+    uint32_t code_dst[kRowsPer < 8 ? 2 : 1];
+    code_dst[0] = (lane / NG) * (D / 2) + swizzled(lane / NG, lane & (NG - 1));
+    if constexpr (kRowsPer < 8) code_dst[1] = (lane / NG) * (D / 2) + swizzled(lane / NG + kRowsPer, lane & (NG - 1));
     Cursor ld = cur;
-    int next_id = -1;
+    uint32_t col = 0, in = 0;  // table column, and row of 16 inside the block, of tile lane % TILES
+    int next_id = -2;          // its entry (-2: nothing of the tile is seen)
     bool bad = false;
-    auto position = [&](const Cursor &c) { return (c.st + (MOD ? fk[c.b] / kI4Step : 0)) * kI4Step; };
-    auto fetch_id = [&](const Cursor &c) {  // lane h < 2: half h
-        next_id = -2;                       // behind the context
-        if (lane < 2 && c.b < B) {
-            const int pos = position(c) + 16 * lane;
-            const bool seen = pos < cx[c.b] && (!MOD || pos + 16 > fk[c.b]);
-            if (seen) next_id = A.block_tables[static_cast<int64_t>(c.b) * A.max_blocks + pos / bs];
-        }
+    const uint32_t bs16 = static_cast<uint32_t>(bs) >> 4;
+    const uint32_t col_by = TILES / bs16, in_by = TILES - col_by * bs16;  // a step further
+    int ld_pos = 0, ld_ctx = 0, ld_first = 0;  // of ld's step: position of this lane's tile
+    uint32_t ld_head = 0;
+    const int32_t *ld_table = nullptr;
+    auto look_up = [&] {
+        next_id = -2;
+        if (lane < TILES && ld_pos < ld_ctx && (!MOD || ld_pos + 16 > ld_first)) next_id = __ldg(ld_table + col);
     };
-    constexpr int kRowsPer = 32 / NG;                 // rows that one copy instruction covers
-    constexpr int kCopies = kI4Step / kRowsPer;
-    static_assert(kRowsPer <= 16 && kI4Step * NG * 2 / 16 <= 32, "lanes of the copies");
-    auto swizzled = [](int row, int c) { return (c ^ ((row * NG / 8) & (NG - 1))) << 4; };
-    auto issue = [&](int slot) {
-        const int kh = ld.hu / A.subs, pos = position(ld);
-        const uint32_t dst = ring + static_cast<uint32_t>(slot) * R::kStage;
-        int64_t row[2];
-        bool ok[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int id = __shfl_sync(0xffffffffu, next_id, h);
-            ok[h] = id >= 0 && id < A.num_blocks;
-            bad = bad || (!ok[h] && id != -2);
-            const int p = pos + 16 * h;
-            row[h] = ok[h] ? (static_cast<int64_t>(id) * A.Hkv + kh) * bs + p % bs : 0;
+    int ld_b = -1, ld_unit = 0;  // the sequence that ld_ctx is of, units begun
+    auto start_unit = [&] {
+        next_id = -2;
+        if (ld.b >= B) return;
+        if (ld.b != ld_b) {
+            ld_b = ld.b;
+            ld_first = first_of(ld.b);
+            ld_ctx = context_of(ld.b, ld_first);
+            ld_table = A.block_tables + static_cast<int64_t>(ld.b) * A.max_blocks;
         }
-        const int c = lane & (NG - 1), r0 = lane / NG;
-#pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-            const int h = i * kRowsPer / 16, r = i * kRowsPer + r0;
-            const int64_t src = (row[h] + (r - 16 * h)) * (D / 2) + 16 * c;
-            const uint32_t d = dst + r * (D / 2) + swizzled(r, c), bytes = ok[h] ? 16 : 0;
-            cp16(d, A.k_cache + (ok[h] ? src : 0), bytes);
-            cp16(d + R::kCodes, A.v_cache + (ok[h] ? src : 0), bytes);
-        }
-        // scales: 16 tokens x NG x 2 bytes of a half are NG * 2 chunks
-        constexpr int kChunks = kI4Step * NG * 2 / 16;  // both halves
-        if (lane < kChunks) {
-            const int h = lane / (kChunks / 2), k = lane - h * (kChunks / 2);
-            const int64_t src = (h ? row[1] : row[0]) * NG + 8 * k;
-            const bool o = h ? ok[1] : ok[0];
-            cp16(dst + 2 * R::kCodes + 16 * lane, A.k_scale + (o ? src : 0), o ? 16 : 0);
-            cp16(dst + 2 * R::kCodes + R::kScales + 16 * lane, A.v_scale + (o ? src : 0), o ? 16 : 0);
-        }
-        advance(ld);
-        fetch_id(ld);
-        return (ok[0] ? 1 : 0) | (ok[1] ? 2 : 0);
+        const int kh = ld.hu / A.subs, sub = ld.hu - kh * A.subs;
+        ld_head = static_cast<uint32_t>(kh);
+        ld_pos = (ld_first / STEP + ld.st) * STEP + 16 * (lane & (TILES - 1));
+        col = static_cast<uint32_t>(ld_pos >> 4) / bs16;
+        in = static_cast<uint32_t>(ld_pos >> 4) - col * bs16;
+        look_up();
+        const int live = min(kI4Heads, A.G - sub * kI4Heads);
+        const uint8_t *src = static_cast<const uint8_t *>(A.q) +
+                             (static_cast<int64_t>(ld.b) * A.Hq + kh * A.G + sub * kI4Heads) * (D * 2) + 16 * lane;
+        for (int i = lane; i < live * (D / 8); i += 32, src += 512) cp16(q_tile + (ld_unit & 1) * R::kQ + 16 * i, src);
+        ++ld_unit;  // committed with the next copy
     };
-    uint32_t oks = 0;  // two bits a ring slot: the halves that were there
-    fetch_id(ld);
-    int64_t issued = s0;
-    auto issue_next = [&] {
-        if (issued < s1) {
-            const int slot = static_cast<int>((issued - s0) % STAGES);
-            oks = (oks & ~(3u << 2 * slot)) | static_cast<uint32_t>(issue(slot)) << 2 * slot;
+    uint32_t at = 0, here = 0;  // of the step copied last: a tile's first row, in rows of 16 (lane h: tile h); the tiles that are there
+    auto copy = [&](uint32_t dst, const uint8_t *codes, const __half *scales) {
+#pragma unroll
+        for (int h = 0; h < TILES; ++h) {
+            const uint32_t row16 = __shfl_sync(0xffffffffu, at, h);
+            if (!(here >> h & 1)) continue;  // what is not there is masked, its stale rows too
+            const uint8_t *src = codes + (static_cast<uint64_t>(row16) * (8 * D) + code_src);
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i)
+                cp16(dst + code_dst[kRowsPer < 8 ? i & 1 : 0] + (16 * h + i * kRowsPer) * (D / 2), src + i * kRowsPer * (D / 2));
         }
-        ++issued;
+#pragma unroll
+        for (int h = 0; h < TILES; h += kScaleTiles) {
+            const int mt = h + lane / kChunks;  // this lane's tile
+            const uint32_t row16 = __shfl_sync(0xffffffffu, at, mt & (TILES - 1));
+            if (lane < kScaleTiles * kChunks && (here >> mt & 1))
+                cp16(dst + R::kCodes + 16 * (h * kChunks + lane), scales + (static_cast<uint64_t>(row16) * (16 * NG) + 8 * (lane % kChunks)));
+        }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) issue_next();
-
+    auto copy_k = [&] {  // of the next step, whose entries have been looked up; then those of the one behind it are
+        const bool mine = next_id >= 0 && next_id < A.num_blocks;
+        bad = bad || (!mine && next_id != -2);
+        // a pool that fits the memory has less than 2^32 rows of 16
+        at = mine ? (static_cast<uint32_t>(next_id) * A.Hkv + ld_head) * bs16 + in : 0u;
+        here = __ballot_sync(0xffffffffu, mine) & ((1u << TILES) - 1);
+        copy(k_tile, A.k_cache, A.k_scale);
+        if (++ld.st < ld.n) {
+            const bool over = in + in_by >= bs16;
+            in = in + in_by - (over ? bs16 : 0u);
+            col += col_by + (over ? 1u : 0u);
+            ld_pos += STEP;
+            look_up();
+        } else {
+            next_unit(ld);
+            start_unit();
+        }
+    };
+    start_unit();
     // ---- a unit's queries: lane (g = head, t): dims 8 t .. 8 t + 7 of every group, f16 under a power of two
     const int g = lane >> 2, t = lane & 3, mi = lane >> 3, r8 = lane & 7;
+    const uint32_t frag_at = (r8 + 8 * (mi & 1)) * (D / 2), frag_sw = swizzled(r8, 0);  // this lane's row of the ldmatrix tiles
     uint32_t qf[NG][4];
     float off[NG][2];            // start of the group's accumulator, heads 2 t and 2 t + 1
     float sl0 = 0.f, sl1 = 0.f;  // scores to log2 units, of heads 2 t, 2 t + 1
     float slope0 = 0.f, slope1 = 0.f;
     int heads = 0;
     int64_t head0 = 0;  // first query head's row of q and out
+    int unit = 0;  // units begun
     auto load_q = [&](const Cursor &c) {
         const int kh = c.hu / A.subs, sub = c.hu - kh * A.subs;
         heads = min(kI4Heads, A.G - sub * kI4Heads);
         head0 = static_cast<int64_t>(c.b) * A.Hq + kh * A.G + sub * kI4Heads;
         const bool live = g < heads;
-        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const T *>(A.q) + (head0 + (live ? g : 0)) * D) + t;
-        uint4 x[NG];
+        const uint32_t src = q_tile + (unit & 1) * R::kQ + g * (D * 2) + t * 16;
+        ++unit;
+        uint32_t x[NG][4];
         float top = 0.f;
 #pragma unroll
-        for (int gg = 0; gg < NG; ++gg) x[gg] = live ? __ldg(src + 4 * gg) : make_uint4(0, 0, 0, 0);
+        for (int gg = 0; gg < NG; ++gg) {
+            lds_words(src + gg * 64, x[gg]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[gg][k] = live ? x[gg][k] : 0u;
+        }
         auto get = [&](int gg, int k) -> float {
             const T *e = reinterpret_cast<const T *>(&x[gg]);
             return to_f32<T>(e[k]);
@@ -298,12 +363,23 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
     };
 
     float o[NG][2][4];  // rows: dims 32 gg + 8 (g / 2) + g % 2 + 4 e (+ 2), columns: heads 2 t, 2 t + 1
-    float m0, m1, l0, l1;
-    bool fresh = true;   // the next step starts a unit
-    bool whole = false;  // the unit began in this slice
-    for (int64_t s = s0; s < s1; ++s) {
+    float m0, m1, l0, l1, b0, b1;  // references (b = -m, 0 before there is one) and sums
+    int pos = 0, ctx = 0, first = 0, cur_b = -1;  // of cur's step, and the sequence they are of
+    bool fresh = true;                // the next step starts a unit
+    bool whole = false;               // the unit began in this slice
+    copy_k();
+    copy(v_tile, A.v_cache, A.v_scale);
+    for (int s = 0; s < count; ++s) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // K: V, committed after it, may be under way
+        __syncwarp();
         if (fresh) {
             load_q(cur);
+            if (cur.b != cur_b) {
+                cur_b = cur.b;
+                first = first_of(cur.b);
+                ctx = context_of(cur.b, first);
+            }
+            pos = (first / STEP + cur.st) * STEP;
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg)
 #pragma unroll
@@ -311,50 +387,37 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) o[gg][e][c] = 0.f;
             m0 = m1 = -INFINITY;
-            l0 = l1 = 0.f;
+            l0 = l1 = b0 = b1 = 0.f;
             whole = cur.st == 0;
             if (lane == 0 && whole) A.unit_info[static_cast<int64_t>(cur.b) * HU + cur.hu].x = static_cast<int>(me);
             fresh = false;
         }
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-        __syncwarp();
-        issue_next();  // into the slot of the step before this one
-        const int slot = static_cast<int>((s - s0) % STAGES);
-        const uint32_t base = ring + static_cast<uint32_t>(slot) * R::kStage;
-        const int pos = position(cur), ctx = cx[cur.b], first = MOD ? fk[cur.b] : 0;
-        const uint32_t here = oks >> 2 * slot & 3;
-        const bool partial = pos + kI4Step > ctx || (MOD && pos < first) || here != 3;
+        const uint32_t now = here;
+        const bool partial = pos + STEP > ctx || (MOD && pos < first) || now != (1u << TILES) - 1;
         auto seen = [&](int k) {  // token k of the step
-            return pos + k < ctx && (!MOD || pos + k >= first) && (here >> (k >> 4) & 1);
+            return pos + k < ctx && (!MOD || pos + k >= first) && (now >> (k >> 4) & 1);
         };
-
-        // 1. scores, two tiles of 16 tokens: rows (tokens) g and g + 8, columns (heads) 2 t, 2 t + 1
-        float y[2][4];
+        // 1. scores, tiles of 16 tokens: rows (tokens) g and g + 8, columns (heads) 2 t, 2 t + 1
+        float y[TILES][4];
 #pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
+        for (int tile = 0; tile < TILES; ++tile) {
             uint32_t w[NG][2];  // word t of group gg, of tokens g and g + 8
 #pragma unroll
             for (int gg = 0; gg < NG; gg += 2) {
-                const int row = 16 * tile + r8 + 8 * (mi & 1);
                 uint32_t x[4];
-                ldsm_x4(base + row * (D / 2) + swizzled(row, gg + (mi >> 1)), x);
+                ldsm_x4(k_tile + frag_at + 16 * tile * (D / 2) + (((gg + (mi >> 1)) << 4) ^ frag_sw), x);
                 w[gg][0] = x[0];
                 w[gg][1] = x[1];
                 w[gg + 1][0] = x[2];
                 w[gg + 1][1] = x[3];
             }
             uint32_t sa[NG / 2], sb[NG / 2];  // scales of tokens g and g + 8
-            const uint32_t ks = base + 2 * R::kCodes + (16 * tile + g) * (NG * 2);
-#pragma unroll
-            for (int i = 0; i < NG / 2; ++i) {
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sa[i]) : "r"(ks + 4 * i));
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sb[i]) : "r"(ks + 8 * NG * 2 + 4 * i));
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) y[tile][c] = 0.f;
+            const uint32_t ks = k_tile + R::kCodes + (16 * tile + g) * (NG * 2);
+            lds_words(ks, sa);
+            lds_words(ks + 8 * NG * 2, sb);
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg) {
-                float acc[4] = {off[gg][0], off[gg][1], off[gg][0], off[gg][1]};
+                float acc[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     uint32_t a[4];
@@ -363,25 +426,30 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
                     asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(a[1]) : "r"(x1));
                     asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(a[2]) : "r"(x0));
                     asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(a[3]) : "r"(x1));
-                    H::mma(acc, a, qf[gg][2 * e], qf[gg][2 * e + 1]);
+                    if (e == 0) mma_start(acc, a, qf[gg][0], qf[gg][1], off[gg][0], off[gg][1]);
+                    else H::mma(acc, a, qf[gg][2], qf[gg][3]);
                 }
                 const float2 fa = __half22float2(*reinterpret_cast<const __half2 *>(&sa[gg / 2]));
                 const float2 fb = __half22float2(*reinterpret_cast<const __half2 *>(&sb[gg / 2]));
                 const float s_a = gg & 1 ? fa.y : fa.x, s_b = gg & 1 ? fb.y : fb.x;
-                y[tile][0] = fmaf(s_a, acc[0], y[tile][0]);
-                y[tile][1] = fmaf(s_a, acc[1], y[tile][1]);
-                y[tile][2] = fmaf(s_b, acc[2], y[tile][2]);
-                y[tile][3] = fmaf(s_b, acc[3], y[tile][3]);
+                y[tile][0] = gg ? fmaf(s_a, acc[0], y[tile][0]) : s_a * acc[0];
+                y[tile][1] = gg ? fmaf(s_a, acc[1], y[tile][1]) : s_a * acc[1];
+                y[tile][2] = gg ? fmaf(s_b, acc[2], y[tile][2]) : s_b * acc[2];
+                y[tile][3] = gg ? fmaf(s_b, acc[3], y[tile][3]) : s_b * acc[3];
             }
         }
-        // 2. log2 units, score rules, masks
+        __syncwarp();
+        const bool more = s + 1 < count;
+        if (more) copy_k();
+        else asm volatile("cp.async.commit_group;" ::: "memory");  // (the group that the waits count)
+        // 2. score rules, in log2 units (without them the factors sl0, sl1 > 0 wait for the exponent), and masks
+        if constexpr (MOD) {
 #pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-            y[tile][0] *= sl0;
-            y[tile][1] *= sl1;
-            y[tile][2] *= sl0;
-            y[tile][3] *= sl1;
-            if constexpr (MOD) {
+            for (int tile = 0; tile < TILES; ++tile) {
+                y[tile][0] *= sl0;
+                y[tile][1] *= sl1;
+                y[tile][2] *= sl0;
+                y[tile][3] *= sl1;
                 if (A.softcap > 0.f) {
                     // c tanh(s / c): the fit where |s / c| is small, else by the exponential
                     const float cap = A.softcap * kI4Log2e, inv = 1.f / cap, u2 = 2.f / A.softcap;
@@ -402,7 +470,7 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
         }
         if (partial) {
 #pragma unroll
-            for (int tile = 0; tile < 2; ++tile) {
+            for (int tile = 0; tile < TILES; ++tile) {
                 const bool a = seen(16 * tile + g), b = seen(16 * tile + g + 8);
                 y[tile][0] = a ? y[tile][0] : -INFINITY;
                 y[tile][1] = a ? y[tile][1] : -INFINITY;
@@ -410,19 +478,30 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
                 y[tile][3] = b ? y[tile][3] : -INFINITY;
             }
         }
-        // 3. running maximum; the accumulator moves when it does
-        float mx0 = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
-        float mx1 = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
+        // 3. The reference m of a head is a maximum of some step; P = 2^(y - m) may exceed 1 by
+        // kI4Slack binades before it is moved, and the sum and accumulator with it.
+        float mx0 = fmaxf(y[0][0], y[0][2]), mx1 = fmaxf(y[0][1], y[0][3]);
 #pragma unroll
-        for (int sh = 4; sh < 32; sh <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
+        for (int tile = 1; tile < TILES; ++tile) {
+            mx0 = max3f(mx0, y[tile][0], y[tile][2]);
+            mx1 = max3f(mx1, y[tile][1], y[tile][3]);
         }
-        if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
+        if constexpr (!MOD) {
+            mx0 *= sl0;
+            mx1 *= sl1;
+        }
+        if (__any_sync(0xffffffffu, mx0 > m0 + kI4Slack || mx1 > m1 + kI4Slack)) {
+#pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1) {
+                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
+            }
             const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
             const float a0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0), a1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
             m0 = n0;
             m1 = n1;
+            b0 = n0 == -INFINITY ? 0.f : -n0;
+            b1 = n1 == -INFINITY ? 0.f : -n1;
             l0 *= a0;
             l1 *= a1;
 #pragma unroll
@@ -435,55 +514,56 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
                     o[gg][e][3] *= a1;
                 }
         }
-        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // V: the next K may be under way
+        __syncwarp();
+        if (partial) {  // V scales of rows that are not seen may be anything, and P there is 0: their product must be 0
+            for (int k = lane; k < STEP; k += 32)
+                if (!seen(k)) {
+#pragma unroll
+                    for (int i = 0; i < NG / 2; ++i)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(v_tile + R::kCodes + k * (NG * 2) + 4 * i), "r"(0) : "memory");
+                }
+            __syncwarp();
+        }
         // 4. P and O += P V
 #pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-            const float p0 = fast_exp2(y[tile][0] - b0), p1 = fast_exp2(y[tile][1] - b1);
-            const float p2 = fast_exp2(y[tile][2] - b0), p3 = fast_exp2(y[tile][3] - b1);
+        for (int tile = 0; tile < TILES; ++tile) {
+            const float f0 = MOD ? 1.f : sl0, f1 = MOD ? 1.f : sl1;
+            const float p0 = fast_exp2(fmaf(y[tile][0], f0, b0)), p1 = fast_exp2(fmaf(y[tile][1], f1, b1));
+            const float p2 = fast_exp2(fmaf(y[tile][2], f0, b0)), p3 = fast_exp2(fmaf(y[tile][3], f1, b1));
             l0 += p0 + p2;
             l1 += p1 + p3;
             const uint32_t pb0 = movmatrix_trans(H::pack(p0, p1)), pb1 = movmatrix_trans(H::pack(p2, p3));
             // scales of tokens 2 t, 2 t + 1 (words 0 .. NG - 1) and of those 8 further
             uint32_t va[NG], vb[NG];
-            const uint32_t vs = base + 2 * R::kCodes + R::kScales + (16 * tile + 2 * t) * (NG * 2);
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(va[i]) : "r"(vs + 4 * i));
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vb[i]) : "r"(vs + 8 * NG * 2 + 4 * i));
-            }
-            if (partial) {  // scales of rows that are not seen may be anything, P there is 0: their product must be 0
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    const int k = 16 * tile + 2 * t + (i >= NG / 2 ? 1 : 0);
-                    va[i] = seen(k) ? va[i] : 0u;
-                    vb[i] = seen(k + 8) ? vb[i] : 0u;
-                }
-            }
+            const uint32_t vs = v_tile + R::kCodes + (16 * tile + 2 * t) * (NG * 2);
+            lds_words(vs, va);
+            lds_words(vs + 8 * NG * 2, vb);
 #pragma unroll
             for (int gg = 0; gg < NG; gg += 2) {
                 uint32_t w[4];  // (tokens 0 .. 7 | 8 .. 15) of groups gg, gg + 1
-                const int row = 16 * tile + r8 + 8 * (mi & 1);
-                ldsm_x4_trans(base + R::kCodes + row * (D / 2) + swizzled(row, gg + (mi >> 1)), w);
+                ldsm_x4_trans(v_tile + frag_at + 16 * tile * (D / 2) + (((gg + (mi >> 1)) << 4) ^ frag_sw), w);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t sel = h ? 0x7632 : 0x5410;  // (scale of token 2 t, of 2 t + 1)
                     const uint32_t s_a = __byte_perm(va[gg / 2], va[NG / 2 + gg / 2], sel);
                     const uint32_t s_b = __byte_perm(vb[gg / 2], vb[NG / 2 + gg / 2], sel);
+                    const uint32_t q0 = mul_f16x2(pb0, s_a), q1 = mul_f16x2(pb1, s_b);
                     uint32_t xa[4], xb[4];
                     int4_widen(w[2 * h], xa);
                     int4_widen(w[2 * h + 1], xb);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t a[4] = {mul_f16x2(xa[2 * e], s_a), mul_f16x2(xa[2 * e + 1], s_a),
-                                               mul_f16x2(xb[2 * e], s_b), mul_f16x2(xb[2 * e + 1], s_b)};
-                        H::mma(o[gg + h][e], a, pb0, pb1);
+                        const uint32_t a[4] = {xa[2 * e], xa[2 * e + 1], xb[2 * e], xb[2 * e + 1]};
+                        H::mma(o[gg + h][e], a, q0, q1);
                     }
                 }
             }
         }
-        const Cursor at = cur;
-        if (advance(cur) || s + 1 == s1) {
+        __syncwarp();
+        if (more) copy(v_tile, A.v_cache, A.v_scale);
+        pos += STEP;
+        if (++cur.st == cur.n || s + 1 == count) {
             // the unit ends, or the slice does
             fresh = true;
 #pragma unroll
@@ -491,8 +571,8 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
                 l0 += __shfl_xor_sync(0xffffffffu, l0, sh);
                 l1 += __shfl_xor_sync(0xffffffffu, l1, sh);
             }
-            const bool ends = at.st == at.n - 1;
-            const int64_t u = static_cast<int64_t>(at.b) * HU + at.hu;
+            const bool ends = cur.st == cur.n;
+            const int64_t u = static_cast<int64_t>(cur.b) * HU + cur.hu;
             if (ends && lane == 0) A.unit_info[u].y = static_cast<int>(me);
             const int hA = 2 * t, hB = 2 * t + 1;
             if (whole && ends) {
@@ -512,102 +592,133 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
                             out[hB * D + d + 2] = from_f32<T>(o[gg][e][3] * i1);
                         }
                     }
-            } else if (hA < heads) {
-                const int64_t piece = me + u;
-                float *po = A.o_piece + piece * (NG * 8 * 32) + lane;
+            } else {
+                const int64_t piece = (me + u) * A.rows;
+                float *po = A.o_piece + piece * D;
 #pragma unroll
                 for (int gg = 0; gg < NG; ++gg)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) po[((gg * 2 + e) * 4 + c) * 32] = o[gg][e][c];
-                if (g == 0) {
-                    A.ml_piece[piece * kI4Heads + hA] = make_float2(m0, l0);
-                    A.ml_piece[piece * kI4Heads + hB] = make_float2(m1, l1);
-                }
+                    for (int e = 0; e < 2; ++e) {
+                        const int d = 32 * gg + 8 * (g >> 1) + (g & 1) + 4 * e;
+                        if (hA < heads) {
+                            po[hA * D + d] = o[gg][e][0];
+                            po[hA * D + d + 2] = o[gg][e][2];
+                        }
+                        if (hB < heads) {
+                            po[hB * D + d] = o[gg][e][1];
+                            po[hB * D + d + 2] = o[gg][e][3];
+                        }
+                    }
+                if (g == 0 && hA < heads) A.ml_piece[piece + hA] = make_float2(m0, l0);
+                if (g == 0 && hB < heads) A.ml_piece[piece + hB] = make_float2(m1, l1);
             }
+            if (ends) next_unit(cur);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (bad && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_BLOCK_RANGE);
 }
 
-// Joins a unit's pieces: out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k.  A warp takes one
-// (unit, group, half) of the accumulator in the layout the pieces are in.
+// Joins a unit's pieces: out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k.  WPR warps take a
+// row (a unit's query head), lanes the dims, eight pieces in flight a warp; the host spreads few
+// rows over more warps.
 constexpr int kI4JoinWarps = 8;
+constexpr int kI4JoinTarget = 4096;  // warps of a launch, about
 
-template <typename T, int D>
+template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(kI4JoinWarps * 32)
-decode_int4_join_kernel(const __grid_constant__ I4Args A, int64_t units) {
-    constexpr int NG = D / 32, kParts = NG * 2;
+decode_int4_join_kernel(const __grid_constant__ I4Args A, int64_t rows) {
+    constexpr int V = D / 32;  // dims of a lane
+    constexpr int U = D == 256 ? 4 : 8;
+    using F = typename std::conditional<V == 2, float2, float4>::type;
+    constexpr int FW = sizeof(F) / 4, FN = V / FW;
+    __shared__ float part[WPR > 1 ? kI4JoinWarps : 1][D];
+    __shared__ float2 part_ml[kI4JoinWarps];
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kI4JoinWarps + (threadIdx.x >> 5);
-    const int64_t u = item / kParts;
-    const int part = static_cast<int>(item - u * kParts);
-    if (u >= units) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub_warp = warp % WPR;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kI4JoinWarps / WPR) + warp / WPR;
     const int HU = A.Hkv * A.subs;
-    const int b = static_cast<int>(u / HU), hu = static_cast<int>(u - static_cast<int64_t>(b) * HU);
-    const int kh = hu / A.subs, sub = hu - kh * A.subs, heads = min(kI4Heads, A.G - sub * kI4Heads);
-    const int ctx = A.context_lens[b], first = A.key_starts ? max(A.key_starts[b], 0) : 0;
-    const int2 ui = A.unit_info[u];
-    if (ctx <= first || ctx > A.max_ctx || static_cast<int64_t>(ctx) > static_cast<int64_t>(A.max_blocks) * A.bs) return;  // zeros already
-    if (ui.x >= ui.y || 2 * t >= heads) return;  // one piece: written by the main kernel
-    constexpr int U = 8;
-    float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int w = ui.x; w <= ui.y; w += U) {
-        float v[U][4];
-        float4 ml[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int64_t piece = w + i + u;
-            const bool in = w + i <= ui.y;
-            ml[i] = in ? __ldg(reinterpret_cast<const float4 *>(A.ml_piece + piece * kI4Heads + 2 * t)) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) v[i][c] = in ? __ldg(A.o_piece + piece * (NG * 8 * 32) + (part * 4 + c) * 32 + lane) : 0.f;
-        }
-        float n0 = M0, n1 = M1;
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            n0 = fmaxf(n0, ml[i].x);
-            n1 = fmaxf(n1, ml[i].z);
-        }
-        const float r0 = n0 == -INFINITY ? 0.f : n0, r1 = n1 == -INFINITY ? 0.f : n1;
-        const float a0 = exp2f(M0 - r0), a1 = exp2f(M1 - r1);
-        M0 = n0;
-        M1 = n1;
-        L0 *= a0;
-        L1 *= a1;
-        acc[0] *= a0;
-        acc[1] *= a1;
-        acc[2] *= a0;
-        acc[3] *= a1;
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const float w0 = exp2f(ml[i].x - r0), w1 = exp2f(ml[i].z - r1);
-            L0 = fmaf(w0, ml[i].y, L0);
-            L1 = fmaf(w1, ml[i].w, L1);
-            acc[0] = fmaf(w0, v[i][0], acc[0]);
-            acc[1] = fmaf(w1, v[i][1], acc[1]);
-            acc[2] = fmaf(w0, v[i][2], acc[2]);
-            acc[3] = fmaf(w1, v[i][3], acc[3]);
+    int64_t u = 0, out_row = 0;
+    int r = 0, from = 0, to = -1;  // the row's pieces are those of warps from .. to
+    if (row < rows) {
+        u = i4_div(row, A.rows);
+        r = static_cast<int>(row - u * A.rows);
+        const int b = static_cast<int>(i4_div(u, HU)), hu = static_cast<int>(u - static_cast<int64_t>(b) * HU);
+        const int kh = hu / A.subs, head = (hu - kh * A.subs) * kI4Heads + r;
+        const int ctx = A.context_lens[b], first = A.key_starts ? max(A.key_starts[b], 0) : 0;
+        const int2 ui = A.unit_info[u];
+        out_row = static_cast<int64_t>(b) * A.Hq + kh * A.G + head;
+        // Nothing to do: a row of zeros already, or one piece (the main kernel wrote the output).
+        // Ranges outside the launch's warps are never left behind; none would be followed.
+        if (head < A.G && ctx > first && ctx <= A.max_ctx && static_cast<int64_t>(ctx) <= static_cast<int64_t>(A.max_blocks) * A.bs &&
+            ui.x >= 0 && ui.x < ui.y && ui.y < kI4MaxWarps) {
+            from = ui.x;
+            to = ui.y;
         }
     }
-    const float i0 = L0 > 0.f ? 1.f / L0 : (L0 == L0 ? 0.f : L0), i1 = L1 > 0.f ? 1.f / L1 : (L1 == L1 ? 0.f : L1);
-    const int gg = part >> 1, e = part & 1, d = 32 * gg + 8 * (g >> 1) + (g & 1) + 4 * e, hA = 2 * t;
-    T *out = static_cast<T *>(A.out) + (static_cast<int64_t>(b) * A.Hq + kh * A.G + sub * kI4Heads + hA) * D + d;
-    out[0] = from_f32<T>(acc[0] * i0);
-    out[2] = from_f32<T>(acc[2] * i0);
-    if (hA + 1 < heads) {
-        out[D] = from_f32<T>(acc[1] * i1);
-        out[D + 2] = from_f32<T>(acc[3] * i1);
+    float M = -INFINITY, L = 0.f, acc[V] = {};
+    for (int w = from + sub_warp; w <= to; w += U * WPR) {
+        F v[U][FN];
+        float2 ml[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const bool in = w + i * WPR <= to;
+            const int64_t piece = (w + i * WPR + u) * A.rows + r;
+            ml[i] = in ? __ldg(A.ml_piece + piece) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int k = 0; k < FN; ++k) v[i][k] = in ? __ldg(reinterpret_cast<const F *>(A.o_piece + piece * D) + lane * FN + k) : F{};
+        }
+        float n = M;
+#pragma unroll
+        for (int i = 0; i < U; ++i) n = fmaxf(n, ml[i].x);
+        const float base = n == -INFINITY ? 0.f : n, a = exp2f(M - base);
+        M = n;
+        L *= a;
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] *= a;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const float f = exp2f(ml[i].x - base);
+            L = fmaf(f, ml[i].y, L);
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] = fmaf(f, reinterpret_cast<const float *>(v[i])[k], acc[k]);
+        }
     }
+    if constexpr (WPR > 1) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) part[warp][lane * V + k] = acc[k];
+        if (lane == 0) part_ml[warp] = make_float2(M, L);
+        __syncthreads();
+        if (sub_warp != 0) return;
+        M = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) M = fmaxf(M, part_ml[warp + i].x);
+        const float base = M == -INFINITY ? 0.f : M;
+        L = 0.f;
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) {
+            const float f = exp2f(part_ml[warp + i].x - base);
+            L = fmaf(f, part_ml[warp + i].y, L);
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[k] = fmaf(f, part[warp + i][lane * V + k], acc[k]);
+        }
+    }
+    if (to < from) return;
+    const float inv = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
+    uint32_t o[V / 2];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) o[k] = Half16<T>::pack(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(A.out) + out_row * D) + lane * (V / 2);
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) dst[k] = o[k];
 }
 
 // ----------------------------------------------------------------------------- host side
 struct I4Plan {
-    int32_t subs = 1, group = 0;  // units of a KV head, sequences of a launch
+    int32_t subs = 1, rows = 0, group = 0;  // units of a KV head, query heads of a unit at most, sequences of a launch
     int64_t units = 0;            // of a launch
     size_t o_bytes = 0, ml_bytes = 0, ws_bytes = 0;
 };
@@ -617,20 +728,22 @@ bool i4_shape(int32_t d) { return d == 64 || d == 128 || d == 256; }
 I4Plan i4_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t d) {
     I4Plan p;
     p.subs = (Hq / Hkv + kI4Heads - 1) / kI4Heads;
+    p.rows = Hq / Hkv < kI4Heads ? Hq / Hkv : kI4Heads;
     p.group = B < kI4MaxSeqs ? B : kI4MaxSeqs;
     p.units = static_cast<int64_t>(p.group) * Hkv * p.subs;
     const int64_t slots = kI4MaxWarps + p.units;
-    p.o_bytes = static_cast<size_t>(slots) * d * kI4Heads * sizeof(float);
-    p.ml_bytes = static_cast<size_t>(slots) * kI4Heads * sizeof(float2);
+    p.o_bytes = static_cast<size_t>(slots) * p.rows * d * sizeof(float);
+    p.ml_bytes = (static_cast<size_t>(slots) * p.rows * sizeof(float2) + 255) / 256 * 256;
     p.ws_bytes = p.o_bytes + p.ml_bytes + (static_cast<size_t>(p.units) * sizeof(int2) + 255) / 256 * 256;
     return p;
 }
 
 template <typename T, int D, bool MOD>
 cudaError_t i4_launch(const I4Args &a, const I4Plan &p, cudaStream_t stream) {
-    constexpr int WARPS = 4, STAGES = D == 256 ? 2 : 3, CTAS = D == 256 ? 2 : 3;
-    constexpr int smem = WARPS * STAGES * I4Ring<D>::kStage + (kI4MaxSeqs + 1) * 8 + kI4MaxSeqs * 8;
-    auto kern = decode_int4_kernel<T, D, WARPS, STAGES, CTAS, MOD>;
+    constexpr int STEP = D == 256 ? 32 : 64, WARPS = 4, CTAS = D == 256 ? 2 : D == 128 ? 3 : 4;
+    constexpr int smem = WARPS * I4Tile<D, STEP>::kWarp;
+    static_assert(smem >= (kI4MaxSeqs + 1) * 8 + kI4MaxSeqs * 4, "the prefix lies in the tiles");
+    auto kern = decode_int4_kernel<T, D, STEP, WARPS, CTAS, MOD>;
     static std::atomic<int> grids[64];  // resident CTAs, per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -649,9 +762,13 @@ cudaError_t i4_launch(const I4Args &a, const I4Plan &p, cudaStream_t stream) {
     }
     e = launch_pdl(kPdlDecode, kern, dim3(grid), dim3(WARPS * 32), smem, stream, a);
     if (e != cudaSuccess) return e;
-    const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * a.subs, items = units * (D / 16);
-    return launch_pdl(kPdlCombine, decode_int4_join_kernel<T, D>, dim3(static_cast<unsigned>((items + kI4JoinWarps - 1) / kI4JoinWarps)),
-                      dim3(kI4JoinWarps * 32), 0, stream, a, units);
+    const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv * a.subs * a.rows;
+    int wpr = kI4JoinWarps;
+    while (wpr > 1 && rows * wpr > kI4JoinTarget) wpr >>= 1;
+    const int64_t per = kI4JoinWarps / wpr;
+    auto join = wpr == 8 ? decode_int4_join_kernel<T, D, 8> : wpr == 4 ? decode_int4_join_kernel<T, D, 4>
+              : wpr == 2 ? decode_int4_join_kernel<T, D, 2> : decode_int4_join_kernel<T, D, 1>;
+    return launch_pdl(kPdlCombine, join, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kI4JoinWarps * 32), 0, stream, a, rows);
 }
 
 template <typename T, bool MOD>
@@ -683,7 +800,7 @@ extern "C" pkv_status pkv_paged_attention_decode_int4(
         return set_error(PKV_ERR_INVALID_ARG, "int4 decode: num_q_heads (%d) is not a multiple of num_kv_heads (%d)", num_q_heads, num_kv_heads);
     if (static_cast<int64_t>(num_blocks) * block_size > INT32_MAX)
         return set_error(PKV_ERR_INVALID_ARG, "int4 decode: num_blocks * block_size >= 2^31");
-    if (max_context_len > INT32_MAX - kI4Step) return set_error(PKV_ERR_INVALID_ARG, "int4 decode: max_context_len is too long");
+    if (max_context_len > INT32_MAX - 64) return set_error(PKV_ERR_INVALID_ARG, "int4 decode: max_context_len is too long");
     const pkv_score_mod none{};
     const pkv_score_mod m = mod ? *mod : none;
     if (!(m.softcap >= 0.f) || m.softcap > 1e30f || (m.softcap > 0.f && m.softcap < 1e-30f))
@@ -712,6 +829,7 @@ extern "C" pkv_status pkv_paged_attention_decode_int4(
     a.Hkv = num_kv_heads;
     a.G = num_q_heads / num_kv_heads;
     a.subs = p.subs;
+    a.rows = p.rows;
     a.bs = block_size;
     a.num_blocks = num_blocks;
     a.max_ctx = max_context_len;
@@ -722,7 +840,8 @@ extern "C" pkv_status pkv_paged_attention_decode_int4(
     a.ml_piece = reinterpret_cast<float2 *>(ws + p.o_bytes);
     a.unit_info = reinterpret_cast<int2 *>(ws + p.o_bytes + p.ml_bytes);
     a.err_flag = err_flag;
-    const bool rules = m.softcap > 0.f || m.alibi_slopes || m.key_starts;
+    // without rules the score's factor goes into the exponent, which wants it positive
+    const bool rules = m.softcap > 0.f || m.alibi_slopes || m.key_starts || !(scale > 1e-30f);
     for (int32_t b0 = 0; b0 < num_seqs; b0 += p.group) {  // consecutive launches, one workspace
         const int64_t at = static_cast<int64_t>(b0) * num_q_heads * head_dim * 2;
         a.out = static_cast<char *>(out) + at;

@@ -7,6 +7,9 @@ of the f32 accumulator.  A group of 32 dims is two instructions; each may cut it
 of its largest term or partial sum, at most 1200 sum |q| over the group: together 2 x 1200 x
 2^-22 < 2^-10 sum |q|, in code steps.  With scales up to s the score is off by at most
 scale s 2^-10 sum |q| more.
+P is rounded to float16 twice, by itself and times V's scale, and not in the row sum: the same
+two half steps.  Below float16's normal range p s is off by 2^-25 and its codes are up to 7: that
+term is 2^-25 keys max(8, |V|), with p at least 1 for the key that set the reference.
 """
 import pytest
 import torch
@@ -46,7 +49,7 @@ def check(got, q, caches, want, scale):
     s_max = float(torch.nan_to_num(caches[2].float()).abs().max())
     score = sr.SCORE + scale * s_max * 2.0 ** -10 * q.double().abs().sum(-1).max().item()
     out, mag, keys = want
-    v_max = 8 * float(torch.nan_to_num(caches[3].float()).abs().max())
+    v_max = 8 * max(1.0, float(torch.nan_to_num(caches[3].float()).abs().max()))
     tol = sr.tolerance(want, got.dtype, F16, v_max) + 2 * (score - sr.SCORE) * mag
     err = (got.cpu().double() - out).abs()
     assert torch.isfinite(got).all()
@@ -132,6 +135,23 @@ def test_magnitudes(pkv, cuda_dev, gain):
     scale = 128 ** -0.5 / gain
     out = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, torch.tensor(ctx, dtype=torch.int32).cuda(), scale, 200)
     check(out, q, caches, reference(q, caches, tables, ctx, scale), scale)
+
+
+@pytest.mark.parametrize("top", [30.0, 3000.0, 65408.0])
+def test_large_values(pkv, cuda_dev, top):
+    """V up to the largest that the format holds: P times its scale stays in float16's range."""
+    n, Hkv, d = 150, 2, 128
+    g = torch.Generator().manual_seed(4)
+    key, value = torch.randn(n, Hkv, d, generator=g), torch.rand(n, Hkv, d, generator=g) * 2 - 1
+    value[:, :, ::32] = 1.0
+    caches = ref.empty_cache(10, Hkv, 16, d, 4, cuda_dev)
+    slots = torch.arange(n, dtype=torch.int32).cuda()
+    pkv.pkv_store_kvcache_int4(key.cuda(), (value * top).cuda(), *caches, slots)
+    # rising scores: every later key may exceed the reference
+    q = (key[-1].repeat_interleave(4, 0)[None] * 2).to(BF16).cuda()
+    tables = torch.arange(10, dtype=torch.int32).cuda()[None]
+    out = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, torch.tensor([n], dtype=torch.int32).cuda(), d ** -0.5, n)
+    check(out, q, caches, reference(q, caches, tables, [n], d ** -0.5), d ** -0.5)
 
 
 def test_empty_batch(pkv, cuda_dev):
