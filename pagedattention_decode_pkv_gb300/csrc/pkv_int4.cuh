@@ -27,21 +27,22 @@ namespace {
 constexpr int kInt4Group = 32;         // dims that share a scale
 constexpr float kInt4TopScale = 9344.f;
 
-// The bf16 nearest to top / 7 (ties to even) for top >= 0, exactly: the f32 quotient may have
-// been rounded onto a midpoint, the remainder of the midpoint says on which side it was.
+// The bf16 nearest to top / 7 (ties to even) for top >= 0, exactly: the remainder of a midpoint
+// says on which side of it the quotient is, and an f32 product off by a few 2^-24 always finds
+// the midpoint that matters.
 __device__ __forceinline__ float int4_seventh_bf16(float top, float &mid) {
-    const uint32_t lo = __float_as_uint(__fdiv_rn(top, 7.f)) & 0xffff0000u;
+    const uint32_t lo = __float_as_uint(top * 0.14285714924335479736328125f) & 0xffff0000u;
     mid = __uint_as_float(lo | 0x8000u);
     const float side = fmaf(-7.f, mid, top);
     const bool up = side > 0.f || (side == 0.f && (lo & 0x10000u));
     return __uint_as_float(up ? lo + 0x10000u : lo);
 }
 
-// The stored scale of a group whose largest magnitude is `top` (NaN left out by the caller).
-__device__ __forceinline__ __half int4_scale(float top) {
-    if (!(top < 3e38f)) return __float2half_rn(kInt4TopScale);
-    float mid;
-    return __float2half_rn(fminf(int4_seventh_bf16(top, mid), kInt4TopScale));
+// The stored scale of a group whose largest magnitude is `top` (NaN left out by the caller), and
+// the midpoint of two bf16 values nearest to top / 7.
+__device__ __forceinline__ __half int4_scale(float top, float &mid) {
+    const float s = int4_seventh_bf16(fminf(top, 3e38f), mid);
+    return __float2half_rn(fminf(s, kInt4TopScale));
 }
 
 // Code of x under the scale s > 0: the integer nearest to x / s, ties to even, within +-7,

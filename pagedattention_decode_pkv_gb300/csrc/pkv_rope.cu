@@ -26,6 +26,7 @@
 
 #include "pkv_int4.cuh"
 #include "pkv_internal.h"
+#include "pkv_pack.cuh"
 #include "pkv_pdl.cuh"
 
 namespace pkv {
@@ -129,6 +130,51 @@ __device__ __forceinline__ int int4_code_f64(double x, float s) {
     return static_cast<int>(fmin(fmax(rint(x / static_cast<double>(s)), -7.0), 7.0));
 }
 
+// The largest magnitude of eight values, NaN if one is.
+__device__ __forceinline__ float max_abs8(const float (&x)[8]) {
+    float m = fabsf(x[0]);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(x[1])));
+#pragma unroll
+    for (int k = 2; k < 8; k += 2) asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(x[k])), "f"(fabsf(x[k + 1])));
+    return m;
+}
+
+// The word of eight values (no NaN, none beyond 7 s) under the scale s (inv = 1 / s, 0 for a zero
+// scale), two values an operation.  `snap` 384 rounds x inv to multiples of 2^-15 first: of 16-bit
+// values (11 bits over the scale's 8) a quotient is a tie or 2^-13 away from one, and a tie may
+// come out of the rounded inv a little off it; then it is one again and goes to even.  With 0 a
+// product next to a border may fall to either side: `near` becomes the smallest distance of
+// |x - c s| from half a step.
+template <bool NEAR>
+__device__ __forceinline__ uint32_t int4_word(const float (&x)[8], float s, float inv, float snap, float &near) {
+    const uint64_t inv2 = splat2(inv), on = splat2(snap), off = splat2(-snap);
+    const uint64_t magic = splat2(12582912.f), back = splat2(-12582912.f);  // 1.5 x 2^23: a sum with it is an integer
+    uint64_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint64_t v = pack2(x[2 * j], x[2 * j + 1]);
+        c[j] = add2(add2(add2(fma2(v, inv2, on), off), magic), back);
+        if constexpr (NEAR) {
+            float r0, r1;
+            unpack2(fma2(c[j], splat2(-s), v), r0, r1);
+            near = fminf(near, fminf(fabsf(fabsf(r0) - 0.5f * s), fabsf(fabsf(r1) - 0.5f * s)));
+        }
+    }
+    // both halves of the word at once: nibble j is dim 2 j below and dim 2 j + 1 above; 0x8888: all + 8
+    const uint64_t u = add2(fma2(c[3], splat2(4096.f), fma2(c[2], splat2(256.f), fma2(c[1], splat2(16.f), c[0]))), splat2(34952.f));
+    float lo, hi;
+    unpack2(u, lo, hi);
+    return static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
+}
+
+// Nibble k of w, one of the two codes next to z / s, to the right one.
+__device__ __forceinline__ void int4_settle(uint32_t &w, int k, double z, float s) {
+    const int c = static_cast<int>(w >> int4_shift(k) & 15) - 8;
+    const double r = fma(-static_cast<double>(c), static_cast<double>(s), z), h = 0.5 * s;
+    const int to = c + (r > 0.0 ? 1 : -1);  // (values that saturate stay where they are)
+    if ((fabs(r) > h || (fabs(r) == h && (c & 1))) && to >= -7 && to <= 7) w += static_cast<uint32_t>(to - c) << int4_shift(k);
+}
+
 // Whether x lies within `err` of the border between two codes under s.
 __device__ __forceinline__ bool int4_near_border(float x, float s, int code, float err) {
     const float r = fmaf(-static_cast<float>(code), s, x);
@@ -142,9 +188,9 @@ __device__ __forceinline__ bool int4_near_border(float x, float s, int code, flo
 // dims are 2 lanes or twice 4 lanes, so a rotation never leaves a lane and a group's maximum
 // takes one or two shuffles.
 template <typename T, bool INTER, bool Q4>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 4)
 rope_store_kernel(const __grid_constant__ RopeArgs A) {
-    constexpr int U = sizeof(T) == 2 ? 4 : 2;  // steps in flight
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;  // steps in flight of the queries
     __shared__ __align__(16) float2 table[kRopeWarps][kRopeMaxDim / 2];
     pdl_wait();
     pdl_trigger();
@@ -173,204 +219,245 @@ rope_store_kernel(const __grid_constant__ RopeArgs A) {
         const bool stored = slot >= 0 && slot < A.num_slots;
         if (slot != -1 && !stored && s0 <= nq && nq < s1 && lane == 0 && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_SLOT_RANGE);
         const int32_t position = r > 0 ? A.positions[i] : 0;
-        const int64_t block = Q4 ? slot / A.bs : 0;
-        const int64_t row0 = Q4 ? block * A.Hkv * A.bs + (slot - block * A.bs) : static_cast<int64_t>(slot) * A.Hkv;
         float cs[8], sn[8];  // of pairs 8 l + k
         bool have = false;
-        for (int sb = s0; sb < s1; sb += U) {
-            Eight<T> x0[U], x1[U];
+        auto angles = [&] {  // the token's, while the first loads are under way
+            if (have || r == 0 || s0 >= nq + nk) return;
+            have = true;
+            __syncwarp();
+            for (int p = lane; 2 * p < r; p += 32) {
+                const float2 t = turn_cos_sin(position, A.turns[p]);
+                table[warp][p] = make_float2(t.x * A.amp, t.y * A.amp);
+            }
+            __syncwarp();
+            if (rot0 && on) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int s = sb + u, role = s < nq ? 0 : s < nq + nk ? 1 : 2;
-                const int h = (role == 0 ? s : role == 1 ? s - nq : s - nq - nk) * hpw + hl;
-                const bool live = on && s < s1 && h < (role == 0 ? A.Hq : A.Hkv) && (role == 0 || stored);
-                const T *src = role == 0 ? static_cast<const T *>(A.q) + i * A.q_stride
-                             : role == 1 ? static_cast<const T *>(A.key) + i * A.k_stride
-                                         : static_cast<const T *>(A.value) + i * A.v_stride;
-                if (live) {
-                    x0[u].load(src + static_cast<int64_t>(h) * d + 8 * c0);
-                    x1[u].load(src + static_cast<int64_t>(h) * d + 8 * c1);
+                for (int k = 0; k < 8; ++k) {
+                    const float2 t = table[warp][8 * l + k];  // past the last pair (r / 2 not whole lanes): not used
+                    cs[k] = t.x;
+                    sn[k] = t.y;
+                }
+            }
+        };
+        // (a, b), the lane's two chunks, -> (y0, y1)
+        auto turn = [&](const float (&a)[8], const float (&b)[8], bool turned, float (&y0)[8], float (&y1)[8]) {
+            if (turned) {
+                if constexpr (INTER) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        y0[2 * k] = fmaf(a[2 * k], cs[k], -(a[2 * k + 1] * sn[k]));
+                        y0[2 * k + 1] = fmaf(a[2 * k + 1], cs[k], a[2 * k] * sn[k]);
+                        y1[2 * k] = rot1 ? fmaf(b[2 * k], cs[4 + k], -(b[2 * k + 1] * sn[4 + k])) : b[2 * k];
+                        y1[2 * k + 1] = rot1 ? fmaf(b[2 * k + 1], cs[4 + k], b[2 * k] * sn[4 + k]) : b[2 * k + 1];
+                    }
                 } else {
-                    x0[u].clear();
-                    x1[u].clear();
-                }
-            }
-            if (!have && r > 0 && s0 < nq + nk) {  // the token's angles, while the first loads are under way
-                __syncwarp();
-                for (int p = lane; 2 * p < r; p += 32) {
-                    const float2 t = turn_cos_sin(position, A.turns[p]);
-                    table[warp][p] = make_float2(t.x * A.amp, t.y * A.amp);
-                }
-                __syncwarp();
-                if (rot0 && on) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float2 t = table[warp][8 * l + k];  // past the last pair (r / 2 not whole lanes): not used
-                        cs[k] = t.x;
-                        sn[k] = t.y;
+                    for (int k = 0; k < 8; k += 2) {  // two pairs an operation
+                        const uint64_t va = pack2(a[k], a[k + 1]), vb = pack2(b[k], b[k + 1]);
+                        const uint64_t c = pack2(cs[k], cs[k + 1]), n = pack2(sn[k], sn[k + 1]);
+                        unpack2(fma2(va, c, mul2(vb, pack2(-sn[k], -sn[k + 1]))), y0[k], y0[k + 1]);
+                        unpack2(fma2(vb, c, mul2(va, n)), y1[k], y1[k + 1]);
                     }
                 }
-                have = true;
-            }
+            } else {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int s = sb + u, role = s < nq ? 0 : s < nq + nk ? 1 : 2;
-                if (s >= s1 || (role != 0 && !stored)) continue;
-                const int h = (role == 0 ? s : role == 1 ? s - nq : s - nq - nk) * hpw + hl;
-                const bool live = on && h < (role == 0 ? A.Hq : A.Hkv);
-                const bool turned = role != 2 && rot0;  // this lane's first chunk (and in halves the second) is rotated
-                if (!Q4 && (role == 2 || !turned)) {    // as it is
-                    if (live) {
-                        T *dst = role == 0 ? static_cast<T *>(A.q_out) + (i * A.Hq + h) * d
-                                           : static_cast<T *>(role == 1 ? A.k_cache : A.v_cache) + (row0 + h) * d;
-                        x0[u].store(dst + 8 * c0);
-                        x1[u].store(dst + 8 * c1);
-                    }
-                    continue;
+                for (int k = 0; k < 8; ++k) {
+                    y0[k] = a[k];
+                    y1[k] = b[k];
                 }
-                float a[8], b[8], y0[8], y1[8];
-                x0[u].get(a);
-                x1[u].get(b);
-                float mag = 0.f;  // largest |x_a| + |x_b| of the lane's rotated pairs
-                if (turned) {
-                    if constexpr (INTER) {
+            }
+        };
+        const int64_t lane_at = static_cast<int64_t>(hl) * d;  // the lane's head of a step of hpw heads
+        const int hop = hpw * d;
+        // Steps [from, to) of a token's `heads` heads from src to dst, rotated or as they are.
+        auto stream = [&](const T *src, T *dst, int heads, int from, int to, bool turned) {
+            for (int sb = from; sb < to; sb += U) {
+                Eight<T> x0[U], x1[U];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            y0[2 * k] = fmaf(a[2 * k], cs[k], -(a[2 * k + 1] * sn[k]));
-                            y0[2 * k + 1] = fmaf(a[2 * k + 1], cs[k], a[2 * k] * sn[k]);
-                            mag = fmaxf(mag, fabsf(a[2 * k]) + fabsf(a[2 * k + 1]));
-                            y1[2 * k] = rot1 ? fmaf(b[2 * k], cs[4 + k], -(b[2 * k + 1] * sn[4 + k])) : b[2 * k];
-                            y1[2 * k + 1] = rot1 ? fmaf(b[2 * k + 1], cs[4 + k], b[2 * k] * sn[4 + k]) : b[2 * k + 1];
-                            if (rot1) mag = fmaxf(mag, fabsf(b[2 * k]) + fabsf(b[2 * k + 1]));
-                        }
+                for (int u = 0; u < U; ++u) {
+                    if (sb + u < to && (sb + u) * hpw + hl < heads && on) {
+                        const T *p = src + static_cast<int64_t>(sb + u) * hop;
+                        x0[u].load(p + 8 * c0);
+                        x1[u].load(p + 8 * c1);
                     } else {
+                        x0[u].clear();
+                        x1[u].clear();
+                    }
+                }
+                angles();
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            y0[k] = fmaf(a[k], cs[k], -(b[k] * sn[k]));
-                            y1[k] = fmaf(b[k], cs[k], a[k] * sn[k]);
-                            mag = fmaxf(mag, fabsf(a[k]) + fabsf(b[k]));
+                for (int u = 0; u < U; ++u) {
+                    if (sb + u < to && (sb + u) * hpw + hl < heads && on) {
+                        if (turned) {  // (in halves both of the lane's chunks)
+                            float a[8], b[8], y0[8], y1[8];
+                            x0[u].get(a);
+                            x1[u].get(b);
+                            turn(a, b, true, y0, y1);
+                            x0[u].put(y0);
+                            x1[u].put(y1);
+                        }
+                        T *p = dst + static_cast<int64_t>(sb + u) * hop;
+                        x0[u].store(p + 8 * c0);
+                        x1[u].store(p + 8 * c1);
+                    }
+                }
+            }
+        };
+        if (s0 < nq)
+            stream(static_cast<const T *>(A.q) + i * A.q_stride + lane_at, static_cast<T *>(A.q_out) + i * A.Hq * d + lane_at, A.Hq, s0,
+                   min(s1, nq), rot0);
+        if (!stored || s1 <= nq) continue;
+        const T *key = static_cast<const T *>(A.key) + i * A.k_stride + lane_at;
+        const T *value = static_cast<const T *>(A.value) + i * A.v_stride + lane_at;
+        if constexpr (!Q4) {
+            const int64_t at = static_cast<int64_t>(slot) * A.Hkv * d + lane_at;
+            stream(key, static_cast<T *>(A.k_cache) + at, A.Hkv, max(s0 - nq, 0), min(s1 - nq, nk), rot0);
+            stream(value, static_cast<T *>(A.v_cache) + at, A.Hkv, max(s0 - nq - nk, 0), s1 - nq - nk, false);
+        } else {
+            // Keys and values into codes, the next step's loads under way.  One copy of the code:
+            // unrolled over steps it outgrows the instruction caches (32700 tokens of 32 + 2 x 8
+            // heads: four copies 394 us with the rows read back, two 274, at that step).
+            const int64_t block = slot / A.bs, row0 = block * A.Hkv * A.bs + (slot - block * A.bs);
+            Eight<T> n0, n1;
+            auto load = [&](int e) {  // step e of the keys, then of the values
+                const int step = e < nk ? e : e - nk;
+                if (on && step * hpw + hl < A.Hkv) {
+                    const T *p = (e < nk ? key : value) + static_cast<int64_t>(step) * hop;
+                    n0.load(p + 8 * c0);
+                    n1.load(p + 8 * c1);
+                } else {
+                    n0.clear();
+                    n1.clear();
+                }
+            };
+            const int last = s1 - nq;
+            load(max(s0 - nq, 0));
+            angles();
+#pragma unroll 1
+            for (int e = max(s0 - nq, 0); e < last; ++e) {
+                const int role = e < nk ? 1 : 2, h = (e < nk ? e : e - nk) * hpw + hl;
+                const bool live = on && h < A.Hkv, turned = role == 1 && rot0;
+                float a[8], b[8], y0[8], y1[8];
+                n0.get(a);
+                n1.get(b);
+                if (e + 1 < last) load(e + 1);
+                turn(a, b, turned, y0, y1);
+                constexpr int kReach = INTER ? 2 : 4;  // lanes of a group
+                const bool loose0 = turned, loose1 = turned && rot1;  // rotated: off by up to err
+                // largest magnitudes; NaN are zeros (seldom there: the maximum keeps them)
+                float top0 = max_abs8(y0), top1 = max_abs8(y1);
+                if (__any_sync(0xffffffffu, top0 != top0 || top1 != top1)) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        y0[k] = y0[k] == y0[k] ? y0[k] : 0.f;
+                        y1[k] = y1[k] == y1[k] ? y1[k] : 0.f;
+                    }
+                    top0 = max_abs8(y0);
+                    top1 = max_abs8(y1);
+                }
+                if constexpr (INTER) top0 = top1 = fmaxf(top0, top1);
+#pragma unroll
+                for (int o = 1; o < kReach; o <<= 1) {
+                    top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
+                    if (!INTER) top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
+                }
+                if (INTER) top1 = top0;
+                // |x_a| + |x_b| of a pair is at most sqrt(2) times its norm, which the turn keeps
+                // and which the groups' maxima bound; A is in them
+                const float err = turned ? 1.42f * kRotError * (top0 + top1) : 0.f;
+                float far = err;  // of the group
+                if (INTER) far = fmaxf(far, __shfl_xor_sync(0xffffffffu, far, 1));
+                float m0, m1;
+                __half h0 = int4_scale(top0, m0), h1 = h0;
+                if (INTER) m1 = m0;
+                else h1 = int4_scale(top1, m1);
+                const bool unsure0 = far > 0.f && fabsf(fmaf(-7.f, m0, top0)) <= far;
+                const bool unsure1 = !INTER && far > 0.f && fabsf(fmaf(-7.f, m1, top1)) <= far;
+                // The pair k of the lane (its elements in y0, y1) in f64.
+                auto exact = [&](int k) -> double2 {
+                    const float xa = !INTER ? a[k] : k < 4 ? a[2 * (k & 3)] : b[2 * (k & 3)];
+                    const float xb = !INTER ? b[k] : k < 4 ? a[2 * (k & 3) + 1] : b[2 * (k & 3) + 1];
+                    return (INTER && k >= 4 ? loose1 : loose0) ? rotate_exact(position, A.turns[8 * l + k], A.amplitude, xa, xb)
+                                                               : make_double2(xa, xb);
+                };
+                if (__any_sync(0xffffffffu, unsure0 || unsure1)) {  // a maximum next to the border of two scales
+                    double g0 = 0.0, g1 = 0.0;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float ya = !INTER ? y0[k] : k < 4 ? y0[2 * (k & 3)] : y1[2 * (k & 3)];
+                        const float yb = !INTER ? y1[k] : k < 4 ? y0[2 * (k & 3) + 1] : y1[2 * (k & 3) + 1];
+                        const bool pa = unsure0 && fabsf(ya) >= top0 - 2.f * far;
+                        const bool pb = INTER ? unsure0 && fabsf(yb) >= top0 - 2.f * far : unsure1 && fabsf(yb) >= top1 - 2.f * far;
+                        if (__any_sync(0xffffffffu, pa || pb)) {
+                            const double2 z = exact(k);
+                            if (pa) g0 = fmax(g0, fabs(z.x));
+                            if (pb && INTER) g0 = fmax(g0, fabs(z.y));
+                            if (pb && !INTER) g1 = fmax(g1, fabs(z.y));
                         }
                     }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        y0[k] = a[k];
-                        y1[k] = b[k];
-                    }
-                }
-                if (!Q4 || role == 0) {
-                    if (live) {
-                        T *dst = role == 0 ? static_cast<T *>(A.q_out) + (i * A.Hq + h) * d
-                                           : static_cast<T *>(A.k_cache) + (row0 + h) * d;
-                        x0[u].put(y0);
-                        x1[u].put(y1);
-                        x0[u].store(dst + 8 * c0);
-                        x1[u].store(dst + 8 * c1);
-                    }
-                    continue;
-                }
-                if constexpr (Q4) {
-                    // scales of the lane's groups, then eight codes a chunk
-                    float top0 = 0.f, top1 = 0.f, err = mag * fabsf(A.amp) * kRotError;  // 0 where nothing was rotated
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        top0 = fmaxf(top0, fabsf(y0[k]));
-                        top1 = fmaxf(top1, fabsf(y1[k]));
-                    }
-                    if constexpr (INTER) top0 = top1 = fmaxf(top0, top1);
-                    constexpr int kReach = INTER ? 2 : 4;  // lanes of a group
 #pragma unroll
                     for (int o = 1; o < kReach; o <<= 1) {
-                        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
-                        top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
-                        err = fmaxf(err, __shfl_xor_sync(0xffffffffu, err, o));
+                        g0 = fmax(g0, __shfl_xor_sync(0xffffffffu, g0, o));
+                        if (!INTER) g1 = fmax(g1, __shfl_xor_sync(0xffffffffu, g1, o));
                     }
-                    __half h0 = int4_scale(top0), h1 = int4_scale(top1);
-                    float m0, m1;
-                    int4_seventh_bf16(top0, m0);
-                    int4_seventh_bf16(top1, m1);
-                    bool unsure = err > 0.f && (fabsf(fmaf(-7.f, m0, top0)) <= err || fabsf(fmaf(-7.f, m1, top1)) <= err);
-                    float t0 = __half2float(h0), t1 = __half2float(h1);
-                    uint32_t w0 = 0, w1 = 0;
-                    {
-                        const float i0 = 1.f / t0, i1 = 1.f / t1;
+                    if (unsure0) h0 = int4_scale_f64(g0);
+                    if (unsure1) h1 = int4_scale_f64(g1);
+                    if (INTER) h1 = h0;
+                }
+                const float t0 = __half2float(h0), t1 = __half2float(h1);
+                if (__any_sync(0xffffffffu, top0 > 7.5f * t0 || top1 > 7.5f * t1)) {  // saturated groups, or too small for a scale
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int e0 = t0 > 0.f ? int4_code(y0[k], t0, i0) : 0, e1 = t1 > 0.f ? int4_code(y1[k], t1, i1) : 0;
-                            unsure = unsure || (err > 0.f && (int4_near_border(y0[k], t0, e0, err) || int4_near_border(y1[k], t1, e1, err)));
-                            w0 |= static_cast<uint32_t>(e0 + 8) << int4_shift(k);
-                            w1 |= static_cast<uint32_t>(e1 + 8) << int4_shift(k);
-                        }
+                    for (int k = 0; k < 8; ++k) {
+                        y0[k] = fminf(fmaxf(y0[k], -7.f * t0), 7.f * t0);
+                        y1[k] = fminf(fmaxf(y1[k], -7.f * t1), 7.f * t1);
                     }
-                    if (__any_sync(0xffffffffu, unsure)) {  // again in f64
-                        double z0[8], z1[8], g0 = 0.0, g1 = 0.0;
-#pragma unroll 1
-                        for (int k = 0; k < 8; ++k) {  // pair k of the lane
-                            // (selected, so that the arrays stay in registers)
-                            float xa = 0.f, xb = 0.f;
+                }
+                const float i0 = t0 > 0.f ? __frcp_rn(t0) : 0.f, i1 = t1 > 0.f ? __frcp_rn(t1) : 0.f;
+                float gap0 = 3e38f, gap1 = 3e38f;
+                uint32_t w0, w1;
+                constexpr bool kWide = sizeof(T) == 4;
+                if (kWide || role == 1) {
+                    w0 = int4_word<true>(y0, t0, i0, kWide || loose0 ? 0.f : 384.f, gap0);
+                    w1 = int4_word<true>(y1, t1, i1, kWide || loose1 ? 0.f : 384.f, gap1);
+                } else {
+                    w0 = int4_word<false>(y0, t0, i0, 384.f, gap0);
+                    w1 = int4_word<false>(y1, t1, i1, 384.f, gap1);
+                }
+                // rotated (and f32) values next to the border of two codes: 2^-18 s for x inv
+                const float e0 = fmaf(t0, 3.8e-6f, loose0 ? err : 0.f), e1 = fmaf(t1, 3.8e-6f, loose1 ? err : 0.f);
+                const bool border0 = (kWide || loose0) && t0 > 0.f && gap0 <= e0, border1 = (kWide || loose1) && t1 > 0.f && gap1 <= e1;
+                if (__any_sync(0xffffffffu, border0 || border1)) {
+                    uint32_t near0 = 0, near1 = 0;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                if (INTER) {
-                                    const float lo = e < 4 ? a[2 * (e & 3)] : b[2 * (e & 3)], hi = e < 4 ? a[2 * (e & 3) + 1] : b[2 * (e & 3) + 1];
-                                    xa = e == k ? lo : xa;
-                                    xb = e == k ? hi : xb;
-                                } else {
-                                    xa = e == k ? a[e] : xa;
-                                    xb = e == k ? b[e] : xb;
-                                }
-                            }
-                            const bool spin = turned && (!INTER || k < 4 || rot1);
-                            const double2 z = spin ? rotate_exact(position, A.turns[8 * l + k], A.amplitude, xa, xb)
-                                                   : make_double2(xa, xb);
+                    for (int k = 0; k < 8; ++k) {
+                        if (border0 && int4_near_border(y0[k], t0, static_cast<int>(w0 >> int4_shift(k) & 15) - 8, e0)) near0 |= 1u << k;
+                        if (border1 && int4_near_border(y1[k], t1, static_cast<int>(w1 >> int4_shift(k) & 15) - 8, e1)) near1 |= 1u << k;
+                    }
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                if (INTER) {
-                                    if ((e >> 1) == (k & 3)) {
-                                        if (k < 4) z0[e] = e & 1 ? z.y : z.x;
-                                        else z1[e] = e & 1 ? z.y : z.x;
-                                    }
-                                } else if (e == k) {
-                                    z0[e] = z.x;
-                                    z1[e] = z.y;
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            g0 = fmax(g0, fabs(z0[e]));
-                            g1 = fmax(g1, fabs(z1[e]));
-                        }
-                        if constexpr (INTER) g0 = g1 = fmax(g0, g1);
-#pragma unroll
-                        for (int o = 1; o < kReach; o <<= 1) {
-                            g0 = fmax(g0, __shfl_xor_sync(0xffffffffu, g0, o));
-                            g1 = fmax(g1, __shfl_xor_sync(0xffffffffu, g1, o));
-                        }
-                        h0 = int4_scale_f64(g0);
-                        h1 = int4_scale_f64(g1);
-                        t0 = __half2float(h0);
-                        t1 = __half2float(h1);
-                        w0 = w1 = 0;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int e0 = t0 > 0.f ? int4_code_f64(z0[k], t0) : 0, e1 = t1 > 0.f ? int4_code_f64(z1[k], t1) : 0;
-                            w0 |= static_cast<uint32_t>(e0 + 8) << int4_shift(k);
-                            w1 |= static_cast<uint32_t>(e1 + 8) << int4_shift(k);
+                    for (int k = 0; k < 8; ++k) {
+                        // bits of the pair's two elements
+                        const int ea = !INTER ? k : 2 * (k & 3), eb = !INTER ? k : ea + 1;
+                        const uint32_t na = !INTER || k < 4 ? near0 : near1, nb = !INTER ? near1 : na;
+                        if (__any_sync(0xffffffffu, (na >> ea & 1) || (nb >> eb & 1))) {
+                            const double2 z = exact(k);
+                            const bool second = INTER && k >= 4;
+                            if (na >> ea & 1) int4_settle(second ? w1 : w0, ea, z.x, second ? t1 : t0);
+                            if (nb >> eb & 1) int4_settle(!INTER || second ? w1 : w0, eb, z.y, !INTER || second ? t1 : t0);
                         }
                     }
-                    if (live) {
-                        const int64_t row = row0 + static_cast<int64_t>(h) * A.bs;
-                        uint32_t *codes = static_cast<uint32_t *>(role == 1 ? A.k_cache : A.v_cache) + row * (d >> 3);
-                        __half *scales = (role == 1 ? A.k_scale : A.v_scale) + row * (d >> 5);
-                        if (INTER) {
-                            *reinterpret_cast<uint2 *>(codes + c0) = make_uint2(w0, w1);
-                        } else {
-                            codes[c0] = w0;
-                            codes[c1] = w1;
-                        }
-                        if ((c0 & 3) == 0) scales[c0 >> 2] = h0;
-                        if (!INTER && (c1 & 3) == 0) scales[c1 >> 2] = h1;
+                }
+                if (live) {
+                    const int64_t row = row0 + static_cast<int64_t>(h) * A.bs;
+                    uint32_t *codes = static_cast<uint32_t *>(role == 1 ? A.k_cache : A.v_cache) + row * (d >> 3);
+                    __half *scales = (role == 1 ? A.k_scale : A.v_scale) + row * (d >> 5);
+                    if (INTER) {
+                        *reinterpret_cast<uint2 *>(codes + c0) = make_uint2(w0, w1);
+                    } else {
+                        codes[c0] = w0;
+                        codes[c1] = w1;
                     }
+                    if ((c0 & 3) == 0) scales[c0 >> 2] = h0;
+                    if (!INTER && (c1 & 3) == 0) scales[c1 >> 2] = h1;
                 }
             }
         }
@@ -437,9 +524,9 @@ rope_store_generic_kernel(const __grid_constant__ RopeArgs A) {
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 far = fmaxf(far, __shfl_xor_sync(0xffffffffu, far, o));
             }
-            __half hs = int4_scale(top);
-            float s = __half2float(hs), mid;
-            int4_seventh_bf16(top, mid);
+            float mid;
+            __half hs = int4_scale(top, mid);
+            float s = __half2float(hs);
             int code = s > 0.f ? int4_code(y, s, 1.f / s) : 0;
             const bool unsure = far > 0.f && (fabsf(fmaf(-7.f, mid, top)) <= far || int4_near_border(y, s, code, far));
             if (__any_sync(0xffffffffu, unsure)) {
@@ -599,6 +686,8 @@ pkv_status rope_store(const char *what, bool q4, void *q_out, const void *q, int
     if (es == 0) return set_error(PKV_ERR_INVALID_ARG, "%s: unknown dtype %d", what, (int)dtype);
     if (num_tokens < 0 || Hq < 0 || Hkv <= 0 || d <= 0 || bs <= 0 || num_slots < 0)
         return set_error(PKV_ERR_INVALID_ARG, "%s: bad sizes", what);
+    if (static_cast<int64_t>(Hq) * d > INT32_MAX || static_cast<int64_t>(Hkv) * d > INT32_MAX)
+        return set_error(PKV_ERR_INVALID_ARG, "%s: a token's heads hold 2^31 elements or more", what);
     if (num_slots > INT32_MAX) return set_error(PKV_ERR_INVALID_ARG, "%s: num_blocks * block_size >= 2^31", what);
     const int32_t r = rope ? rope->rotary_dim : 0;
     if (r < 0 || r > d || r % 2) return set_error(PKV_ERR_INVALID_ARG, "%s: rotary_dim must be even, from 0 to head_dim (%d)", what, d);
