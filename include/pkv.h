@@ -784,8 +784,9 @@ PKV_API pkv_status pkv_rope_store_kvcache_int4(void *q_out, const void *q, int64
  * what is stored; P is rounded to f16, and again times the scale of V (scales below 2^-14 lose
  * bits there); f32 scores and sums.
  *   caches, scales   16-byte aligned, as are q and out
- *   workspace        pkv_paged_attention_decode_int4_workspace_size bytes, 256-byte aligned,
- *                    needed during the call only; calls that may overlap need one each
+ *   workspace        pkv_paged_attention_decode_int4_workspace_size bytes (0 for few short
+ *                    contexts), 256-byte aligned, needed during the call only; calls that may
+ *                    overlap need one each
  *   other arguments, zero rows and device errors as in pkv_paged_attention_decode_mod.
  * head_dim 64, 128 or 256, block_size a multiple of 16, any num_q_heads / num_kv_heads (more
  * than 8 read the cache once for every 8 query heads); others return PKV_ERR_UNSUPPORTED.  Of
@@ -793,7 +794,7 @@ PKV_API pkv_status pkv_rope_store_kvcache_int4(void *q_out, const void *q, int64
  * More than 512 sequences run as consecutive launches over groups of at most 512.
  */
 PKV_API size_t pkv_paged_attention_decode_int4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
-                                                              int32_t head_dim);
+                                                              int32_t head_dim, int32_t max_context_len);
 PKV_API pkv_status pkv_paged_attention_decode_int4(
     void *out, const void *q, const void *k_cache, const void *v_cache, const uint16_t *k_scale, const uint16_t *v_scale,
     const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,

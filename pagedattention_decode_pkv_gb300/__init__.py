@@ -102,7 +102,7 @@ _SIGS = {
                                 ctypes.c_int, _vp, _vp], ctypes.c_int),
     "pkv_rope_store_kvcache_int4": ([_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32,
                                      _i32, _i32, _i32, _i32, ctypes.c_int, _vp, _vp], ctypes.c_int),
-    "pkv_paged_attention_decode_int4_workspace_size": ([_i32] * 4, _sz),
+    "pkv_paged_attention_decode_int4_workspace_size": ([_i32] * 5, _sz),
     "pkv_paged_attention_decode_int4": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
                                          _i32, _f32, _vp, ctypes.c_int, _vp, _sz, _vp, _vp], ctypes.c_int),
     "pkv_paged_attention_prefill_int4": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
@@ -196,12 +196,14 @@ def _addrs(*tensors):
     return [None if t is None else t.data_ptr() for t in tensors]
 
 
+# the raw handle alone: a Stream object costs a short call 2 to 4 us
+_CURRENT_RAW = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(dev, stream):
     if stream is not None:
         return stream.cuda_stream
-    # the raw handle alone: a Stream object costs a short call 2 to 4 us
-    current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return torch.cuda.current_stream(dev).cuda_stream if current is None else current(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream if _CURRENT_RAW is None else _CURRENT_RAW(dev.index)
 
 
 def _empty(n, dtype, dev, stream):
@@ -790,62 +792,66 @@ def pkv_rope_turns(inv_freq, *, amplitude: float = 1.0, device="cuda") -> RopeFr
     return RopeFrequencies(turns.to(device), amplitude)
 
 
-def _heads(x, dtype, dev_index, name):
-    """A [tokens, heads, head_dim] tensor whose heads and dims are contiguous: elements between tokens."""
-    if x.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-    if x.get_device() != dev_index:
+def _heads(x, h, d, index, name):
+    """Elements between the tokens of x [tokens, h, d], whose heads and dims are contiguous."""
+    if x.get_device() != index:
         raise ValueError("all tensors must be on one CUDA device")
-    n, h, d = x.shape
-    s = x.stride()
-    if n and h and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s[0] if n > 1 else h * d
+    n, a, b = x.stride()
+    if (b != 1 and d > 1) or (a != d and h > 1):
+        if x.numel():
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return n if x.shape[0] > 1 else h * d
 
 
 def _int4_cache(k_cache, v_cache, k_scale, v_scale):
     """(num_blocks, Hkv, block_size, d) of 4-bit caches, checked."""
-    shape = k_cache.shape
+    shape, scales = k_cache.shape, k_scale.shape
     if k_cache.dtype is not torch.uint8 or v_cache.dtype is not torch.uint8:
         raise TypeError("k_cache and v_cache must be torch.uint8 (two codes a byte)")
     if k_scale.dtype is not torch.float16 or v_scale.dtype is not torch.float16:
         raise TypeError("k_scale and v_scale must be torch.float16")
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache, v_cache: [num_blocks, Hkv, bs, head_dim / 2]")
-    if k_scale.shape != (*shape[:3], shape[3] // 16) or v_scale.shape != k_scale.shape:
+    nb, H, bs, half = shape
+    if scales != (nb, H, bs, half // 16) or v_scale.shape != scales:
         raise ValueError("k_scale, v_scale: [num_blocks, Hkv, bs, head_dim / 32]")
-    return shape[0], shape[1], shape[2], 2 * shape[3]
+    return nb, H, bs, 2 * half
 
 
-def _rope_store(fn, geometry, tail, q, key, value, positions, rope, caches, slot_mapping, interleaved, out, err_flag, stream):
-    """The marshalling of the store calls; q and rope may be absent.  `geometry` is (num_blocks, Hkv, bs, d)."""
-    dev = _device_of(*caches, slot_mapping, positions, None if rope is None else rope.turns, out, err_flag)
-    _, H, _, d = geometry
-    n, dtype, index = slot_mapping.numel(), key.dtype, dev.index
-    if dtype not in _DTYPE:
-        raise TypeError("key and value must be float32/float16/bfloat16")
+def _rope_store(fn, H, d, tail, q, key, value, positions, rope, caches, slot_mapping, interleaved, out, err_flag, stream):
+    """The marshalling of the store calls; q, and with it positions and rope, may be absent."""
+    dtype, n = key.dtype, slot_mapping.numel()
+    if dtype not in _DTYPE or value.dtype is not dtype:
+        raise TypeError("key and value must share one of float32/float16/bfloat16")
     if slot_mapping.dtype is not torch.int32:
         raise TypeError("slot_mapping must be torch.int32")
-    if key.shape != (n, H, d) or value.shape != (n, H, d):
+    rows = (n, H, d)
+    if key.shape != rows or value.shape != rows:
         raise ValueError(f"key/value must be [{n}, {H}, {d}]")
-    ks, vs = _heads(key, dtype, index, "key"), _heads(value, dtype, index, "value")
     if q is None:
-        front = (key.data_ptr(), ks, value.data_ptr(), vs)
+        dev = _device_of(slot_mapping, *caches, err_flag)
+        index = dev.index
+        front = (key.data_ptr(), _heads(key, H, d, index, "key"), value.data_ptr(), _heads(value, H, d, index, "value"))
     else:
-        shape = q.shape
+        turns, shape = rope.turns, q.shape
+        dev = _device_of(slot_mapping, *caches, positions, turns, out, err_flag)
+        index = dev.index
+        if q.dtype is not dtype:
+            raise TypeError("q must have the type of key and value")
         if len(shape) != 3 or shape[0] != n or shape[2] != d:
             raise ValueError(f"q must be [{n}, Hq, {d}]")
-        qs = _heads(q, dtype, index, "q")
         if positions.dtype is not torch.int32 or positions.numel() != n:
             raise ValueError(f"positions: {n} entries of torch.int32")
         if out is None:
             out = _empty(shape, dtype, dev, stream)
         elif out.shape != shape or out.dtype is not dtype:
             raise ValueError("out must have the shape and type of q")
-        c = ctypes.byref(_Rope(rope.turns.data_ptr(), rope.amplitude, rope.rotary_dim, 1 if interleaved else 0))
-        front = (out.data_ptr(), q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs, positions.data_ptr(), c)
-        tail = (shape[1], *tail)
-    _call(dev, fn, *front, *_addrs(*caches), slot_mapping.data_ptr(), n, *tail, _DTYPE[dtype], _flag(err_flag),
+        Hq = shape[1]
+        front = (out.data_ptr(), q.data_ptr(), _heads(q, Hq, d, index, "q"), key.data_ptr(), _heads(key, H, d, index, "key"),
+                 value.data_ptr(), _heads(value, H, d, index, "value"), positions.data_ptr(),
+                 ctypes.byref(_Rope(turns.data_ptr(), rope.amplitude, rope.rotary_dim, 1 if interleaved else 0)))
+        tail = (Hq, *tail)
+    _call(dev, fn, *front, *[t.data_ptr() for t in caches], slot_mapping.data_ptr(), n, *tail, _DTYPE[dtype], _flag(err_flag),
           _raw_stream(dev, stream))
     return out
 
@@ -861,7 +867,7 @@ def pkv_rope_store_kvcache(q, key, value, positions, rope: RopeFrequencies, k_ca
     if k_cache.dtype is not key.dtype or v_cache.dtype is not key.dtype:
         raise TypeError("key, value and caches must share one type")
     nb, bs, H, d = shape
-    return _rope_store(_lib.pkv_rope_store_kvcache, (nb, H, bs, d), (H, d, nb * bs), q, key, value, positions, rope,
+    return _rope_store(_lib.pkv_rope_store_kvcache, H, d, (H, d, nb * bs), q, key, value, positions, rope,
                        (k_cache, v_cache), slot_mapping, interleaved, out, err_flag, stream)
 
 
@@ -869,16 +875,16 @@ def pkv_rope_store_kvcache_int4(q, key, value, positions, rope: RopeFrequencies,
                                 slot_mapping, *, interleaved: bool = False, out=None, err_flag=None, stream=None):
     """pkv_rope_store_kvcache into 4-bit caches (uint8 [num_blocks, Hkv, bs, head_dim / 2] with
     float16 scales [num_blocks, Hkv, bs, head_dim / 32])."""
-    geometry = nb, H, bs, d = _int4_cache(k_cache, v_cache, k_scale, v_scale)
-    return _rope_store(_lib.pkv_rope_store_kvcache_int4, geometry, (H, d, bs, nb), q, key, value, positions, rope,
+    nb, H, bs, d = _int4_cache(k_cache, v_cache, k_scale, v_scale)
+    return _rope_store(_lib.pkv_rope_store_kvcache_int4, H, d, (H, d, bs, nb), q, key, value, positions, rope,
                        (k_cache, v_cache, k_scale, v_scale), slot_mapping, interleaved, out, err_flag, stream)
 
 
 def pkv_store_kvcache_int4(key, value, k_cache, v_cache, k_scale, v_scale, slot_mapping, *, err_flag=None, stream=None):
     """Row slot_mapping[i] of the 4-bit caches <- key[i] / value[i], each 32 dims under their own
     scale (in place; slot -1 skipped)."""
-    geometry = nb, H, bs, d = _int4_cache(k_cache, v_cache, k_scale, v_scale)
-    _rope_store(_lib.pkv_store_kvcache_int4, geometry, (H, d, bs, nb), None, key, value, None, None,
+    nb, H, bs, d = _int4_cache(k_cache, v_cache, k_scale, v_scale)
+    _rope_store(_lib.pkv_store_kvcache_int4, H, d, (H, d, bs, nb), None, key, value, None, None,
                 (k_cache, v_cache, k_scale, v_scale), slot_mapping, False, None, err_flag, stream)
 
 
@@ -903,8 +909,9 @@ def pkv_load_kvcache_int4(k_cache, v_cache, k_scale, v_scale, slot_mapping, dtyp
     return key, value
 
 
-def pkv_paged_attention_decode_int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim) -> int:
-    return int(_lib.pkv_paged_attention_decode_int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim))
+def pkv_paged_attention_decode_int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len) -> int:
+    return int(_lib.pkv_paged_attention_decode_int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                                   max_context_len))
 
 
 def pkv_paged_attention_decode_int4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale: float,
@@ -929,12 +936,13 @@ def pkv_paged_attention_decode_int4(q, k_cache, v_cache, k_scale, v_scale, block
         out = _empty(shape, dtype, dev, stream)
     elif out.shape != shape or out.dtype is not dtype:
         raise ValueError("out must have the shape and type of q")
-    if workspace is None:
-        workspace = _empty(_lib.pkv_paged_attention_decode_int4_workspace_size(B, Hq, Hkv, d), torch.uint8, dev, stream)
+    ws = _lib.pkv_paged_attention_decode_int4_workspace_size(B, Hq, Hkv, d, max_context_len)
+    if ws and workspace is None:
+        workspace = _empty(ws, torch.uint8, dev, stream)
     _call(dev, _lib.pkv_paged_attention_decode_int4, *_addrs(out, q, k_cache, v_cache, k_scale, v_scale),
           block_tables.data_ptr(), tables[1], context_lens.data_ptr(), B, Hq, Hkv, d, bs, nb, max_context_len, scale, mod,
-          _DTYPE[dtype], workspace.data_ptr(), workspace.numel() * workspace.element_size(), _flag(err_flag),
-          _raw_stream(dev, stream))
+          _DTYPE[dtype], workspace.data_ptr() if ws else None, workspace.numel() * workspace.element_size() if ws else 0,
+          _flag(err_flag), _raw_stream(dev, stream))
     return out
 
 

@@ -45,6 +45,11 @@ constexpr int kI4MaxSeqs = 512;      // sequences of a launch (shared-memory pre
 constexpr int kI4MaxWarps = 152 * 16;  // working warps of a launch (sizes the workspace)
 constexpr int kI4MinSteps = 1;       // steps that a working warp takes at least
 constexpr int kI4Heads = 8;          // query heads of a unit
+// Few units (one wave) of short contexts: a CTA each, its warps meeting in shared memory, in one
+// launch without a workspace.  Against slices and the join, 32 heads over 8 KV heads, bf16, on the
+// GPU: 1 sequence of 500 tokens 8.3 us / 10.3, 16 of up to 1000 10.3 / 14.4, 36 of up to 1000 14.4 /
+// 16.5; 4 of up to 2000, where more SMs help, 15.6 / 12.4.
+constexpr int kI4DirectCtas = 3, kI4DirectLen = 1024;  // CTAs an SM (2 at head_dim 256)
 constexpr float kI4Log2e = 1.4426950408889634f;
 constexpr float kI4Slack = 2.5f;     // log2 units: 2^2.5 times the largest V scale is in f16's range
 
@@ -107,7 +112,7 @@ template <int D, int STEP> struct I4Tile {
     static constexpr int kWarp = 2 * kHalf + 2 * kQ;
 };
 
-template <typename T, int D, int STEP, int WARPS, int CTAS, bool MOD>
+template <typename T, int D, int STEP, int WARPS, int CTAS, bool MOD, bool DIRECT>
 __global__ void __launch_bounds__(WARPS * 32, CTAS)
 decode_int4_kernel(const __grid_constant__ I4Args A) {
     using R = I4Tile<D, STEP>;
@@ -133,7 +138,19 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
     Cursor cur;
     int64_t me = 0;
     int count = 0;  // steps of this warp's slice
-    {
+    if constexpr (DIRECT) {
+        // The CTA's one unit: its warps take every WARPS-th step.
+        cur.b = static_cast<int>(blockIdx.x / HU);
+        cur.hu = static_cast<int>(blockIdx.x) - cur.b * HU;
+        cur.st = warp;
+        cur.n = steps_of(cur.b);
+        count = cur.n > warp ? (cur.n - 1 - warp) / WARPS + 1 : 0;
+        if (cur.n == 0 && threadIdx.x == 0) {
+            const int ctx = A.context_lens[cur.b];
+            if ((ctx < 0 || ctx > A.max_ctx || static_cast<int64_t>(ctx) > static_cast<int64_t>(A.max_blocks) * bs) && A.err_flag)
+                atomicOr(A.err_flag, PKV_ERRBIT_CONTEXT);
+        }
+    } else {
         // The prefix of steps over the sequences (of one unit each), in what holds the tiles later.
         int64_t *pref = reinterpret_cast<int64_t *>(smem);  // [B + 1]
         int32_t *ns = reinterpret_cast<int32_t *>(pref + kI4MaxSeqs + 1);
@@ -189,7 +206,8 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
         }
         __syncthreads();  // the prefix has been read: the tiles may be filled
     }
-    if (count == 0) return;
+    if (!DIRECT && count == 0) return;
+    constexpr int kStride = DIRECT ? WARPS : 1;  // steps from one of the warp's to the next
     auto next_unit = [&](Cursor &c) {  // the first step of the next unit (b == B: there is none)
         c.st = 0;
         if (++c.hu == HU) {
@@ -221,7 +239,7 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
     int next_id = -2;          // its entry (-2: nothing of the tile is seen)
     bool bad = false;
     const uint32_t bs16 = static_cast<uint32_t>(bs) >> 4;
-    const uint32_t col_by = TILES / bs16, in_by = TILES - col_by * bs16;  // a step further
+    const uint32_t col_by = kStride * TILES / bs16, in_by = kStride * TILES - col_by * bs16;  // the warp's next step
     int ld_pos = 0, ld_ctx = 0, ld_first = 0;  // of ld's step: position of this lane's tile
     uint32_t ld_head = 0;
     const int32_t *ld_table = nullptr;
@@ -278,18 +296,19 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
         at = mine ? (static_cast<uint32_t>(next_id) * A.Hkv + ld_head) * bs16 + in : 0u;
         here = __ballot_sync(0xffffffffu, mine) & ((1u << TILES) - 1);
         copy(k_tile, A.k_cache, A.k_scale);
-        if (++ld.st < ld.n) {
+        ld.st += kStride;
+        if (DIRECT || ld.st < ld.n) {
             const bool over = in + in_by >= bs16;
             in = in + in_by - (over ? bs16 : 0u);
             col += col_by + (over ? 1u : 0u);
-            ld_pos += STEP;
+            ld_pos += kStride * STEP;
             look_up();
         } else {
             next_unit(ld);
             start_unit();
         }
     };
-    start_unit();
+    if (count > 0) start_unit();
     // ---- a unit's queries: lane (g = head, t): dims 8 t .. 8 t + 7 of every group, f16 under a power of two
     const int g = lane >> 2, t = lane & 3, mi = lane >> 3, r8 = lane & 7;
     const uint32_t frag_at = (r8 + 8 * (mi & 1)) * (D / 2), frag_sw = swizzled(r8, 0);  // this lane's row of the ldmatrix tiles
@@ -367,8 +386,10 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
     int pos = 0, ctx = 0, first = 0, cur_b = -1;  // of cur's step, and the sequence they are of
     bool fresh = true;                // the next step starts a unit
     bool whole = false;               // the unit began in this slice
-    copy_k();
-    copy(v_tile, A.v_cache, A.v_scale);
+    if (count > 0) {
+        copy_k();
+        copy(v_tile, A.v_cache, A.v_scale);
+    }
     for (int s = 0; s < count; ++s) {
         asm volatile("cp.async.wait_group 1;" ::: "memory");  // K: V, committed after it, may be under way
         __syncwarp();
@@ -389,7 +410,7 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
             m0 = m1 = -INFINITY;
             l0 = l1 = b0 = b1 = 0.f;
             whole = cur.st == 0;
-            if (lane == 0 && whole) A.unit_info[static_cast<int64_t>(cur.b) * HU + cur.hu].x = static_cast<int>(me);
+            if (!DIRECT && lane == 0 && whole) A.unit_info[static_cast<int64_t>(cur.b) * HU + cur.hu].x = static_cast<int>(me);
             fresh = false;
         }
         const uint32_t now = here;
@@ -562,7 +583,8 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
         }
         __syncwarp();
         if (more) copy(v_tile, A.v_cache, A.v_scale);
-        pos += STEP;
+        pos += kStride * STEP;
+        if constexpr (DIRECT) continue;
         if (++cur.st == cur.n || s + 1 == count) {
             // the unit ends, or the slice does
             fresh = true;
@@ -617,6 +639,58 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (bad && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_BLOCK_RANGE);
+    if constexpr (DIRECT) {
+        // The warps' accumulators meet in shared memory, each in its own tiles.
+        __shared__ float2 warp_ml[WARPS][kI4Heads];
+        const int kh = cur.hu / A.subs, sub = cur.hu - kh * A.subs, live = min(kI4Heads, A.G - sub * kI4Heads);
+        constexpr int kFloats = R::kWarp / 4;
+        static_assert(kFloats >= kI4Heads * D, "a unit's accumulator fits the warp's tiles");
+        float *mine = reinterpret_cast<float *>(smem) + warp * kFloats;
+        __syncwarp();
+        if (count == 0) {
+            if (lane < kI4Heads) warp_ml[warp][lane] = make_float2(-INFINITY, 0.f);
+        } else {
+#pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1) {
+                l0 += __shfl_xor_sync(0xffffffffu, l0, sh);
+                l1 += __shfl_xor_sync(0xffffffffu, l1, sh);
+            }
+            if (g == 0) {
+                warp_ml[warp][2 * t] = make_float2(m0, l0);
+                warp_ml[warp][2 * t + 1] = make_float2(m1, l1);
+            }
+#pragma unroll
+            for (int gg = 0; gg < NG; ++gg)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int d = 32 * gg + 8 * (g >> 1) + (g & 1) + 4 * e;
+                    mine[2 * t * D + d] = o[gg][e][0];
+                    mine[2 * t * D + d + 2] = o[gg][e][2];
+                    mine[(2 * t + 1) * D + d] = o[gg][e][1];
+                    mine[(2 * t + 1) * D + d + 2] = o[gg][e][3];
+                }
+        }
+        __syncthreads();
+        uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<T *>(A.out) + (static_cast<int64_t>(cur.b) * A.Hq + kh * A.G + sub * kI4Heads) * D);
+        for (int i = threadIdx.x; i < live * (D / 2); i += WARPS * 32) {
+            const int h = i / (D / 2);
+            float M = -INFINITY, L = 0.f, a = 0.f, c = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) M = fmaxf(M, warp_ml[w][h].x);
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                const float2 ml = warp_ml[w][h];
+                if (ml.x == -INFINITY && ml.y == 0.f) continue;  // (scores that are all NaN leave the maximum there, and a NaN sum)
+                const float f = exp2f(ml.x - (M == -INFINITY ? 0.f : M));
+                const float2 v = reinterpret_cast<const float2 *>(smem)[w * (kFloats / 2) + i];
+                L = fmaf(f, ml.y, L);
+                a = fmaf(f, v.x, a);
+                c = fmaf(f, v.y, c);
+            }
+            const float inv = L > 0.f ? 1.f / L : (L == L ? 0.f : L);
+            out[i] = Half16<T>::pack(a * inv, c * inv);
+        }
+    }
 }
 
 // Joins a unit's pieces: out = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k.  WPR warps take a
@@ -720,17 +794,20 @@ decode_int4_join_kernel(const __grid_constant__ I4Args A, int64_t rows) {
 struct I4Plan {
     int32_t subs = 1, rows = 0, group = 0;  // units of a KV head, query heads of a unit at most, sequences of a launch
     int64_t units = 0;            // of a launch
+    bool direct = false;          // a CTA per unit, nothing to join
     size_t o_bytes = 0, ml_bytes = 0, ws_bytes = 0;
 };
 
 bool i4_shape(int32_t d) { return d == 64 || d == 128 || d == 256; }
 
-I4Plan i4_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t d) {
+I4Plan i4_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_ctx) {
     I4Plan p;
     p.subs = (Hq / Hkv + kI4Heads - 1) / kI4Heads;
     p.rows = Hq / Hkv < kI4Heads ? Hq / Hkv : kI4Heads;
     p.group = B < kI4MaxSeqs ? B : kI4MaxSeqs;
     p.units = static_cast<int64_t>(p.group) * Hkv * p.subs;
+    p.direct = B <= kI4MaxSeqs && p.units <= 152 * (d == 256 ? 2 : kI4DirectCtas) && max_ctx <= kI4DirectLen;
+    if (p.direct) return p;
     const int64_t slots = kI4MaxWarps + p.units;
     p.o_bytes = static_cast<size_t>(slots) * p.rows * d * sizeof(float);
     p.ml_bytes = (static_cast<size_t>(slots) * p.rows * sizeof(float2) + 255) / 256 * 256;
@@ -738,12 +815,12 @@ I4Plan i4_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t d) {
     return p;
 }
 
-template <typename T, int D, bool MOD>
+template <typename T, int D, bool MOD, bool DIRECT>
 cudaError_t i4_launch(const I4Args &a, const I4Plan &p, cudaStream_t stream) {
     constexpr int STEP = D == 256 ? 32 : 64, WARPS = 4, CTAS = D == 256 ? 2 : D == 128 ? 3 : 4;
     constexpr int smem = WARPS * I4Tile<D, STEP>::kWarp;
     static_assert(smem >= (kI4MaxSeqs + 1) * 8 + kI4MaxSeqs * 4, "the prefix lies in the tiles");
-    auto kern = decode_int4_kernel<T, D, STEP, WARPS, CTAS, MOD>;
+    auto kern = decode_int4_kernel<T, D, STEP, WARPS, CTAS, MOD, DIRECT>;
     static std::atomic<int> grids[64];  // resident CTAs, per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -760,6 +837,7 @@ cudaError_t i4_launch(const I4Args &a, const I4Plan &p, cudaStream_t stream) {
         if (grid < 1) return cudaErrorInvalidConfiguration;
         grids[dev & 63].store(grid, std::memory_order_release);
     }
+    if (DIRECT) return launch_pdl(kPdlDecode, kern, dim3(static_cast<unsigned>(p.units)), dim3(WARPS * 32), smem, stream, a);
     e = launch_pdl(kPdlDecode, kern, dim3(grid), dim3(WARPS * 32), smem, stream, a);
     if (e != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(a.B) * a.Hkv * a.subs * a.rows;
@@ -771,9 +849,16 @@ cudaError_t i4_launch(const I4Args &a, const I4Plan &p, cudaStream_t stream) {
     return launch_pdl(kPdlCombine, join, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(kI4JoinWarps * 32), 0, stream, a, rows);
 }
 
-template <typename T, bool MOD>
+template <typename T, bool MOD, bool DIRECT>
 cudaError_t i4_launch_d(const I4Args &a, const I4Plan &p, int32_t d, cudaStream_t s) {
-    return d == 64 ? i4_launch<T, 64, MOD>(a, p, s) : d == 128 ? i4_launch<T, 128, MOD>(a, p, s) : i4_launch<T, 256, MOD>(a, p, s);
+    return d == 64 ? i4_launch<T, 64, MOD, DIRECT>(a, p, s) : d == 128 ? i4_launch<T, 128, MOD, DIRECT>(a, p, s)
+                                                                      : i4_launch<T, 256, MOD, DIRECT>(a, p, s);
+}
+
+template <typename T>
+cudaError_t i4_launch_any(const I4Args &a, const I4Plan &p, int32_t d, bool rules, cudaStream_t s) {
+    if (p.direct) return rules ? i4_launch_d<T, true, true>(a, p, d, s) : i4_launch_d<T, false, true>(a, p, d, s);
+    return rules ? i4_launch_d<T, true, false>(a, p, d, s) : i4_launch_d<T, false, false>(a, p, d, s);
 }
 
 }  // namespace
@@ -782,9 +867,9 @@ cudaError_t i4_launch_d(const I4Args &a, const I4Plan &p, int32_t d, cudaStream_
 using namespace pkv;
 
 extern "C" size_t pkv_paged_attention_decode_int4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
-                                                                 int32_t head_dim) {
+                                                                 int32_t head_dim, int32_t max_context_len) {
     if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || !i4_shape(head_dim)) return 0;
-    return i4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim).ws_bytes;
+    return i4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len).ws_bytes;
 }
 
 extern "C" pkv_status pkv_paged_attention_decode_int4(
@@ -815,8 +900,8 @@ extern "C" pkv_status pkv_paged_attention_decode_int4(
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 16) ||
         !aligned(v_scale, 16))
         return set_error(PKV_ERR_UNSUPPORTED, "int4 decode: caches, scales, q and out must be 16-byte aligned");
-    const I4Plan p = i4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim);
-    if (!workspace || workspace_bytes < p.ws_bytes || !aligned(workspace, 256))
+    const I4Plan p = i4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len);
+    if (p.ws_bytes > 0 && (!workspace || workspace_bytes < p.ws_bytes || !aligned(workspace, 256)))
         return set_error(PKV_ERR_WORKSPACE, "int4 decode: workspace needs %zu bytes (256-byte aligned), got %zu", p.ws_bytes, workspace_bytes);
     I4Args a{};
     a.k_cache = static_cast<const uint8_t *>(k_cache);
@@ -851,8 +936,7 @@ extern "C" pkv_status pkv_paged_attention_decode_int4(
         a.key_starts = m.key_starts ? m.key_starts + b0 : nullptr;
         a.B = num_seqs - b0 < p.group ? num_seqs - b0 : p.group;
         auto s = static_cast<cudaStream_t>(stream);
-        const cudaError_t e = dtype == PKV_BF16 ? (rules ? i4_launch_d<__nv_bfloat16, true>(a, p, head_dim, s) : i4_launch_d<__nv_bfloat16, false>(a, p, head_dim, s))
-                                                : (rules ? i4_launch_d<__half, true>(a, p, head_dim, s) : i4_launch_d<__half, false>(a, p, head_dim, s));
+        const cudaError_t e = dtype == PKV_BF16 ? i4_launch_any<__nv_bfloat16>(a, p, head_dim, rules, s) : i4_launch_any<__half>(a, p, head_dim, rules, s);
         if (e != cudaSuccess) return set_error(PKV_ERR_CUDA, "int4 decode launch: %s", cudaGetErrorString(e));
     }
     return ok();
