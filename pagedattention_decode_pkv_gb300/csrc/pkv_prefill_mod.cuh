@@ -1,5 +1,5 @@
 // Causal varlen / chunked prefill attention over the paged cache with score
-// rules and over 8-bit caches.
+// rules and over 8-bit and 4-bit caches.
 //
 // Query i of sequence b sits at position p = starts[b] + i.  Its score for key t
 // (query head h reading KV head h / G) is
@@ -30,6 +30,12 @@
 // no bf16 magnitude overflows; elements from 2^-30 of their row's largest on are exact,
 // smaller ones off by at most 2^-38 of it.
 //
+// 4-bit caches (pkv_int4.cuh): a scale per 32 dims of a row goes into the f16 tile with its
+// codes, exactly (its eight significant bits and a code's three fit f16's eleven), so scores and
+// P take no factor; P is rounded once and its row sum adds what was rounded, as over 16-bit caches.
+// A lane of the converter warps takes a group: 16 bytes of codes, five operations for eight codes
+// to f16 1024 + u, four to u - 8, four times the scale.
+//
 // The CTA.  Two tiles of 128 query rows (128 / G positions x G heads) of one KV
 // head, accumulators in tensor memory: eight softmax warps hold one query row per
 // thread, one producer warp copies pages by TMA, two warps issue the tcgen05.mma, one
@@ -47,7 +53,7 @@
 // in their softmax together).  With the copies into the ring the step is 1534, with the
 // softmax warps beside it 1834.  Cap 50: 1049 us; the polynomial's operations come on
 // top.  With a bias 1236.  E4M3 and int8: 1264 and 1297; widening writes every tile once
-// more.  Short spans: of a CTA's ~13k clk of setup, first products and output nothing
+// more.  int4: 1231 (fp16, prompts of 3700 to 4096).  Short spans: of a CTA's ~13k clk of setup, first products and output nothing
 // overlaps, for both tiles do them together (2 x 8k rows of packed documents of 60 to
 // 2500 rows: 150 us, 664 TFLOP/s).
 //
@@ -88,8 +94,7 @@ constexpr int kConvWarps = 4;
 constexpr int kHalfKeys = kModKeys / 2;  // keys per step of the softmax and the products
 constexpr int kModTile = 32768;       // a 128 x 128 tile of 16-bit values: two 64-column halves
 constexpr int kModHalf = kModTile / 2;
-constexpr int kModCodeTile = 16384;   // the same tile in codes (4-bit ones and their scales: 9216 bytes of it)
-constexpr int kModScales4 = kModKeys * 64;  // where a 4-bit tile's scales begin, 8 bytes a key
+constexpr int kModScales4 = kModKeys * 64;  // where a 4-bit code tile's scales begin, 8 bytes a key
 constexpr uint64_t kModDeadlineNs = 2000000000ull;
 constexpr float kModRescale = 8.f;    // log2 units a block may exceed the reference maximum by before O is rescaled
 // CAP: no cap, a cap, or a cap that bounds the scores so far that no reference
@@ -113,14 +118,18 @@ struct ModInfo {
 };
 static_assert(sizeof(ModInfo) <= 128, "info slot");
 
-template <bool C8>
+// 4-bit code tiles are small enough for a fourth ring tile beside them (8 prompts of 3700 to 4096,
+// fp16: 1231 us with two code tiles, 1251 with three, 1268 with three ring tiles and four).
+template <int FMT>
 struct ModLayout {
-    static constexpr int kRing = C8 ? 3 : 4;    // 32 KB tiles
-    static constexpr int kStage = C8 ? 4 : 0;   // 16 KB code tiles
+    static constexpr bool C8 = FMT != kCode16, C4 = FMT == kCodeInt4;
+    static constexpr int kRing = C8 && !C4 ? 3 : 4;      // 32 KB tiles
+    static constexpr int kStage = C4 ? 2 : C8 ? 4 : 0;   // code tiles
+    static constexpr int kCodeTile = C4 ? kModScales4 + kModKeys * 8 : 16384;
     static constexpr int kQ = 0;
     static constexpr int kRingOff = 2 * kModTile;
     static constexpr int kStageOff = kRingOff + kRing * kModTile;
-    static constexpr int kInfoOff = kStageOff + kStage * kModCodeTile;
+    static constexpr int kInfoOff = kStageOff + kStage * kCodeTile;
     static constexpr int kRangeOff = kInfoOff + 4 * 128;
     static constexpr int kBarOff = kRangeOff + 64;
     static constexpr int kTmemSlot = kBarOff + 320;
@@ -185,7 +194,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     constexpr bool C4 = FMT == kCodeInt4;  // with their scales, row by row
     constexpr bool BS = C8 && !C4;         // a scale per block, kept out of the tiles
     constexpr bool RAW = !CAP && !ALIBI;  // the score's factor goes into the exponent's FMA
-    using L = ModLayout<C8>;
+    using L = ModLayout<FMT>;
     using M16 = typename std::conditional<C8, __half, T>::type;  // operand type of the products
     using H = Half16<M16>;
     constexpr bool kBf16 = std::is_same<M16, __nv_bfloat16>::value;
@@ -396,7 +405,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 return __shfl_sync(0xffffffffu, ok, 0) != 0;
             };
             constexpr int kSlots = C8 ? L::kStage : kRing;
-            constexpr int kSlotBytes = C8 ? kModCodeTile : kModTile;
+            constexpr int kSlotBytes = C8 ? L::kCodeTile : kModTile;
             constexpr int kSlotFull = C8 ? L::kStFull : L::kFull, kSlotEmpty = C8 ? L::kStEmpty : L::kEmpty;
             const uint32_t sDst = C8 ? sStage : sRing;
             int issued = 0;
@@ -609,7 +618,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const ModInfo *f = info(item >> 1);
                 const bool fix = (item & 1) && f->fix;
                 const int miss = f->miss, key0 = (j0 + (item >> 1)) * kModKeys;
-                const uint32_t src = sStage + static_cast<uint32_t>(st) * kModCodeTile;
+                const uint32_t src = sStage + static_cast<uint32_t>(st) * L::kCodeTile;
                 const uint32_t dst = sRing + static_cast<uint32_t>(slot) * kModTile;
                 if constexpr (C4) {
                     // A lane takes a group: 16 bytes of codes, one scale, four chunks of eight
@@ -1064,7 +1073,7 @@ pkv_status prefill_mod_configure() {
     if (FMT != kCode16 && e == cudaSuccess && attr.numRegs < kModLaunchRegs)
         return set_error(PKV_ERR_CUDA, "prefill: the kernel was built with %d registers, not %d", attr.numRegs, kModLaunchRegs);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ModLayout<FMT != kCode16>::kAlloc);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ModLayout<FMT>::kAlloc);
     if (e != cudaSuccess) return set_error(PKV_ERR_CUDA, "prefill: kernel attributes: %s", cudaGetErrorString(e));
     done.fetch_or(bit, std::memory_order_acq_rel);
     return PKV_OK;
@@ -1130,7 +1139,7 @@ pkv_status prefill_mod_launch(const PrefillCall &c) {
         return set_error(PKV_ERR_UNSUPPORTED, "prefill: max_q_len is too long for so many sequences");
     cudaError_t e = launch_pdl(kPdlDecode, prefill_mod_kernel<T, FMT, CAP, ALIBI>,
                                dim3(c.Hkv, items < kMaxGridPairs ? items : kMaxGridPairs, c.num_seqs * a.pair_grids), dim3(kModThreads<FMT != kCode16>),
-                               ModLayout<FMT != kCode16>::kAlloc, c.stream, mk, mv, a);
+                               ModLayout<FMT>::kAlloc, c.stream, mk, mv, a);
     if (e == cudaSuccess && a.nsplit > 1) {
         const int64_t rows = static_cast<int64_t>(c.num_seqs) * c.max_q_len * c.Hq;
         constexpr int kRows = kModMergeThreads / 32;
