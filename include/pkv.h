@@ -806,18 +806,25 @@ PKV_API pkv_status pkv_paged_attention_decode_int4(
  * pkv_paged_attention_prefill_int4 -- pkv_paged_attention_prefill_mod over 4-bit caches: K and V
  * are widened to f16 under their scales, exactly for the scales that the store writes; queries
  * as over 8-bit caches; P enters its product rounded to f16, and the row sum adds the rounded
- * values.
- *   workspace   pkv_paged_attention_prefill_mod_workspace_size bytes, as there
- *   scales      16-byte aligned, not negative
+ * values.  Calls of few rows, or over long tables, widen as they go; others (1024 rows of a KV head
+ * and more, up to 1 GiB) widen the sequences' blocks once into the workspace.
+ *   max_total_len  host bound on starts[b] + n_b, or 0 for the tables' width; sequences beyond it
+ *                  are errors like those beyond their table.  It bounds the workspace.
+ *   workspace      pkv_paged_attention_prefill_int4_workspace_size bytes (may be 0), 256-byte
+ *                  aligned, needed during the call only; calls that may overlap need one each
+ *   scales         16-byte aligned, not negative
  *   other arguments, shapes, limits and device errors as in pkv_paged_attention_prefill_mod;
  *   what may hold anything there may here, codes and scales.
  */
+PKV_API size_t pkv_paged_attention_prefill_int4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                                               int32_t head_dim, int32_t block_size, int32_t max_q_len,
+                                                               int32_t max_blocks_per_seq, int32_t max_total_len);
 PKV_API pkv_status pkv_paged_attention_prefill_int4(
     void *out, const void *q, const void *k_cache, const void *v_cache, const uint16_t *k_scale, const uint16_t *v_scale,
     const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *starts, const int32_t *cu_q, int32_t num_seqs,
-    int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
-    int32_t num_blocks, float scale, const pkv_score_mod *mod, pkv_dtype dtype, void *workspace, size_t workspace_bytes,
-    int32_t *err_flag, void *stream);
+    int32_t max_q_len, int32_t max_total_len, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t block_size, int32_t num_blocks, float scale, const pkv_score_mod *mod, pkv_dtype dtype, void *workspace,
+    size_t workspace_bytes, int32_t *err_flag, void *stream);
 
 /*
  * Host block allocator -- which physical block of the pool each sequence

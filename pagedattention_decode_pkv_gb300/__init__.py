@@ -105,8 +105,9 @@ _SIGS = {
     "pkv_paged_attention_decode_int4_workspace_size": ([_i32] * 5, _sz),
     "pkv_paged_attention_decode_int4": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
                                          _i32, _f32, _vp, ctypes.c_int, _vp, _sz, _vp, _vp], ctypes.c_int),
+    "pkv_paged_attention_prefill_int4_workspace_size": ([_i32] * 8, _sz),
     "pkv_paged_attention_prefill_int4": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
-                                          _i32, _i32, _f32, _vp, ctypes.c_int, _vp, _sz, _vp, _vp], ctypes.c_int),
+                                          _i32, _i32, _i32, _f32, _vp, ctypes.c_int, _vp, _sz, _vp, _vp], ctypes.c_int),
     "pkv_selftest_wait_timeout": ([_vp, ctypes.c_uint32, _vp], ctypes.c_int),
     "pkv_allocator_create": ([_i32, _i32, _vp], ctypes.c_int),
     "pkv_allocator_destroy": ([_vp], None),
@@ -946,11 +947,19 @@ def pkv_paged_attention_decode_int4(q, k_cache, v_cache, k_scale, v_scale, block
     return out
 
 
+def pkv_paged_attention_prefill_int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len,
+                                                    max_blocks_per_seq, max_total_len=0) -> int:
+    return int(_lib.pkv_paged_attention_prefill_int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                                    max_q_len, max_blocks_per_seq, max_total_len))
+
+
 def pkv_paged_attention_prefill_int4(q, k_cache, v_cache, k_scale, v_scale, block_tables, starts, cu_q, scale: float,
-                                     max_q_len: int, *, softcap: float = 0.0, alibi_slopes=None, key_starts=None,
-                                     prefix_lens=None, out=None, workspace=None, err_flag=None, stream=None):
+                                     max_q_len: int, *, max_total_len: int = 0, softcap: float = 0.0, alibi_slopes=None,
+                                     key_starts=None, prefix_lens=None, out=None, workspace=None, err_flag=None,
+                                     stream=None):
     """Prefill attention over 4-bit caches (as pkv_store_kvcache_int4 writes them), with the score
-    rules and workspace of pkv_paged_attention_prefill_mod."""
+    rules of pkv_paged_attention_prefill_mod.  max_total_len, a bound on a sequence's positions
+    (0: the tables' width), bounds the workspace."""
     nb, Hkv, bs, d = _int4_cache(k_cache, v_cache, k_scale, v_scale)
     dev = _device_of(q, k_cache, v_cache, k_scale, v_scale, block_tables, starts, cu_q, alibi_slopes, key_starts,
                      prefix_lens, out, workspace, err_flag)
@@ -968,12 +977,12 @@ def pkv_paged_attention_prefill_int4(q, k_cache, v_cache, k_scale, v_scale, bloc
         out = _empty(shape, dtype, dev, stream)
     elif out.shape != shape or out.dtype is not dtype:
         raise ValueError("out must have the shape and type of q")
-    ws = _lib.pkv_paged_attention_prefill_mod_workspace_size(B, Hq, Hkv, d, bs, max_q_len, tables[1])
+    ws = _lib.pkv_paged_attention_prefill_int4_workspace_size(B, Hq, Hkv, d, bs, max_q_len, tables[1], max_total_len)
     if ws and workspace is None:
         workspace = _empty(ws, torch.uint8, dev, stream)
     _call(dev, _lib.pkv_paged_attention_prefill_int4, *_addrs(out, q, k_cache, v_cache, k_scale, v_scale),
-          block_tables.data_ptr(), tables[1], starts.data_ptr(), cu_q.data_ptr(), B, max_q_len, Hq, Hkv, d, bs, nb, scale,
-          mod, _DTYPE[dtype], workspace.data_ptr() if ws else None,
+          block_tables.data_ptr(), tables[1], starts.data_ptr(), cu_q.data_ptr(), B, max_q_len, max_total_len, Hq, Hkv, d, bs, nb,
+          scale, mod, _DTYPE[dtype], workspace.data_ptr() if ws else None,
           workspace.numel() * workspace.element_size() if ws else 0, _flag(err_flag), _raw_stream(dev, stream))
     return out
 

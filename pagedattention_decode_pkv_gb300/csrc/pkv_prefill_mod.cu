@@ -65,7 +65,7 @@ pkv_status pkv::prefill_mod_run(PrefillCall c, int format, int32_t head_dim, voi
     if (format != kCode16 && format != kCodeE4M3 && format != kCodeInt8 && format != kCodeInt4)
         return set_error(PKV_ERR_INVALID_ARG, "prefill: unknown cache format %d", format);
     if (c.num_seqs < 0 || c.max_q_len < 0 || c.Hq <= 0 || c.Hkv <= 0 || head_dim <= 0 || c.block_size <= 0 ||
-        c.num_blocks < 0 || c.max_blocks < 0)
+        c.num_blocks < 0 || c.max_blocks < 0 || c.max_total_len < 0)
         return set_error(PKV_ERR_INVALID_ARG, "prefill: bad sizes");
     if (c.Hq % c.Hkv)
         return set_error(PKV_ERR_INVALID_ARG, "prefill: num_q_heads (%d) is not a multiple of num_kv_heads (%d)", c.Hq, c.Hkv);
@@ -92,16 +92,38 @@ pkv_status pkv::prefill_mod_run(PrefillCall c, int format, int32_t head_dim, voi
         if (!aligned(c.k_scale4, 16) || !aligned(c.v_scale4, 16))
             return set_error(PKV_ERR_UNSUPPORTED, "prefill: scales of a 4-bit cache must be 16-byte aligned");
     }
-    c.plan = prefill_plan(c.num_seqs, c.Hq, c.Hkv, c.max_q_len, c.max_blocks, c.block_size);
-    if (c.plan.ws_bytes > 0 && (!workspace || workspace_bytes < c.plan.ws_bytes || !aligned(workspace, 256)))
-        return set_error(PKV_ERR_WORKSPACE, "prefill: workspace needs %zu bytes (256-byte aligned), got %zu",
-                         c.plan.ws_bytes, workspace_bytes);
+    WidePlan w;
+    if (format == kCodeInt4) {
+        w = wide_plan(c.num_seqs, c.Hq, c.Hkv, c.block_size, c.max_q_len, c.max_blocks, c.max_total_len);
+    }
+    c.plan = prefill_plan(c.num_seqs, c.Hq, c.Hkv, c.max_q_len, w.bytes ? w.stride : c.max_blocks, c.block_size);
+    const size_t need = c.plan.ws_bytes + w.bytes;
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+        return set_error(PKV_ERR_WORKSPACE, "prefill: workspace needs %zu bytes (256-byte aligned), got %zu", need, workspace_bytes);
     c.workspace = static_cast<char *>(workspace);
+    if (w.bytes) {
+        const pkv_status st = widen_int4(c, w, c.workspace + c.plan.ws_bytes);
+        if (st != PKV_OK) return st;
+        format = c.dtype == PKV_F16 ? kCode16 : kCodeF16;
+    }
     const pkv_status st = format == kCodeE4M3   ? prefill_mod_e4m3(c)
                           : format == kCodeInt8 ? prefill_mod_int8(c)
                           : format == kCodeInt4 ? prefill_mod_int4(c)
+                          : format == kCodeF16  ? prefill_mod_f16(c)
                                                 : prefill_mod_16bit(c);
     return st == PKV_OK ? ok() : st;
+}
+
+extern "C" size_t pkv_paged_attention_prefill_int4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                                                  int32_t head_dim, int32_t block_size, int32_t max_q_len,
+                                                                  int32_t max_blocks_per_seq, int32_t max_total_len) {
+    if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || block_size <= 0 ||
+        max_q_len <= 0 || max_blocks_per_seq < 0 || max_total_len < 0 ||
+        !supported_shape(num_q_heads, num_kv_heads, head_dim, block_size))
+        return 0;
+    const WidePlan w = wide_plan(num_seqs, num_q_heads, num_kv_heads, block_size, max_q_len, max_blocks_per_seq, max_total_len);
+    return w.bytes + prefill_plan(num_seqs, num_q_heads, num_kv_heads, max_q_len, w.bytes ? w.stride : max_blocks_per_seq,
+                                  block_size).ws_bytes;
 }
 
 extern "C" pkv_status pkv_paged_attention_prefill_mod(

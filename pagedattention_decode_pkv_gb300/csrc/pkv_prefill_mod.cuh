@@ -87,6 +87,7 @@ constexpr int kModKeys = 128;   // keys per block
 // caches four converter warps.  384 threads have 168 registers each.  512 have 128,
 // of which the service warps give up 40 so that the softmax warps get theirs:
 // 256 x 168 + 256 x 88 = 512 x 128.
+template <int FMT> constexpr bool kCoded = FMT != kCode16 && FMT != kCodeF16;
 template <bool C8> constexpr int kModThreads = C8 ? 512 : 384;
 constexpr int kModLaunchRegs = 128, kModSoftRegs = 168, kModServiceRegs = 88;  // 8-bit caches
 static_assert(256 * (kModSoftRegs + kModServiceRegs) <= 512 * kModLaunchRegs, "the split draws on the launch's registers");
@@ -122,7 +123,7 @@ static_assert(sizeof(ModInfo) <= 128, "info slot");
 // fp16: 1231 us with two code tiles, 1251 with three, 1268 with three ring tiles and four).
 template <int FMT>
 struct ModLayout {
-    static constexpr bool C8 = FMT != kCode16, C4 = FMT == kCodeInt4;
+    static constexpr bool C8 = kCoded<FMT>, C4 = FMT == kCodeInt4;
     static constexpr int kRing = C8 && !C4 ? 3 : 4;      // 32 KB tiles
     static constexpr int kStage = C4 ? 2 : C8 ? 4 : 0;   // code tiles
     static constexpr int kCodeTile = C4 ? kModScales4 + kModKeys * 8 : 16384;
@@ -187,15 +188,17 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&x)[4]) {
 }
 
 template <typename T, int FMT, int CAP, bool ALIBI>
-__global__ void __launch_bounds__(kModThreads<FMT != kCode16>, 1)
+__global__ void __launch_bounds__(kModThreads<kCoded<FMT>>, 1)
 prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ ModArgs A) {
-    constexpr bool C8 = FMT != kCode16;    // codes, which converter warps widen
+    constexpr bool C8 = kCoded<FMT>;        // codes, which converter warps widen
     constexpr bool C4 = FMT == kCodeInt4;  // with their scales, row by row
     constexpr bool BS = C8 && !C4;         // a scale per block, kept out of the tiles
+    constexpr bool HQ = FMT != kCode16;    // f16 products, whatever the queries' type
+    constexpr bool RQ = HQ && !BS;         // the queries' power of two is the scores' only factor
     constexpr bool RAW = !CAP && !ALIBI;  // the score's factor goes into the exponent's FMA
     using L = ModLayout<FMT>;
-    using M16 = typename std::conditional<C8, __half, T>::type;  // operand type of the products
+    using M16 = typename std::conditional<HQ, __half, T>::type;  // operand type of the products
     using H = Half16<M16>;
     constexpr bool kBf16 = std::is_same<M16, __nv_bfloat16>::value;
     constexpr bool kFree = CAP == kCapBounded;
@@ -693,7 +696,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             hi_r = min(total, max(pos + 1, A.prefix_lens ? A.prefix_lens[b] : 0));
             if (lo_r >= hi_r) lo_r = hi_r = 0;
         }
-        float rq = 1.f;  // C8: what the row's scores are multiplied by, a power of two
+        float rq = 1.f;  // HQ: what the row's scores are multiplied by, a power of two
         if (on) {
             const uint32_t sQt = sQ + static_cast<uint32_t>(t) * kModTile;
             if constexpr (C8) load_q();
@@ -702,7 +705,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const int rr = (warp & 3) * 32 + 2 * i + (lane >> 4), c = lane & 15;
                 st_shared_v4(sQt + (c >> 3) * kModHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4), qv[i].x, qv[i].y, qv[i].z, qv[i].w);
             }
-            if constexpr (C8 && std::is_same<T, __nv_bfloat16>::value) {
+            if constexpr (HQ && std::is_same<T, __nv_bfloat16>::value) {
                 // bf16 becomes f16 with the row's largest value moved to [2^13, 2^14), a row per
                 // thread in place (rolled loops: unrolled over the loads above they cost every CTA
                 // more in instruction fetches than they save)
@@ -782,7 +785,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 float top = 0.f;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const uint64_t sa = splat2(BS ? A.sa * f->ks[g0 + g] * rq : C4 ? A.sa * rq : A.sa);
+                    const uint64_t sa = splat2(BS ? A.sa * f->ks[g0 + g] * rq : RQ ? A.sa * rq : A.sa);
 #pragma unroll
                     for (int k = 16 * g; k < 16 * g + 16; k += 2) {
                         const uint64_t u = mul2(pack2(x[k], x[k + 1]), sa), u2 = mul2(u, u);
@@ -799,7 +802,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         tmem_ld32(scol + c0, v);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float su = BS ? A.su * f->ks[g0 + (c0 + i) / 16] * rq : C4 ? A.su * rq : A.su;
+                            const float su = BS ? A.su * f->ks[g0 + (c0 + i) / 16] * rq : RQ ? A.su * rq : A.su;
                             const float e = __uint_as_float(v[i]) * su;  // 2 log2 e score / cap
                             const float big = fmaf(fast_rcp(1.f + fast_exp2(e)), -2.f * A.capl2, A.capl2);
                             // each score by its own size: a row's bits are its own
@@ -820,7 +823,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const uint64_t on = splat2(-2.f * by);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const uint64_t sl = splat2(CAP ? 1.f : BS ? A.sl * f->ks[g0 + g] * rq : C4 ? A.sl * rq : A.sl);
+                    const uint64_t sl = splat2(CAP ? 1.f : BS ? A.sl * f->ks[g0 + g] * rq : RQ ? A.sl * rq : A.sl);
                     uint64_t bias = pack2(by * (c - 16 * g), by * (c - 16 * g - 1));  // two keys on by one addition
 #pragma unroll
                     for (int k = 16 * g; k < 16 * g + 16; k += 2) {
@@ -881,7 +884,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll
                 for (int k = 0; k < kHalfKeys; k += 2) m4[(k >> 1) & 3] = max3f(m4[(k >> 1) & 3], x[k], x[k + 1]);
                 mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                if (RAW) mx *= C4 ? A.sl * rq : A.sl;
+                if (RAW) mx *= RQ ? A.sl * rq : A.sl;
             }
             if (!kFree && mx > m_ref + kModRescale) {  // also the row's first visible key (m_ref = -inf)
                 if (m_ref != -INFINITY) {
@@ -917,7 +920,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             uint32_t pk[32];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const uint64_t mul = splat2(RAW ? (BS ? (scaled ? 1.f : A.sl * f->ks[g0 + g] * rq) : C4 ? A.sl * rq : A.sl) : 1.f);
+                const uint64_t mul = splat2(RAW ? (BS ? (scaled ? 1.f : A.sl * f->ks[g0 + g] * rq) : RQ ? A.sl * rq : A.sl) : 1.f);
                 const uint64_t sv = splat2(BS ? f->vs[g0 + g] : 1.f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -1069,8 +1072,8 @@ pkv_status prefill_mod_configure() {
     if (e == cudaSuccess && (done.load(std::memory_order_acquire) & bit)) return PKV_OK;
     auto kern = prefill_mod_kernel<T, FMT, CAP, ALIBI>;
     cudaFuncAttributes attr;
-    if (FMT != kCode16 && e == cudaSuccess) e = cudaFuncGetAttributes(&attr, kern);
-    if (FMT != kCode16 && e == cudaSuccess && attr.numRegs < kModLaunchRegs)
+    if (kCoded<FMT> && e == cudaSuccess) e = cudaFuncGetAttributes(&attr, kern);
+    if (kCoded<FMT> && e == cudaSuccess && attr.numRegs < kModLaunchRegs)
         return set_error(PKV_ERR_CUDA, "prefill: the kernel was built with %d registers, not %d", attr.numRegs, kModLaunchRegs);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ModLayout<FMT>::kAlloc);
@@ -1089,12 +1092,13 @@ pkv_status prefill_mod_launch(const PrefillCall &c) {
     if constexpr (FMT == kCodeInt4) {
         mk = mv = CUtensorMap{};  // its copies are whole runs of a (block, head)
         st = PKV_OK;
-    } else if constexpr (FMT != kCode16) {
+    } else if constexpr (kCoded<FMT>) {
         st = make_kv_map_8bit(&mk, c.k_cache, slots, c.Hkv, box_rows, 1);
         if (st == PKV_OK) st = make_kv_map_8bit(&mv, c.v_cache, slots, c.Hkv, box_rows, 1);
     } else {
-        st = make_kv_map_box(&mk, c.k_cache, Half16<T>::kTmaType, slots, c.Hkv, box_rows, 1);
-        if (st == PKV_OK) st = make_kv_map_box(&mv, c.v_cache, Half16<T>::kTmaType, slots, c.Hkv, box_rows, 1);
+        using M16 = typename std::conditional<FMT == kCodeF16, __half, T>::type;
+        st = make_kv_map_box(&mk, c.k_cache, Half16<M16>::kTmaType, slots, c.Hkv, box_rows, 1);
+        if (st == PKV_OK) st = make_kv_map_box(&mv, c.v_cache, Half16<M16>::kTmaType, slots, c.Hkv, box_rows, 1);
     }
     if (st == PKV_OK) st = prefill_mod_configure<T, FMT, CAP, ALIBI>();
     if (st != PKV_OK) return st;
@@ -1138,7 +1142,7 @@ pkv_status prefill_mod_launch(const PrefillCall &c) {
     if (static_cast<int64_t>(c.num_seqs) * a.pair_grids > 65535)
         return set_error(PKV_ERR_UNSUPPORTED, "prefill: max_q_len is too long for so many sequences");
     cudaError_t e = launch_pdl(kPdlDecode, prefill_mod_kernel<T, FMT, CAP, ALIBI>,
-                               dim3(c.Hkv, items < kMaxGridPairs ? items : kMaxGridPairs, c.num_seqs * a.pair_grids), dim3(kModThreads<FMT != kCode16>),
+                               dim3(c.Hkv, items < kMaxGridPairs ? items : kMaxGridPairs, c.num_seqs * a.pair_grids), dim3(kModThreads<kCoded<FMT>>),
                                ModLayout<FMT>::kAlloc, c.stream, mk, mv, a);
     if (e == cudaSuccess && a.nsplit > 1) {
         const int64_t rows = static_cast<int64_t>(c.num_seqs) * c.max_q_len * c.Hq;
@@ -1162,7 +1166,8 @@ pkv_status prefill_mod_format(const PrefillCall &c) {
     if constexpr (FMT == kCode16)
         if (c.dtype == PKV_BF16 && cap && !bias && c.mod.softcap * 1.4426950408889634f <= kFreeCap)
             return prefill_mod_launch<__nv_bfloat16, FMT, kCapBounded, false>(c);
-    return c.dtype == PKV_BF16 ? PKV_MOD(__nv_bfloat16) : PKV_MOD(__half);
+    if constexpr (FMT == kCodeF16) return PKV_MOD(__nv_bfloat16);  // f16 queries over f16 pools are kCode16
+    else return c.dtype == PKV_BF16 ? PKV_MOD(__nv_bfloat16) : PKV_MOD(__half);
 #undef PKV_MOD
 }
 

@@ -162,7 +162,9 @@ __device__ __forceinline__ uint32_t byte_pairs(uint32_t w) {
 }
 
 // Code formats of the caches the attention kernels read (4-bit codes carry their scales by row).
-enum CacheCode { kCode16 = 0, kCodeE4M3 = 1, kCodeInt8 = 2, kCodeInt4 = 3 };
+enum CacheCode { kCode16 = 0, kCodeE4M3 = 1, kCodeInt8 = 2, kCodeInt4 = 3, kCodeF16 = 4 };
+
+// kCodeF16: plain f16 values under queries of another type.
 
 // Four int8 codes -> two f16x2 words, exactly.  Each byte, offset by 128 to an
 // unsigned u (xor of its sign bit), becomes the low mantissa byte of the f16

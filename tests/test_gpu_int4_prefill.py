@@ -55,6 +55,66 @@ def test_spans(pkv, cuda_dev, spans):
     check(pkv, q, caches, tables, starts, cu, ns, spans, {"softcap": 20.0}, 128 ** -0.5, max_q=max(ns) + 200)
 
 
+LONG = [(0, 900), (37, 771), (512, 16), (5, 1), (3000, 900), (127, 130), (0, 800)]
+
+
+@pytest.mark.parametrize("rule", ["plain", "cap-alibi", "window-cap", "blind", "prefix-alibi"])
+@pytest.mark.parametrize("dtype,Hq,Hkv,bs", [(BF16, 8, 2, 16), (F16, 4, 2, 256), (BF16, 8, 1, 48)])
+def test_widened_rules(pkv, cuda_dev, dtype, Hq, Hkv, bs, rule):
+    """Calls of many rows, whose blocks are widened into the workspace first."""
+    q, caches, tables, starts, cu, ns = case(Hq, Hkv, bs, LONG, dtype, Hq + bs)
+    size = pkv.pkv_paged_attention_prefill_int4_workspace_size(len(LONG), Hq, Hkv, 128, bs, 900, tables.shape[1])
+    assert size > 2 * len(LONG) * 3900 * Hkv * 128 * 2
+    check(pkv, q, caches, tables, starts, cu, ns, LONG, _rules(rule, LONG, Hq, cuda_dev), 128 ** -0.5)
+
+
+def test_widened_equals_fused(pkv, cuda_dev):
+    """The same keys, the same products: a bound on the positions that changes the way changes no more than the order of sums."""
+    spans = [(100, 800)]
+    q, caches, tables, starts, cu, ns = case(8, 2, 16, spans, F16, 3)
+    wide = torch.full((1, 70000), -1, dtype=torch.int32, device=cuda_dev)  # a table for a million tokens: fused
+    wide[:, :tables.shape[1]] = tables
+    size = pkv.pkv_paged_attention_prefill_int4_workspace_size
+    # fused: the splits' workspace alone, as the 16-bit call's; widened: a pool of 57 blocks of K and of V too
+    assert size(1, 8, 2, 128, 16, 800, 70000) == pkv.pkv_paged_attention_prefill_mod_workspace_size(1, 8, 2, 128, 16, 800, 70000)
+    assert size(1, 8, 2, 128, 16, 800, 70000, 900) >= 2 * 57 * 16 * 2 * 128 * 2
+    a = check(pkv, q, caches, wide, starts, cu, ns, spans, {}, 0.1)
+    out = pkv.pkv_paged_attention_prefill_int4(q, *caches, wide, starts, cu, 0.1, 800, max_total_len=900)
+    assert bool(((a.float() - out.float()).abs() <= 2.0 ** -9 * a.float().abs() + 2.0 ** -10).all())
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+    out = pkv.pkv_paged_attention_prefill_int4(q, *caches, wide, starts, cu, 0.1, 800, max_total_len=880, err_flag=err)
+    assert int(err) == pkv.ERRBIT_CONTEXT and not bool(out.any())
+
+
+def test_widened_errors_and_two_graphs(pkv, cuda_dev):
+    spans = [(0, 800), (16, 790), (0, 800)]
+    q, caches, tables, starts, cu, ns = case(4, 2, 16, spans, BF16, 6)
+    want = check(pkv, q, caches, tables, starts, cu, ns, spans, {}, 0.1)
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+    bad = starts.clone()
+    bad[1] = -3
+    out = pkv.pkv_paged_attention_prefill_int4(q, *caches, tables, bad, cu, 0.1, 800, err_flag=err)
+    assert int(err) == pkv.ERRBIT_CONTEXT and not bool(out[800:1590].any())
+    assert torch.equal(out[:800], want[:800]) and torch.equal(out[1590:], want[1590:])
+    holes = tables.clone()
+    holes[2, 0], holes[0, 3] = -1, 10 ** 8
+    err.zero_()
+    out = pkv.pkv_paged_attention_prefill_int4(q, *caches, holes, starts, cu, 0.1, 800, err_flag=err)
+    assert int(err) == pkv.ERRBIT_BLOCK_RANGE and torch.isfinite(out).all() and not bool(out[1590:1606].any())
+    assert torch.equal(out[:48], want[:48]) and torch.equal(out[800:1590], want[800:1590])
+    # two graphs with a workspace each, replayed in turn
+    graphs, outs = [], []
+    for k in range(2):
+        g, o = torch.cuda.CUDAGraph(), torch.empty_like(q)
+        with torch.cuda.graph(g):
+            pkv.pkv_paged_attention_prefill_int4(q, *caches, tables if k == 0 else holes, starts, cu, 0.1, 800, out=o)
+        graphs.append(g)
+        outs.append(o)
+    for k in (0, 1, 0):
+        graphs[k].replay()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], out)
+
+
 def test_negative_scale_and_magnitudes(pkv, cuda_dev):
     spans = [(20, 70)]
     q, caches, tables, starts, cu, ns = case(8, 2, 16, spans, BF16, 5)

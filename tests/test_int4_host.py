@@ -86,13 +86,13 @@ def test_load_refuses(pkv, bad, status):
 
 DECODE = ["out", "q", "k_cache", "v_cache", "k_scale", "v_scale", "tables", "max_blocks", "lens", "B", "Hq", "Hkv", "d", "bs",
           "num_blocks", "max_ctx", "scale", "mod", "dtype", "ws", "ws_bytes", "err", "stream"]
-PREFILL = ["out", "q", "k_cache", "v_cache", "k_scale", "v_scale", "tables", "max_blocks", "starts", "cu", "B", "max_q", "Hq", "Hkv",
-           "d", "bs", "num_blocks", "scale", "mod", "dtype", "ws", "ws_bytes", "err", "stream"]
+PREFILL = ["out", "q", "k_cache", "v_cache", "k_scale", "v_scale", "tables", "max_blocks", "starts", "cu", "B", "max_q", "max_total",
+           "Hq", "Hkv", "d", "bs", "num_blocks", "scale", "mod", "dtype", "ws", "ws_bytes", "err", "stream"]
 
 
 def _attention(pkv, which, **kw):
     a = dict(out=_p(), q=_p(), k_cache=_p(), v_cache=_p(), k_scale=_p(), v_scale=_p(), tables=_p(), max_blocks=200, lens=_p(),
-             starts=_p(), cu=_p(), B=2, max_q=64, Hq=8, Hkv=2, d=128, bs=16, num_blocks=500, max_ctx=3000, scale=0.1, mod=None,
+             starts=_p(), cu=_p(), B=2, max_q=64, max_total=0, Hq=8, Hkv=2, d=128, bs=16, num_blocks=500, max_ctx=3000, scale=0.1, mod=None,
              dtype=pkv.PKV_BF16, ws=_p(), ws_bytes=1 << 30, err=None, stream=None)
     cap = kw.pop("softcap", None)
     if cap is not None:
@@ -119,7 +119,7 @@ def test_attention_refuses(pkv, which, bad, status):
 @pytest.mark.parametrize("which,bad,status", [
     ("decode", dict(max_ctx=-1), "INVALID_ARG"), ("decode", dict(max_ctx=2 ** 31 - 10), "INVALID_ARG"),
     ("decode", dict(lens=None), "INVALID_ARG"), ("prefill", dict(starts=None), "INVALID_ARG"), ("prefill", dict(cu=None), "INVALID_ARG"),
-    ("prefill", dict(max_q=-1), "INVALID_ARG"), ("prefill", dict(Hq=6), "UNSUPPORTED"), ("prefill", dict(d=64), "UNSUPPORTED"),
+    ("prefill", dict(max_q=-1), "INVALID_ARG"), ("prefill", dict(max_total=-1), "INVALID_ARG"), ("prefill", dict(Hq=6), "UNSUPPORTED"), ("prefill", dict(d=64), "UNSUPPORTED"),
     ("prefill", dict(B=70000), "UNSUPPORTED")])
 def test_one_attention_refuses(pkv, which, bad, status):
     assert _attention(pkv, which, **bad) == getattr(pkv, "PKV_ERR_" + status)
@@ -129,6 +129,16 @@ def test_empty_batches(pkv):
     assert _attention(pkv, "decode", B=0, q=None) == pkv.PKV_OK
     assert _attention(pkv, "prefill", B=0, q=None) == pkv.PKV_OK
     assert _attention(pkv, "prefill", max_q=0, q=None) == pkv.PKV_OK
+
+
+def test_prefill_workspace(pkv):
+    size, mod = pkv.pkv_paged_attention_prefill_int4_workspace_size, pkv.pkv_paged_attention_prefill_mod_workspace_size
+    assert size(8, 32, 8, 128, 16, 16, 256) == mod(8, 32, 8, 128, 16, 16, 256)  # few rows: widened as they are read
+    pool = 2 * 8 * 256 * 16 * 8 * 128 * 2
+    assert size(8, 32, 8, 128, 16, 4096, 256) == pool + 8 * 256 * 4
+    assert size(8, 32, 8, 128, 16, 4096, 256, 2048) == pool // 2 + 8 * 128 * 4  # a bound on the positions
+    assert size(64, 32, 8, 128, 16, 4096, 2048) == mod(64, 32, 8, 128, 16, 4096, 2048) == 0  # too much: 8 GiB
+    assert size(0, 32, 8, 128, 16, 4096, 256) == size(8, 32, 8, 64, 16, 4096, 256) == size(8, 32, 8, 128, 16, 4096, 256, -1) == 0
 
 
 def test_decode_workspace(pkv):
