@@ -188,7 +188,7 @@ __device__ __forceinline__ bool int4_near_border(float x, float s, int code, flo
 // dims are 2 lanes or twice 4 lanes, so a rotation never leaves a lane and a group's maximum
 // takes one or two shuffles.
 template <typename T, bool INTER, bool Q4>
-__global__ void __launch_bounds__(kRopeThreads, 4)
+__global__ void __launch_bounds__(kRopeThreads, Q4 && !INTER ? 4 : 5)
 rope_store_kernel(const __grid_constant__ RopeArgs A) {
     constexpr int U = sizeof(T) == 2 ? 4 : 2;  // steps in flight of the queries
     __shared__ __align__(16) float2 table[kRopeWarps][kRopeMaxDim / 2];
@@ -271,36 +271,40 @@ rope_store_kernel(const __grid_constant__ RopeArgs A) {
         const int hop = hpw * d;
         // Steps [from, to) of a token's `heads` heads from src to dst, rotated or as they are.
         auto stream = [&](const T *src, T *dst, int heads, int from, int to, bool turned) {
+            // steps of this lane: its head of a step exists
+            const int end = on ? min(to, hl < heads ? (heads - 1 - hl) / hpw + 1 : 0) : from;
+            src += static_cast<int64_t>(from) * hop;
+            dst += static_cast<int64_t>(from) * hop;
             for (int sb = from; sb < to; sb += U) {
                 Eight<T> x0[U], x1[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    if (sb + u < to && (sb + u) * hpw + hl < heads && on) {
-                        const T *p = src + static_cast<int64_t>(sb + u) * hop;
-                        x0[u].load(p + 8 * c0);
-                        x1[u].load(p + 8 * c1);
+                    if (sb + u < end) {
+                        x0[u].load(src + u * hop + 8 * c0);
+                        x1[u].load(src + u * hop + 8 * c1);
                     } else {
                         x0[u].clear();
                         x1[u].clear();
                     }
                 }
+                src += U * hop;
                 angles();
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    if (sb + u < to && (sb + u) * hpw + hl < heads && on) {
-                        if (turned) {  // (in halves both of the lane's chunks)
-                            float a[8], b[8], y0[8], y1[8];
-                            x0[u].get(a);
-                            x1[u].get(b);
-                            turn(a, b, true, y0, y1);
-                            x0[u].put(y0);
-                            x1[u].put(y1);
-                        }
-                        T *p = dst + static_cast<int64_t>(sb + u) * hop;
-                        x0[u].store(p + 8 * c0);
-                        x1[u].store(p + 8 * c1);
+                    if (turned) {  // (in halves both of the lane's chunks)
+                        float a[8], b[8], y0[8], y1[8];
+                        x0[u].get(a);
+                        x1[u].get(b);
+                        turn(a, b, true, y0, y1);
+                        x0[u].put(y0);
+                        x1[u].put(y1);
+                    }
+                    if (sb + u < end) {
+                        x0[u].store(dst + u * hop + 8 * c0);
+                        x1[u].store(dst + u * hop + 8 * c1);
                     }
                 }
+                dst += U * hop;
             }
         };
         if (s0 < nq)
