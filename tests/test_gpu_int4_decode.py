@@ -91,6 +91,58 @@ def test_decode(pkv, cuda_dev, Hq, Hkv, d, bs, dtype, rule):
                                     kw.get("key_starts")), scale)
 
 
+SHORT = [1, 16, 33, 0, 64, 65, 300, 511, 700, 1000]
+
+
+@pytest.mark.parametrize("rule", ["plain", "all", "window"])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("Hq,Hkv,d,bs", [(8, 8, 128, 16), (32, 8, 128, 48), (12, 1, 128, 256), (6, 2, 64, 16), (9, 1, 256, 16)])
+def test_few_short_contexts(pkv, cuda_dev, Hq, Hkv, d, bs, dtype, rule):
+    """A CTA per unit: no workspace, the warps' parts joined in shared memory."""
+    assert pkv.pkv_paged_attention_decode_int4_workspace_size(len(SHORT), Hq, Hkv, d, max(SHORT)) == 0
+    q, caches, tables = batch(Hq, Hkv, d, bs, SHORT, dtype, Hq + d + bs)
+    kw = rules(rule, SHORT, Hq)
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+    out = torch.full_like(q, float("nan"))
+    ctx = torch.tensor(SHORT, dtype=torch.int32, device=cuda_dev)
+    pkv.pkv_paged_attention_decode_int4(q, *caches, tables, ctx, d ** -0.5, max(SHORT), out=out, err_flag=err, **kw)
+    assert int(err) == 0
+    want = reference(q, caches, tables, SHORT, d ** -0.5, kw.get("softcap", 0.0), kw.get("alibi_slopes"), kw.get("key_starts"))
+    check(out, q, caches, want, d ** -0.5)
+    # the same batch under a bound that makes it slices and a join: two orders of the same sums
+    long = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, ctx, d ** -0.5, 1025, **kw)
+    check(long, q, caches, want, d ** -0.5)
+
+
+def test_two_streams_at_once(pkv, cuda_dev):
+    """Calls that overlap, each with the workspace of its own stream."""
+    ctx = [3000] * 8
+    q, caches, tables = batch(32, 8, 128, 16, ctx, BF16, 12)
+    lens = torch.tensor(ctx, dtype=torch.int32).cuda()
+    want = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, lens, 0.09, 3000)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    outs = [pkv.pkv_paged_attention_decode_int4(q, *caches, tables, lens, 0.09, 3000, stream=s) for _ in range(4) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_nan_stays_in_its_sequence_and_head(pkv, cuda_dev):
+    ctx = [300, 70, 1500]
+    q, caches, tables = batch(8, 2, 128, 16, ctx, F16, 13)
+    lens = torch.tensor(ctx, dtype=torch.int32).cuda()
+    for bound in (1500, 1 << 20):
+        want = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, lens, 0.09, bound)
+        hurt = q.clone()
+        hurt[1, 3, 5], hurt[2, 0, 0] = float("nan"), float("inf")
+        got = pkv.pkv_paged_attention_decode_int4(hurt, *caches, tables, lens, 0.09, bound)
+        assert bool(torch.isnan(got[1, 3]).all())
+        rest = torch.ones(3, 8, dtype=torch.bool, device=cuda_dev)
+        rest[1, 3] = rest[2, 0] = False
+        assert torch.isfinite(got[rest]).all() and bool(((got - want)[rest].abs() <= 2.0 ** -9 * (want[rest].abs() + 1)).all())
+
+
 @pytest.mark.parametrize("ctx", [[1], [40000], [3] * 600, [17000, 1, 0, 9]], ids=["one", "long", "many", "mixed"])
 def test_lengths(pkv, cuda_dev, ctx):
     q, caches, tables = batch(8, 2, 128, 16, ctx, BF16, 5)
