@@ -781,8 +781,9 @@ PKV_API pkv_status pkv_rope_store_kvcache_int4(void *q_out, const void *q, int64
  * pkv_paged_attention_decode_int4 -- "Step 2" over 4-bit caches, with score rules (`mod`, may
  * be NULL; key_starts [num_seqs]): pkv_paged_attention_decode of the values that the codes
  * stand for.  fp16 or bf16; q enters its product in f16 under a power of two per head, K as
- * what is stored; P is rounded to f16, and again times the scale of V (scales below 2^-14 lose
- * bits there); f32 scores and sums.
+ * what is stored; P is rounded to f16, and again times the scale of V (a weight relative to the
+ * largest, times its scale, loses bits there below 2^-24 max(1, the largest scale of V)); f32
+ * scores and sums.
  *   caches, scales   16-byte aligned, as are q and out
  *   workspace        pkv_paged_attention_decode_int4_workspace_size bytes (0 for few short
  *                    contexts), 256-byte aligned, needed during the call only; calls that may

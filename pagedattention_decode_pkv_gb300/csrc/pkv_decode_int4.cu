@@ -14,17 +14,31 @@
 //   * A group's scale multiplies its partial score in f32 (two products of 16 dims each).
 //   * V codes are widened exactly to u - 8.  A group's scale goes into P: p rounded to f16, times
 //     the scale, rounded again, each by 2^-12 of it at most on average, which is what the rounding
-//     of an fp16 output amounts to.  (The scales on V are exact, 64 more half-pair products a
-//     step of 32 tokens: 64 sequences of up to 4096 tokens 132 us against 123, 8 x 32768 61.7
-//     against 59.4.)
+//     of an fp16 output amounts to.  (The scales on V are exact, but 64 more half-pair products
+//     for 32 tokens: 64 sequences of up to 4096 tokens 132 us against 123, 8 x 32768 61.7 against
+//     59.4, when this was chosen.)
+//   * f16 has its bits above 2^-14 only, and a key far below the largest score may be one of many:
+//     P stands as high as the scales of V let it (kI4Slack), so that small values keep their weights
+//     (11 binades more than with the largest P at 1; 3 % of the time: 125 to 128 us, 57.9 to 59.5).
 //   * The transposed fragments of V come from ldmatrix.trans on 16-bit units: four dims of a
 //     token each, two tokens in a register, which is the pair the product wants.
+//   * The fixed offset of V could be taken out by a further product, 1024 + 8 times the row sum, as
+//     for K; but sums of f16 P near 1024 cancel badly where all scores are alike (a bias of 1.7e-3
+//     of |V|), and it was no faster.
 //
-// A warp works alone: it takes its own slice of the launch's (unit, 32-token step) list, a unit
-// being a (sequence, KV head, up to 8 of its query heads), copies its steps by cp.async into a
-// ring of its own and never meets another warp.  The list is cut evenly, whatever the mix of
-// lengths; a unit that several warps share leaves a piece (max, sum, accumulator) each, which a
-// second kernel joins.
+// A warp works alone: it takes its own slice of the launch's (unit, step of 64 tokens) list, a unit
+// being a (sequence, KV head, up to 8 of its query heads), copies its steps by cp.async into tiles
+// of its own (K of the next step while P V of this one runs, V while Q K does) and never meets
+// another warp.  The list is cut evenly, whatever the mix of lengths; a unit that several warps
+// share leaves a piece (max, sum, accumulator) each, which a second kernel joins.
+//
+// Measured with heads of 128 dims, on the GPU: 8 x 32768 tokens, 32 heads over 8 KV heads, 59.5 us, 5.1 TB/s;
+// 64 sequences of up to 4096 tokens, 32 heads each with its own K and V, 128 us, 4.1 TB/s; 4 of up to 500,
+// 16 heads over 8, 8.3 us, its launch and one chain of loads.
+// Long contexts are bound by the issue of what a byte feeds, 544 warp instructions for 32 tokens of a KV
+// head at 0.6 a clock and scheduler, 43 % of them on the integer pipe; the copies alone would keep HBM
+// busy.  Three warps a scheduler at 168 registers: 16 warps of 128 spill (8 x 32768 67 us, when that was
+// tried), steps of 32 tokens pay the rescaling and the table look-ups twice.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -51,7 +65,13 @@ constexpr int kI4Heads = 8;          // query heads of a unit
 // 16.5; 4 of up to 2000, where more SMs help, 15.6 / 12.4.
 constexpr int kI4DirectCtas = 3, kI4DirectLen = 1024;  // CTAs an SM (2 at head_dim 256)
 constexpr float kI4Log2e = 1.4426950408889634f;
-constexpr float kI4Slack = 2.5f;     // log2 units: 2^2.5 times the largest V scale is in f16's range
+// P, and P times a V scale, stay below 2^15, and as near to it as they can, since f16 has few bits
+// below 2^-14: P is 2^room at the score of its reference, and may pass that by kI4Slack binades.
+constexpr float kI4Slack = 4.f;
+constexpr int kI4TopExp = 14;  // exponent field of f16 scales below 1, the least that lowers room
+__device__ __forceinline__ uint32_t i4_top_scale(int exp) { return static_cast<uint32_t>((exp << 10) + 1023) * 0x10001u; }
+__device__ __forceinline__ int i4_exp(uint32_t scale) { return static_cast<int>(scale >> 10 & 63); }  // (a sign would count as a large one)
+__device__ __forceinline__ float i4_room(int top_exp) { return 29.f - kI4Slack - static_cast<float>(top_exp); }  // scales below 2^(top_exp - 14)
 
 struct I4Args {
     void *out;
@@ -72,6 +92,12 @@ struct I4Args {
 __device__ __forceinline__ int64_t i4_div(int64_t a, int64_t b) {  // a >= 0, b > 0
     if (((a | b) >> 32) == 0) return static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
     return a / b;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 // 16 bytes from global to shared memory.
@@ -382,7 +408,8 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
     };
 
     float o[NG][2][4];  // rows: dims 32 gg + 8 (g / 2) + g % 2 + 4 e (+ 2), columns: heads 2 t, 2 t + 1
-    float m0, m1, l0, l1, b0, b1;  // references (b = -m, 0 before there is one) and sums
+    float m0, m1, l0, l1, b0, b1;  // references (b = room - m, 0 before there is one) and sums
+    uint32_t top_scale = i4_top_scale(kI4TopExp);  // twice the largest f16 with the exponent field that room is for
     int pos = 0, ctx = 0, first = 0, cur_b = -1;  // of cur's step, and the sequence they are of
     bool fresh = true;                // the next step starts a unit
     bool whole = false;               // the unit began in this slice
@@ -409,6 +436,7 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
                     for (int c = 0; c < 4; ++c) o[gg][e][c] = 0.f;
             m0 = m1 = -INFINITY;
             l0 = l1 = b0 = b1 = 0.f;
+            top_scale = i4_top_scale(kI4TopExp);
             whole = cur.st == 0;
             if (!DIRECT && lane == 0 && whole) A.unit_info[static_cast<int64_t>(cur.b) * HU + cur.hu].x = static_cast<int>(me);
             fresh = false;
@@ -463,6 +491,27 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
         const bool more = s + 1 < count;
         if (more) copy_k();
         else asm volatile("cp.async.commit_group;" ::: "memory");  // (the group that the waits count)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // V: the next K may be under way
+        __syncwarp();
+        if (partial) {  // V scales of rows that are not seen may be anything, and P there is 0: their product must be 0
+            for (int k = lane; k < STEP; k += 32)
+                if (!seen(k)) {
+#pragma unroll
+                    for (int i = 0; i < NG / 2; ++i)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(v_tile + R::kCodes + k * (NG * 2) + 4 * i), "r"(0) : "memory");
+                }
+            __syncwarp();
+        }
+        uint32_t vmax;  // the largest of this lane's share of V's scales, by halves
+        {
+            constexpr int kWords = STEP * NG / 64;  // pairs of scales of a lane
+            static_assert(kWords == 2 || kWords == 4, "a vector of scales a lane");
+            uint32_t x[kWords];
+            lds_words(v_tile + R::kCodes + lane * (4 * kWords), x);
+            vmax = x[0];
+#pragma unroll
+            for (int i = 1; i < kWords; ++i) vmax = max_u16x2(vmax, x[i]);
+        }
         // 2. score rules, in log2 units (without them the factors sl0, sl1 > 0 wait for the exponent), and masks
         if constexpr (MOD) {
 #pragma unroll
@@ -499,8 +548,9 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
                 y[tile][3] = b ? y[tile][3] : -INFINITY;
             }
         }
-        // 3. The reference m of a head is a maximum of some step; P = 2^(y - m) may exceed 1 by
-        // kI4Slack binades before it is moved, and the sum and accumulator with it.
+        // 3. The reference m of a head is a maximum of some step; P = 2^(y - m + room) may pass 2^room
+        // by kI4Slack binades before it is moved, and the sum and accumulator with it; so they are where
+        // scales of V leave P less room.
         float mx0 = fmaxf(y[0][0], y[0][2]), mx1 = fmaxf(y[0][1], y[0][3]);
 #pragma unroll
         for (int tile = 1; tile < TILES; ++tile) {
@@ -511,18 +561,22 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
             mx0 *= sl0;
             mx1 *= sl1;
         }
-        if (__any_sync(0xffffffffu, mx0 > m0 + kI4Slack || mx1 > m1 + kI4Slack)) {
+        if (__any_sync(0xffffffffu, mx0 > m0 + kI4Slack || mx1 > m1 + kI4Slack || max_u16x2(vmax, top_scale) != top_scale)) {
 #pragma unroll
             for (int sh = 4; sh < 32; sh <<= 1) {
                 mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
             }
+            const int from = i4_exp(top_scale);
+            const int top = __reduce_max_sync(0xffffffffu, max(from, max(i4_exp(vmax), i4_exp(vmax >> 16))));
+            top_scale = i4_top_scale(top);
+            const float room = i4_room(top), less = fast_exp2(static_cast<float>(from - top));
             const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-            const float a0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0), a1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
+            const float a0 = n0 == -INFINITY ? 1.f : less * fast_exp2(m0 - n0), a1 = n1 == -INFINITY ? 1.f : less * fast_exp2(m1 - n1);
             m0 = n0;
             m1 = n1;
-            b0 = n0 == -INFINITY ? 0.f : -n0;
-            b1 = n1 == -INFINITY ? 0.f : -n1;
+            b0 = n0 == -INFINITY ? 0.f : room - n0;
+            b1 = n1 == -INFINITY ? 0.f : room - n1;
             l0 *= a0;
             l1 *= a1;
 #pragma unroll
@@ -534,17 +588,6 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
                     o[gg][e][2] *= a0;
                     o[gg][e][3] *= a1;
                 }
-        }
-        asm volatile("cp.async.wait_group 1;" ::: "memory");  // V: the next K may be under way
-        __syncwarp();
-        if (partial) {  // V scales of rows that are not seen may be anything, and P there is 0: their product must be 0
-            for (int k = lane; k < STEP; k += 32)
-                if (!seen(k)) {
-#pragma unroll
-                    for (int i = 0; i < NG / 2; ++i)
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(v_tile + R::kCodes + k * (NG * 2) + 4 * i), "r"(0) : "memory");
-                }
-            __syncwarp();
         }
         // 4. P and O += P V
 #pragma unroll
@@ -631,8 +674,9 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
                             po[hB * D + d + 2] = o[gg][e][3];
                         }
                     }
-                if (g == 0 && hA < heads) A.ml_piece[piece + hA] = make_float2(m0, l0);
-                if (g == 0 && hB < heads) A.ml_piece[piece + hB] = make_float2(m1, l1);
+                const float room = i4_room(i4_exp(top_scale));
+                if (g == 0 && hA < heads) A.ml_piece[piece + hA] = make_float2(m0 - room, l0);
+                if (g == 0 && hB < heads) A.ml_piece[piece + hB] = make_float2(m1 - room, l1);
             }
             if (ends) next_unit(cur);
         }
@@ -656,8 +700,9 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
                 l1 += __shfl_xor_sync(0xffffffffu, l1, sh);
             }
             if (g == 0) {
-                warp_ml[warp][2 * t] = make_float2(m0, l0);
-                warp_ml[warp][2 * t + 1] = make_float2(m1, l1);
+                const float room = i4_room(i4_exp(top_scale));
+                warp_ml[warp][2 * t] = make_float2(m0 - room, l0);
+                warp_ml[warp][2 * t + 1] = make_float2(m1 - room, l1);
             }
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg)

@@ -53,9 +53,10 @@
 // in their softmax together).  With the copies into the ring the step is 1534, with the
 // softmax warps beside it 1834.  Cap 50: 1049 us; the polynomial's operations come on
 // top.  With a bias 1236.  E4M3 and int8: 1264 and 1297; widening writes every tile once
-// more.  int4: 1231 (fp16, prompts of 3700 to 4096).  Short spans: of a CTA's ~13k clk of setup, first products and output nothing
-// overlaps, for both tiles do them together (2 x 8k rows of packed documents of 60 to
-// 2500 rows: 150 us, 664 TFLOP/s).
+// more.  4-bit codes: 1231 (fp16, prompts of 3700 to 4096), where the 16-bit kernel over the
+// same rows widened beforehand takes 988 with the widening.  Short spans: of a CTA's ~13k clk
+// of setup, first products and output nothing overlaps, for both tiles do them together (2 x
+// 8k rows of packed documents of 60 to 2500 rows: 150 us, 664 TFLOP/s).
 //
 // Few rows over a long context (a small chunk, few sequences) leave most SMs idle,
 // so the blocks of a tile pair are cut into up to nsplit runs, one CTA each, whose

@@ -9,7 +9,8 @@ of its largest term or partial sum, at most 1200 sum |q| over the group: togethe
 scale s 2^-10 sum |q| more.
 P is rounded to float16 twice, by itself and times V's scale, and not in the row sum: the same
 two half steps.  Below float16's normal range p s is off by 2^-25 and its codes are up to 7: that
-term is 2^-25 keys max(8, |V|), with p at least 1 for the key that set the reference.
+term is 2^-25 keys max(8, |V|), with p at least 1 for the key that set the reference (it is 2^11
+there where V's scales are below 1, and less by their binades else: the term shrinks with it).
 """
 import pytest
 import torch
@@ -91,6 +92,10 @@ def test_decode(pkv, cuda_dev, Hq, Hkv, d, bs, dtype, rule):
                                     kw.get("key_starts")), scale)
 
 
+def cdiv16(n):
+    return sr.cdiv(n, 16)
+
+
 SHORT = [1, 16, 33, 0, 64, 65, 300, 511, 700, 1000]
 
 
@@ -112,6 +117,61 @@ def test_few_short_contexts(pkv, cuda_dev, Hq, Hkv, d, bs, dtype, rule):
     # the same batch under a bound that makes it slices and a join: two orders of the same sums
     long = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, ctx, d ** -0.5, 1025, **kw)
     check(long, q, caches, want, d ** -0.5)
+
+
+@pytest.mark.parametrize("bound", [1025, 1 << 16])
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (4, 4, 64), (8, 1, 256)])
+def test_small_values(pkv, cuda_dev, Hq, Hkv, d, bound):
+    """Scales of V that are 2^11 times smaller (still normal in float16) are as exact, relative to them:
+    P makes use of float16's whole range, so p s leaves the normal range 2^11 later than the tolerance has it."""
+    ctx = [900, 1025, 77]
+    q, caches, tables = batch(Hq, Hkv, d, 16, ctx, BF16, 21 + d)
+    caches = (*caches[:3], caches[3].clamp(min=0.25))
+    lens = torch.tensor(ctx, dtype=torch.int32).cuda()
+    small = (*caches[:3], caches[3] / 2048)
+    out = pkv.pkv_paged_attention_decode_int4(q, *small, tables, lens, 0.3 * d ** -0.5, bound)
+    check(out * 2048, q, caches, reference(q, caches, tables, ctx, 0.3 * d ** -0.5), 0.3 * d ** -0.5)
+
+
+@pytest.mark.parametrize("bound", [900, 40000])
+def test_many_small_weights_of_small_values(pkv, cuda_dev, bound):
+    """One key far above the others, which together weigh more: p s of each is 2^-25 where p is 1 for that key.
+
+    The outputs are rounded by 2^-9 of them; p and p s by 2^-11 each of a magnitude that is below 2 times the
+    output; the one key's score is off by at most 2^-10 0.13 64, which moves the output by less than half of that.
+    Together 2^-9 + 2^-9 + 2^-7.9 < 2^-6.9."""
+    n, d = bound, 64
+    top = 12.0 if n > 5000 else 7.0  # binades
+    kc = torch.zeros(cdiv16(n), 1, 16, d)
+    kc[0, 0, 5] = 1
+    vc = torch.full_like(kc, 7)
+    vc[0, 0, 5] = -7
+    ks = torch.full((cdiv16(n), 1, 16, d // 32), top * 0.6931 / 64).to(F16)
+    vs = torch.full_like(ks, 2.0 ** (-13 if n > 5000 else -18))
+    caches = tuple(x.cuda() for x in (ref.pack(kc), ref.pack(vc), ks, vs))
+    q = torch.ones(1, 1, d, dtype=BF16).cuda()
+    tables = torch.arange(cdiv16(n), dtype=torch.int32).cuda()[None]
+    out = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, torch.tensor([n], dtype=torch.int32).cuda(), 1.0, bound)
+    want = reference(q, caches, tables, [n], 1.0)[0]
+    assert bool(((out.cpu().double() - want).abs() <= 2.0 ** -6.9 * want.abs()).all()), (out[0, 0, 0], want[0, 0, 0])
+
+
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (4, 4, 64), (8, 1, 256)])
+def test_scales_that_change_along_the_context(pkv, cuda_dev, Hq, Hkv, d, order):
+    """V's scales from 2^-8 to 2^8 and back down, so that the room of P moves within a unit."""
+    ctx = [1025, 600, 3000]
+    q, caches, tables = batch(Hq, Hkv, d, 16, ctx, BF16, 31 + d)
+    vs = caches[3].clone()
+    for b, c in enumerate(ctx):
+        for j in range(sr.cdiv(c, 16)):
+            e = round(8 * order * torch.tensor(j / 11.0).sin().item())
+            vs[tables[b, j].item()] = (vs[tables[b, j].item()].clamp(0.25, 4) * 2.0 ** e).to(F16)
+    caches = (*caches[:3], vs)
+    lens = torch.tensor(ctx, dtype=torch.int32).cuda()
+    for bound in (3000, 1 << 20):
+        out = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, lens, d ** -0.5, bound)
+        check(out, q, caches, reference(q, caches, tables, ctx, d ** -0.5), d ** -0.5)
 
 
 def test_two_streams_at_once(pkv, cuda_dev):
@@ -148,6 +208,17 @@ def test_lengths(pkv, cuda_dev, ctx):
     q, caches, tables = batch(8, 2, 128, 16, ctx, BF16, 5)
     out = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, torch.tensor(ctx, dtype=torch.int32).cuda(), 128 ** -0.5, max(ctx))
     check(out, q, caches, reference(q, caches, tables, ctx, 128 ** -0.5), 128 ** -0.5)
+
+
+@pytest.mark.parametrize("rule", ["window", "all"])
+def test_groups_of_sequences_with_rules(pkv, cuda_dev, rule):
+    ctx = [(7 * i) % 90 for i in range(1100)]  # three launches over one workspace
+    q, caches, tables = batch(4, 2, 64, 16, ctx, F16, 8)
+    kw = rules(rule, ctx, 4)
+    lens = torch.tensor(ctx, dtype=torch.int32).cuda()
+    out = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, lens, 0.125, max(ctx), **kw)
+    check(out, q, caches, reference(q, caches, tables, ctx, 0.125, kw.get("softcap", 0.0), kw.get("alibi_slopes"),
+                                    kw.get("key_starts")), 0.125)
 
 
 def test_errors_and_holes(pkv, cuda_dev):
