@@ -809,8 +809,9 @@ PKV_API pkv_status pkv_paged_attention_decode_int4(
  * as over 8-bit caches; P enters its product rounded to f16, and the row sum adds the rounded
  * values.  Calls of few rows, or over long tables, widen as they go; others (1024 rows of a KV head
  * and more, up to 1 GiB) widen the sequences' blocks once into the workspace.
- *   max_total_len  host bound on starts[b] + n_b, or 0 for the tables' width; sequences beyond it
- *                  are errors like those beyond their table.  It bounds the workspace.
+ *   max_total_len  host bound on starts[b] + n_b, or 0 for the tables' width; it bounds the
+ *                  workspace.  Where the call widens into it, sequences beyond the bound (rounded
+ *                  up to whole blocks) are errors like those beyond their table.
  *   workspace      pkv_paged_attention_prefill_int4_workspace_size bytes (may be 0), 256-byte
  *                  aligned, needed during the call only; calls that may overlap need one each
  *   scales         16-byte aligned, not negative

@@ -100,6 +100,9 @@ pkv_status pkv::prefill_mod_run(PrefillCall c, int format, int32_t head_dim, voi
     const size_t need = c.plan.ws_bytes + w.bytes;
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return set_error(PKV_ERR_WORKSPACE, "prefill: workspace needs %zu bytes (256-byte aligned), got %zu", need, workspace_bytes);
+    const int64_t grids = (static_cast<int64_t>(c.plan.pairs) * c.plan.nsplit + kMaxGridPairs - 1) / kMaxGridPairs;
+    if (c.num_seqs * grids > 65535)
+        return set_error(PKV_ERR_UNSUPPORTED, "prefill: max_q_len is too long for so many sequences");
     c.workspace = static_cast<char *>(workspace);
     if (w.bytes) {
         const pkv_status st = widen_int4(c, w, c.workspace + c.plan.ws_bytes);

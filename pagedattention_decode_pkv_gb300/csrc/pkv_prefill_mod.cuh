@@ -1140,8 +1140,6 @@ pkv_status prefill_mod_launch(const PrefillCall &c) {
     a.err_flag = c.err_flag;
     const int items = a.pairs * a.nsplit;
     a.pair_grids = (items + kMaxGridPairs - 1) / kMaxGridPairs;
-    if (static_cast<int64_t>(c.num_seqs) * a.pair_grids > 65535)
-        return set_error(PKV_ERR_UNSUPPORTED, "prefill: max_q_len is too long for so many sequences");
     cudaError_t e = launch_pdl(kPdlDecode, prefill_mod_kernel<T, FMT, CAP, ALIBI>,
                                dim3(c.Hkv, items < kMaxGridPairs ? items : kMaxGridPairs, c.num_seqs * a.pair_grids), dim3(kModThreads<kCoded<FMT>>),
                                ModLayout<FMT>::kAlloc, c.stream, mk, mv, a);

@@ -120,7 +120,9 @@ def test_attention_refuses(pkv, which, bad, status):
     ("decode", dict(max_ctx=-1), "INVALID_ARG"), ("decode", dict(max_ctx=2 ** 31 - 10), "INVALID_ARG"),
     ("decode", dict(lens=None), "INVALID_ARG"), ("prefill", dict(starts=None), "INVALID_ARG"), ("prefill", dict(cu=None), "INVALID_ARG"),
     ("prefill", dict(max_q=-1), "INVALID_ARG"), ("prefill", dict(max_total=-1), "INVALID_ARG"), ("prefill", dict(Hq=6), "UNSUPPORTED"), ("prefill", dict(d=64), "UNSUPPORTED"),
-    ("prefill", dict(B=70000), "UNSUPPORTED")])
+    ("prefill", dict(B=70000), "UNSUPPORTED"),
+    # too many tiles for a grid: refused before the blocks are widened into the workspace
+    ("prefill", dict(B=600, max_q=2 ** 31 - 1, max_total=16, Hkv=1), "UNSUPPORTED")])
 def test_one_attention_refuses(pkv, which, bad, status):
     assert _attention(pkv, which, **bad) == getattr(pkv, "PKV_ERR_" + status)
 
