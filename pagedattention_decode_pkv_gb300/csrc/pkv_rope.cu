@@ -19,13 +19,13 @@
 //
 // A warp takes a token's heads, a lane 16 dims of a head.  Measured with heads of 128 dims, on the GPU:
 //   * 16-bit rows are bound by HBM, four steps of heads loaded before the first is used: 16381 tokens of
-//     32 + 2 x 8 heads 68 us, 5.9 TB/s.
-//   * 4-bit rows are bound by the chain and the issue of the quantisation (52 % of the issue slots, 14
-//     warps an SM at 128 registers): 32700 tokens of 32 + 2 x 8 heads, bf16, 160 us, 4.4 TB/s; 5003 rows of
-//     32 heads, not rotated, 38 us, 2.8 TB/s.
+//     32 + 2 x 8 heads 66 us, 6.1 TB/s.
+//   * 4-bit rows are bound by the chain and the issue of the quantisation (half of the issue slots, 14
+//     warps an SM at 128 registers): 32700 tokens of 32 + 2 x 8 heads, bf16, 150 us, 4.7 TB/s; 5003 rows of
+//     32 heads, not rotated, 35 us, 3.0 TB/s.
 //   * A step of 64 tokens is its launch and one chain of loads, 6.3 us.
-//   * Reading back is bound by where the rows lie: 131001 tokens of 8 heads anywhere in the pool 150 us,
-//     4.6 TB/s of codes and outputs, for which DRAM reads 361 MB where the rows are 151.
+//   * Reading back is bound by HBM, and by where the rows lie: 131001 tokens of 8 heads, bf16, by whole
+//     blocks 107 us, 6.4 TB/s; anywhere in the pool 137 us, for DRAM reads 361 MB where the rows are 151.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -167,11 +167,12 @@ __device__ __forceinline__ uint32_t int4_word(const float (&x)[8], float s, floa
             near = fminf(near, fminf(fabsf(fabsf(r0) - 0.5f * s), fabsf(fabsf(r1) - 0.5f * s)));
         }
     }
-    // both halves of the word at once: nibble j is dim 2 j below and dim 2 j + 1 above; 0x8888: all + 8
-    const uint64_t u = add2(fma2(c[3], splat2(4096.f), fma2(c[2], splat2(256.f), fma2(c[1], splat2(16.f), c[0]))), splat2(34952.f));
+    // both halves of the word at once: nibble j is dim 2 j below and dim 2 j + 1 above; 2^23 + 0x8888: all
+    // + 8, and the integer in the low bits
+    const uint64_t sum = fma2(c[3], splat2(4096.f), fma2(c[2], splat2(256.f), fma2(c[1], splat2(16.f), c[0])));
     float lo, hi;
-    unpack2(u, lo, hi);
-    return static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
+    unpack2(add2(sum, splat2(8423560.f)), lo, hi);
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
 }
 
 // Nibble k of w, one of the two codes next to z / s, to the right one.
@@ -223,8 +224,6 @@ rope_store_kernel(const __grid_constant__ RopeArgs A) {
         const int part = static_cast<int>(item - i * A.parts);
         const int s0 = part * A.steps_per_part, s1 = min(s0 + A.steps_per_part, total);
         const int32_t slot = A.slots[i];
-        const bool stored = slot >= 0 && slot < A.num_slots;
-        if (slot != -1 && !stored && s0 <= nq && nq < s1 && lane == 0 && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_SLOT_RANGE);
         const int32_t position = r > 0 ? A.positions[i] : 0;
         float cs[8], sn[8];  // of pairs 8 l + k
         bool have = false;
@@ -314,12 +313,27 @@ rope_store_kernel(const __grid_constant__ RopeArgs A) {
                 dst += U * hop;
             }
         };
+        const T *key = static_cast<const T *>(A.key) + i * A.k_stride + lane_at;
+        const T *value = static_cast<const T *>(A.value) + i * A.v_stride + lane_at;
+        Eight<T> n0, n1;
+        auto load = [&](int e) {  // step e of the keys, then of the values
+            const int step = e < nk ? e : e - nk;
+            if (on && step * hpw + hl < A.Hkv) {
+                const T *p = (e < nk ? key : value) + static_cast<int64_t>(step) * hop;
+                n0.load(p + 8 * c0);
+                n1.load(p + 8 * c1);
+            } else {
+                n0.clear();
+                n1.clear();
+            }
+        };
+        if (Q4 && nq < s1) load(max(s0 - nq, 0));  // on its way beside the queries
         if (s0 < nq)
             stream(static_cast<const T *>(A.q) + i * A.q_stride + lane_at, static_cast<T *>(A.q_out) + i * A.Hq * d + lane_at, A.Hq, s0,
                    min(s1, nq), rot0);
+        const bool stored = slot >= 0 && slot < A.num_slots;
+        if (slot != -1 && !stored && s0 <= nq && nq < s1 && lane == 0 && A.err_flag) atomicOr(A.err_flag, PKV_ERRBIT_SLOT_RANGE);
         if (!stored || s1 <= nq) continue;
-        const T *key = static_cast<const T *>(A.key) + i * A.k_stride + lane_at;
-        const T *value = static_cast<const T *>(A.value) + i * A.v_stride + lane_at;
         if constexpr (!Q4) {
             const int64_t at = static_cast<int64_t>(slot) * A.Hkv * d + lane_at;
             stream(key, static_cast<T *>(A.k_cache) + at, A.Hkv, max(s0 - nq, 0), min(s1 - nq, nk), rot0);
@@ -329,20 +343,7 @@ rope_store_kernel(const __grid_constant__ RopeArgs A) {
             // unrolled over steps it outgrows the instruction caches (32700 tokens of 32 + 2 x 8
             // heads: four copies 394 us with the rows read back, two 274, at that step).
             const int64_t block = slot / A.bs, row0 = block * A.Hkv * A.bs + (slot - block * A.bs);
-            Eight<T> n0, n1;
-            auto load = [&](int e) {  // step e of the keys, then of the values
-                const int step = e < nk ? e : e - nk;
-                if (on && step * hpw + hl < A.Hkv) {
-                    const T *p = (e < nk ? key : value) + static_cast<int64_t>(step) * hop;
-                    n0.load(p + 8 * c0);
-                    n1.load(p + 8 * c1);
-                } else {
-                    n0.clear();
-                    n1.clear();
-                }
-            };
             const int last = s1 - nq;
-            load(max(s0 - nq, 0));
             angles();
 #pragma unroll 1
             for (int e = max(s0 - nq, 0); e < last; ++e) {
@@ -375,15 +376,19 @@ rope_store_kernel(const __grid_constant__ RopeArgs A) {
                 if (INTER) top1 = top0;
                 // |x_a| + |x_b| of a pair is at most sqrt(2) times its norm, which the turn keeps
                 // and which the groups' maxima bound; A is in them
-                const float err = turned ? 1.42f * kRotError * (top0 + top1) : 0.f;
-                float far = err;  // of the group
-                if (INTER) far = fmaxf(far, __shfl_xor_sync(0xffffffffu, far, 1));
+                const bool turns = role == 1 && r > 0;  // of a whole warp
+                float err = 0.f, far = 0.f;             // far: of the group
                 float m0, m1;
                 __half h0 = int4_scale(top0, m0), h1 = h0;
                 if (INTER) m1 = m0;
                 else h1 = int4_scale(top1, m1);
-                const bool unsure0 = far > 0.f && fabsf(fmaf(-7.f, m0, top0)) <= far;
-                const bool unsure1 = !INTER && far > 0.f && fabsf(fmaf(-7.f, m1, top1)) <= far;
+                bool unsure0 = false, unsure1 = false;
+                if (turns) {
+                    far = err = turned ? 1.42f * kRotError * (top0 + top1) : 0.f;
+                    if (INTER) far = fmaxf(far, __shfl_xor_sync(0xffffffffu, far, 1));
+                    unsure0 = far > 0.f && fabsf(fmaf(-7.f, m0, top0)) <= far;
+                    unsure1 = !INTER && far > 0.f && fabsf(fmaf(-7.f, m1, top1)) <= far;
+                }
                 // The pair k of the lane (its elements in y0, y1) in f64.
                 auto exact = [&](int k) -> double2 {
                     const float xa = !INTER ? a[k] : k < 4 ? a[2 * (k & 3)] : b[2 * (k & 3)];
@@ -391,7 +396,7 @@ rope_store_kernel(const __grid_constant__ RopeArgs A) {
                     return (INTER && k >= 4 ? loose1 : loose0) ? rotate_exact(position, A.turns[8 * l + k], A.amplitude, xa, xb)
                                                                : make_double2(xa, xb);
                 };
-                if (__any_sync(0xffffffffu, unsure0 || unsure1)) {  // a maximum next to the border of two scales
+                if (turns && __any_sync(0xffffffffu, unsure0 || unsure1)) {  // a maximum next to the border of two scales
                     double g0 = 0.0, g1 = 0.0;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
@@ -427,7 +432,7 @@ rope_store_kernel(const __grid_constant__ RopeArgs A) {
                 float gap0 = 3e38f, gap1 = 3e38f;
                 uint32_t w0, w1;
                 constexpr bool kWide = sizeof(T) == 4;
-                if (kWide || role == 1) {
+                if (kWide || turns) {
                     w0 = int4_word<true>(y0, t0, i0, kWide || loose0 ? 0.f : 384.f, gap0);
                     w1 = int4_word<true>(y1, t1, i1, kWide || loose1 ? 0.f : 384.f, gap1);
                 } else {
@@ -437,7 +442,7 @@ rope_store_kernel(const __grid_constant__ RopeArgs A) {
                 // rotated (and f32) values next to the border of two codes: 2^-18 s for x inv
                 const float e0 = fmaf(t0, 3.8e-6f, loose0 ? err : 0.f), e1 = fmaf(t1, 3.8e-6f, loose1 ? err : 0.f);
                 const bool border0 = (kWide || loose0) && t0 > 0.f && gap0 <= e0, border1 = (kWide || loose1) && t1 > 0.f && gap1 <= e1;
-                if (__any_sync(0xffffffffu, border0 || border1)) {
+                if ((kWide || turns) && __any_sync(0xffffffffu, border0 || border1)) {
                     uint32_t near0 = 0, near1 = 0;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
@@ -566,14 +571,34 @@ rope_store_generic_kernel(const __grid_constant__ RopeArgs A) {
 
 // ----------------------------------------------------------------------------- read back
 // Rows of both caches through a slot map: a word of eight codes a lane, widened, times its
-// scale (exact in f16), as 16 bytes; bf16 rounds once.
-constexpr int kLoadThreads = 256;
+// scale (exact in f16), as 16 bytes; bf16 rounds once.  A warp takes 128 words of a token.  CTAs in
+// the order of the tokens: as many as fit the GPU, each going from token to token, keep the
+// writes less together (131001 tokens of 8 heads, bf16, whole blocks: 105 us, 117 so).
+constexpr int kLoadThreads = 128, kLoadCtas = 1 << 20;
+
+// A word's codes as the bf16 pairs of u - 8, times a scale that bf16 holds.
+__device__ __forceinline__ uint4 int4_bf16(uint32_t w, uint32_t scale) {
+    uint32_t p[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // 128 + u - 136
+        asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(p[j]) : "r"(w >> 4 * j));
+        asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(p[j]) : "r"(0x43084308u));
+        asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(p[j]) : "r"(scale));
+    }
+    return make_uint4(p[0], p[1], p[2], p[3]);
+}
 
 template <typename T>
-__device__ __forceinline__ void store_eight(T *dst, uint32_t w, __half scale) {
+__device__ __forceinline__ void store_eight(T *dst, uint32_t w, __half scale, bool short_scale) {
+    const float t = __half2float(scale);
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        if (short_scale) {
+            *reinterpret_cast<uint4 *>(dst) = int4_bf16(w, __byte_perm(__float_as_uint(t), 0, 0x3232));
+            return;
+        }
+    }
     uint32_t p[4];
     int4_widen(w, p);
-    const __half2 s = __half2half2(scale);
     if constexpr (sizeof(T) == 4) {
         // a scale that this library did not write may have 11 bits: exact in f32
         float4 v[2];
@@ -581,8 +606,8 @@ __device__ __forceinline__ void store_eight(T *dst, uint32_t w, __half scale) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 c = __half22float2(*reinterpret_cast<__half2 *>(&p[j]));
-            f[2 * j] = c.x * __half2float(scale);
-            f[2 * j + 1] = c.y * __half2float(scale);
+            f[2 * j] = c.x * t;
+            f[2 * j + 1] = c.y * t;
         }
         reinterpret_cast<float4 *>(dst)[0] = v[0];
         reinterpret_cast<float4 *>(dst)[1] = v[1];
@@ -592,11 +617,10 @@ __device__ __forceinline__ void store_eight(T *dst, uint32_t w, __half scale) {
         for (int j = 0; j < 4; ++j) {
             const __half2 c = *reinterpret_cast<__half2 *>(&p[j]);
             if constexpr (std::is_same<T, __half>::value) {
-                const __half2 y = __hmul2(c, s);
+                const __half2 y = __hmul2(c, __half2half2(scale));
                 o[j] = *reinterpret_cast<const uint32_t *>(&y);
             } else {
                 const float2 f = __half22float2(c);
-                const float t = __half2float(scale);
                 const __nv_bfloat162 y = __floats2bfloat162_rn(f.x * t, f.y * t);
                 o[j] = *reinterpret_cast<const uint32_t *>(&y);
             }
@@ -616,39 +640,53 @@ load_int4_kernel(T *__restrict__ key, T *__restrict__ value, const uint32_t *__r
     pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int wph = d >> 3, words = Hkv * wph;  // words of a head, of a token
-    const int segs = (words + 32 * U - 1) / (32 * U);
-    const int64_t items = num_tokens * segs;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kLoadThreads / 32);
-    for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kLoadThreads / 32) + (threadIdx.x >> 5); item < items; item += warps) {
-        const int64_t i = item / segs;
-        const int w0 = static_cast<int>(item - i * segs) * 32 * U + lane;
-        const int32_t slot = slots[i];
-        const bool live = slot >= 0 && slot < num_slots;
-        if (!live && slot != -1 && w0 == 0 && err_flag) atomicOr(err_flag, PKV_ERRBIT_SLOT_RANGE);
-        const int64_t block = live ? slot / bs : 0;
-        const int64_t row0 = block * Hkv * bs + (live ? slot - block * bs : 0);
-        uint32_t kw[U], vw[U];
-        __half ks[U], vs[U];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kLoadThreads / 32);
+    for (int seg = blockIdx.y; seg * (32 * U) < words; seg += gridDim.y) {
+        const int w0 = seg * (32 * U) + lane;
+        int64_t i = static_cast<int64_t>(blockIdx.x) * (kLoadThreads / 32) + (threadIdx.x >> 5);
+        int32_t next = i < num_tokens ? slots[i] : -1;  // on its way beside the divisions
+        int64_t code_at[U];
+        int32_t ends = 0;  // of the lane's words, how many there are
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int w = w0 + 32 * u;
-            kw[u] = vw[u] = 0x88888888u;  // zeros
-            ks[u] = vs[u] = __float2half_rn(0.f);
-            if (live && w < words) {
-                const int h = w / wph, c = w - h * wph;
-                const int64_t row = row0 + static_cast<int64_t>(h) * bs;
-                kw[u] = __ldg(k_cache + row * wph + c);
-                vw[u] = __ldg(v_cache + row * wph + c);
-                ks[u] = __ldg(k_scale + row * (d >> 5) + (c >> 2));
-                vs[u] = __ldg(v_scale + row * (d >> 5) + (c >> 2));
-            }
+            const int w = w0 + 32 * u, h = w / wph;
+            code_at[u] = static_cast<int64_t>(h) * bs * wph + (w - h * wph);
+            ends += w < words ? 1 : 0;
         }
+        for (; i < num_tokens; i += step) {
+            const int32_t slot = next;
+            if (i + step < num_tokens) next = slots[i + step];
+            const bool live = slot >= 0 && slot < num_slots;
+            if (!live && slot != -1 && w0 == 0 && err_flag) atomicOr(err_flag, PKV_ERRBIT_SLOT_RANGE);
+            const int block = live ? slot / bs : 0;
+            // the slot's row of head 0, in words
+            const int64_t row = (static_cast<int64_t>(block) * Hkv * bs + (live ? slot - block * bs : 0)) * wph;
+            uint32_t kw[U], vw[U];
+            __half ks[U], vs[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int w = w0 + 32 * u;
-            if (w < words) {
-                store_eight<T>(key + (i * words + w) * 8, kw[u], ks[u]);
-                store_eight<T>(value + (i * words + w) * 8, vw[u], vs[u]);
+            for (int u = 0; u < U; ++u) {
+                kw[u] = vw[u] = 0x88888888u;  // zeros
+                ks[u] = vs[u] = __float2half_rn(0.f);
+                if (live && u < ends) {
+                    const int64_t at = row + code_at[u];  // a scale for every four words
+                    kw[u] = __ldg(k_cache + at);
+                    vw[u] = __ldg(v_cache + at);
+                    ks[u] = __ldg(k_scale + (at >> 2));
+                    vs[u] = __ldg(v_scale + (at >> 2));
+                }
+            }
+            // scales of eight bits, as the store writes them, are bf16 values too
+            uint32_t low = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) low |= __float_as_uint(__half2float(ks[u])) | __float_as_uint(__half2float(vs[u]));
+            const bool short_scales = __all_sync(0xffffffffu, (low & 0xffffu) == 0);
+            const int64_t out = (i * words + w0) * 8;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (u < ends) {
+                    store_eight<T>(key + out + 256 * u, kw[u], ks[u], short_scales);
+                    store_eight<T>(value + out + 256 * u, vw[u], vs[u], short_scales);
+                }
             }
         }
     }
@@ -851,8 +889,9 @@ extern "C" pkv_status pkv_load_kvcache_int4(void *key, void *value, const void *
         !aligned(v_scale, 2) || !aligned(slot_mapping, 4))
         return set_error(PKV_ERR_INVALID_ARG, "int4 load: key and value must be 16-byte aligned, codes 4-byte aligned");
     const int64_t segs = (static_cast<int64_t>(num_kv_heads) * head_dim / 8 + 127) / 128;
-    const int64_t ctas = (num_tokens * segs + kLoadThreads / 32 - 1) / (kLoadThreads / 32);
-    const dim3 grid(static_cast<unsigned>(ctas < 152 * 8 ? ctas : 152 * 8));
+    const int64_t y = segs < 64 ? segs : 64, x = (num_tokens + kLoadThreads / 32 - 1) / (kLoadThreads / 32);
+    const int64_t most = (kLoadCtas + y - 1) / y;
+    const dim3 grid(static_cast<unsigned>(x < most ? x : most), static_cast<unsigned>(y));
     auto s = static_cast<cudaStream_t>(stream);
     auto kc = static_cast<const uint32_t *>(k_cache), vc = static_cast<const uint32_t *>(v_cache);
     auto ks = reinterpret_cast<const __half *>(k_scale), vs = reinterpret_cast<const __half *>(v_scale);

@@ -108,6 +108,32 @@ def test_load(pkv, cuda_dev, dtype, H, d, bs):
         assert torch.equal(x.cpu(), want.to(dtype))
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_load_under_any_scales(pkv, cuda_dev, dtype):
+    """Scales of all eleven bits, subnormal ones and infinities among them: one rounding of the product."""
+    caches = list(ref.empty_cache(8, 3, 16, 64, 9))
+    g = torch.Generator().manual_seed(2)
+    caches[2] = torch.randint(0, 0x7c01, caches[2].shape, generator=g).to(torch.int16).view(F16)
+    caches[3][5, 1, 7, 0] = 1.0 + 2.0 ** -10  # alone among scales of eight bits
+    slots = torch.arange(8 * 16, dtype=torch.int32)
+    got = pkv.pkv_load_kvcache_int4(*[c.cuda() for c in caches], slots.cuda(), dtype)
+    for x, c, s in zip(got, caches[:2], caches[2:]):
+        want = ref.token_major(c, s).flatten(0, 1).float().to(dtype)  # (the product is exact in float32)
+        assert torch.equal(x.cpu().nan_to_num(7.0), want.nan_to_num(7.0))
+
+
+def test_load_more_tokens_than_a_grid_holds(pkv, cuda_dev):
+    caches = ref.empty_cache(30, 1, 16, 32, 10, cuda_dev)
+    n = 2 ** 22 + 77
+    slots = (torch.arange(n, dtype=torch.int64, device=cuda_dev) * 31 % 480).to(torch.int32)
+    slots[-1] = 480
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_dev)
+    for x, c, s in zip(pkv.pkv_load_kvcache_int4(*caches, slots, F16, err_flag=err), caches[:2], caches[2:]):
+        want = ref.token_major(c, s).flatten(0, 1).to(F16).to(cuda_dev)
+        assert torch.equal(x[:-1], want[slots[:-1].long()]) and not bool(x[-1].any())
+    assert int(err) == pkv.ERRBIT_SLOT_RANGE
+
+
 def test_load_skips_bad_slots(pkv, cuda_dev):
     caches = ref.empty_cache(4, 2, 16, 128, 8, cuda_dev)
     slots = torch.tensor([0, 64, -1, 63, -7], dtype=torch.int32).cuda()
