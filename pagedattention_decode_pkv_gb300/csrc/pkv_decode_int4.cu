@@ -7,10 +7,10 @@
 // A KV head of a token is 144 bytes of K and V at head_dim 128 where 16 bits take 512, so the
 // arithmetic that a byte feeds is 3.6 times that of the 16-bit kernel and the kernel is built
 // to keep it small:
-//   * K enters the products as it unpacks, f16 1024 + u (and 1024 + 16 u under q / 16): five
-//     operations for eight codes.  What 1024 + 8 adds is a constant per query and group, the
-//     accumulator's start, so the codes are never corrected; f32 sums of some 2^12 |q| carry
-//     it with an error of 2^-12 of a code step.
+//   * K enters the products as it unpacks: a nibble in the low byte of a half is the f16 number
+//     u 2^-24, or 16 u 2^-24 (under q / 16), exactly.  Five operations for eight codes; the 8 that a code
+//     is too large by is a constant per query and group, the accumulator's start.  (As 1024 + u, which
+//     costs the same, the start is 128 times larger and the score as much less exact.)
 //   * A group's scale multiplies its partial score in f32 (two products of 16 dims each).
 //   * V codes are widened exactly to u - 8.  A group's scale goes into P: p rounded to f16, times
 //     the scale, rounded again, each by 2^-12 of it at most on average, which is what the rounding
@@ -22,9 +22,9 @@
 //     (11 binades more than with the largest P at 1; 3 % of the time: 125 to 128 us, 57.9 to 59.5).
 //   * The transposed fragments of V come from ldmatrix.trans on 16-bit units: four dims of a
 //     token each, two tokens in a register, which is the pair the product wants.
-//   * The fixed offset of V could be taken out by a further product, 1024 + 8 times the row sum, as
-//     for K; but sums of f16 P near 1024 cancel badly where all scores are alike (a bias of 1.7e-3
-//     of |V|), and it was no faster.
+//   * The offset of V could be taken out by a further product, 8 times the weights' sum, as for K: fewer
+//     operations, but no faster (8 x 32768 59.5 us both ways, more registers), and the rounding of p
+//     then counts for 8 of every code.
 //
 // A warp works alone: it takes its own slice of the launch's (unit, step of 64 tokens) list, a unit
 // being a (sequence, KV head, up to 8 of its query heads), copies its steps by cp.async into tiles
@@ -33,7 +33,7 @@
 // share leaves a piece (max, sum, accumulator) each, which a second kernel joins.
 //
 // Measured with heads of 128 dims, on the GPU: 8 x 32768 tokens, 32 heads over 8 KV heads, 59.5 us, 5.1 TB/s;
-// 64 sequences of up to 4096 tokens, 32 heads each with its own K and V, 128 us, 4.1 TB/s; 4 of up to 500,
+// 64 sequences of up to 4096 tokens, 32 heads each with its own K and V, 126 us, 4.2 TB/s; 4 of up to 500,
 // 16 heads over 8, 8.3 us, its launch and one chain of loads.
 // Long contexts are bound by the issue of what a byte feeds, 544 warp instructions for 32 tokens of a KV
 // head at 0.6 a clock and scheduler, 43 % of them on the integer pipe; the copies alone would keep HBM
@@ -65,6 +65,7 @@ constexpr int kI4Heads = 8;          // query heads of a unit
 // 16.5; 4 of up to 2000, where more SMs help, 15.6 / 12.4.
 constexpr int kI4DirectCtas = 3, kI4DirectLen = 1024;  // CTAs an SM (2 at head_dim 256)
 constexpr float kI4Log2e = 1.4426950408889634f;
+constexpr float kI4Unit = 5.9604644775390625e-8f;  // 2^-24, f16's smallest
 // P, and P times a V scale, stay below 2^15, and as near to it as they can, since f16 has few bits
 // below 2^-14: P is 2^room at the score of its reference, and may pass that by kI4Slack binades.
 constexpr float kI4Slack = 4.f;
@@ -370,9 +371,9 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
             for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(get(gg, k)));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the largest value to [8, 16): all of a 16-bit type's bits down to 2^-17 of it, q / 16 included
+        // the largest value to [2^13, 2^14): all of a 16-bit type's bits down to 2^-23 of it, q / 16 included
         const int e = static_cast<int>(__float_as_uint(top) >> 23);
-        const int k2 = e == 0 || e == 255 ? 0 : min(max(130 - e, -120), 120);
+        const int k2 = e == 0 || e == 255 ? 0 : min(max(140 - e, -120), 120);
         const float f = __uint_as_float(static_cast<uint32_t>(k2 + 127) << 23);
         const float back = __uint_as_float(static_cast<uint32_t>(127 - k2) << 23);
         float start[NG];
@@ -385,13 +386,13 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
                 const uint32_t p = H::pack(get(gg, 2 * j) * w, get(gg, 2 * j + 1) * w);
                 qf[gg][j] = p;
                 const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&p));
-                a = fmaf(v.x + v.y, j & 1 ? -1152.f : -1032.f, a);
+                a = fmaf(v.x + v.y, j & 1 ? -128.f * kI4Unit : -8.f * kI4Unit, a);
             }
             a += __shfl_xor_sync(0xffffffffu, a, 1);
             a += __shfl_xor_sync(0xffffffffu, a, 2);
             start[gg] = a;
         }
-        const float sl = A.scale_log2 * back;
+        const float sl = fminf(fmaxf(A.scale_log2 * back * (1.f / kI4Unit), -3e38f), 3e38f);
         // from the lanes of head g to those of columns 2 t, 2 t + 1
 #pragma unroll
         for (int gg = 0; gg < NG; ++gg) {
@@ -471,10 +472,10 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
                 for (int e = 0; e < 2; ++e) {
                     uint32_t a[4];
                     const uint32_t x0 = e ? w[gg][0] >> 8 : w[gg][0], x1 = e ? w[gg][1] >> 8 : w[gg][1];
-                    asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(a[0]) : "r"(x0));
-                    asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xea;" : "=r"(a[1]) : "r"(x1));
-                    asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(a[2]) : "r"(x0));
-                    asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xea;" : "=r"(a[3]) : "r"(x1));
+                    a[0] = x0 & 0x000f000fu;
+                    a[1] = x1 & 0x000f000fu;
+                    a[2] = x0 & 0x00f000f0u;
+                    a[3] = x1 & 0x00f000f0u;
                     if (e == 0) mma_start(acc, a, qf[gg][0], qf[gg][1], off[gg][0], off[gg][1]);
                     else H::mma(acc, a, qf[gg][2], qf[gg][3]);
                 }
