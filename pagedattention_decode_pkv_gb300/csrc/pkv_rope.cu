@@ -20,7 +20,7 @@
 // A warp takes a token's heads, a lane 16 dims of a head.  Measured with heads of 128 dims, on the GPU:
 //   * 16-bit rows are bound by HBM, four steps of heads loaded before the first is used: 16381 tokens of
 //     32 + 2 x 8 heads 66 us, 6.1 TB/s.
-//   * 4-bit rows are bound by the chain and the issue of the quantisation (half of the issue slots, 14
+//   * 4-bit rows are bound by the chain and the issue of the quantisation (55 % of the issue slots, 14
 //     warps an SM at 128 registers): 32700 tokens of 32 + 2 x 8 heads, bf16, 150 us, 4.7 TB/s; 5003 rows of
 //     32 heads, not rotated, 35 us, 3.0 TB/s.
 //   * A step of 64 tokens is its launch and one chain of loads, 6.3 us.
