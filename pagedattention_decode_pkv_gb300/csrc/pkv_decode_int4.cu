@@ -392,7 +392,8 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
             a += __shfl_xor_sync(0xffffffffu, a, 2);
             start[gg] = a;
         }
-        const float sl = fminf(fmaxf(A.scale_log2 * back * (1.f / kI4Unit), -3e38f), 3e38f);
+        const float whole_sl = A.scale_log2 * back * (1.f / kI4Unit);
+        const float sl = fabsf(whole_sl) > 3e38f ? copysignf(3e38f, whole_sl) : whole_sl;  // (times a score of 0 is 0)
         // from the lanes of head g to those of columns 2 t, 2 t + 1
 #pragma unroll
         for (int gg = 0; gg < NG; ++gg) {

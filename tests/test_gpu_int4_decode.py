@@ -200,6 +200,7 @@ def test_nan_stays_in_its_sequence_and_head(pkv, cuda_dev):
         assert bool(torch.isnan(got[1, 3]).all())
         rest = torch.ones(3, 8, dtype=torch.bool, device=cuda_dev)
         rest[1, 3] = rest[2, 0] = False
+        assert bool(torch.isnan(pkv.pkv_paged_attention_decode_int4(q, *caches, tables, lens, float("nan"), bound)).all())
         assert torch.isfinite(got[rest]).all() and bool(((got - want)[rest].abs() <= 2.0 ** -9 * (want[rest].abs() + 1)).all())
 
 
@@ -249,7 +250,7 @@ def test_errors_and_holes(pkv, cuda_dev):
     assert int(err) == 0
 
 
-@pytest.mark.parametrize("gain", [2.0 ** -30, 1e-3, 1.0, 3e4])
+@pytest.mark.parametrize("gain", [2.0 ** -100, 2.0 ** -30, 1e-3, 1.0, 3e4, 2.0 ** 90, 2.0 ** 110])
 def test_magnitudes(pkv, cuda_dev, gain):
     """Queries far from unit size: the scores, not the queries, decide (the scale makes up for it)."""
     ctx = [200, 33]
