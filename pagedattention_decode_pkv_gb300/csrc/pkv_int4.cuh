@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kInt4Group = 32;         // dims that share a scale
 constexpr float kInt4TopScale = 9344.f;
+constexpr float kInt4TopInput = 3e38f;  // larger maxima are taken as this; both have the largest scale
 
 // The bf16 nearest to top / 7 (ties to even) for top >= 0, exactly: the remainder of a midpoint
 // says on which side of it the quotient is, and an f32 product off by a few 2^-24 always finds
@@ -41,7 +42,7 @@ __device__ __forceinline__ float int4_seventh_bf16(float top, float &mid) {
 // The stored scale of a group whose largest magnitude is `top` (NaN left out by the caller), and
 // the midpoint of two bf16 values nearest to top / 7.
 __device__ __forceinline__ __half int4_scale(float top, float &mid) {
-    const float s = int4_seventh_bf16(fminf(top, 3e38f), mid);
+    const float s = int4_seventh_bf16(fminf(top, kInt4TopInput), mid);
     return __float2half_rn(fminf(s, kInt4TopScale));
 }
 

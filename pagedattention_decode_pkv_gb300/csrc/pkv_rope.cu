@@ -123,7 +123,7 @@ __device__ __noinline__ double2 rotate_exact(int32_t position, uint64_t turns, d
 
 // int4_scale of an f64 maximum.
 __device__ __forceinline__ __half int4_scale_f64(double top) {
-    if (!(top < 3e38)) return __float2half_rn(kInt4TopScale);
+    if (!(top < kInt4TopInput)) return __float2half_rn(kInt4TopScale);
     float mid;
     int4_seventh_bf16(static_cast<float>(top), mid);
     const uint32_t lo = __float_as_uint(mid) & 0xffff0000u;
@@ -386,8 +386,10 @@ rope_store_kernel(const __grid_constant__ RopeArgs A) {
                 if (turns) {
                     far = err = turned ? 1.42f * kRotError * (top0 + top1) : 0.f;
                     if (INTER) far = fmaxf(far, __shfl_xor_sync(0xffffffffu, far, 1));
-                    unsure0 = far > 0.f && fabsf(fmaf(-7.f, m0, top0)) <= far;
-                    unsure1 = !INTER && far > 0.f && fabsf(fmaf(-7.f, m1, top1)) <= far;
+                    // a maximum beyond int4_scale's range is far beyond the largest scale, and top - 2 far below
+                    // would not be a number
+                    unsure0 = far > 0.f && top0 < kInt4TopInput && fabsf(fmaf(-7.f, m0, top0)) <= far;
+                    unsure1 = !INTER && far > 0.f && top1 < kInt4TopInput && fabsf(fmaf(-7.f, m1, top1)) <= far;
                 }
                 // The pair k of the lane (its elements in y0, y1) in f64.
                 auto exact = [&](int k) -> double2 {

@@ -1,0 +1,57 @@
+"""The 4-bit cache at the ends of its inputs' ranges: codes and scales are equal to the
+definition's in binary64, bit for bit, in the vector kernels ("apart") and the scalar one ("odd")."""
+import pytest
+import torch
+
+import int4_reference as ref
+from test_gpu_int4_cache import _same
+from test_gpu_rope import BF16, F16, F32, rope_of
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+
+
+def _laid_out(x, layout):
+    """x [n, H, d] on the device, its rows aligned for vectors or not."""
+    n, H, d = x.shape
+    if layout == "apart":
+        return x.cuda()
+    buf = torch.zeros(n, H * d + 1, dtype=x.dtype, device="cuda")
+    key = buf[:, 1:].unflatten(1, (H, d))
+    key.copy_(x)
+    return key
+
+
+def _store_and_compare(pkv, x, pos, rope, freq, amp, inter, layout):
+    """Stores x [n, H, d] as keys, rotated, and as values; compares both caches."""
+    n, H, d = x.shape
+    nb = -(-n // 16)
+    slots = torch.arange(n, dtype=torch.int32)
+    caches = ref.empty_cache(nb, H, 16, d, 4, "cuda")
+    want = ref.stored(caches, ref.rotate(x, pos, freq, amp, inter)[0], x.double(), slots)
+    key = _laid_out(x, layout)
+    pkv.pkv_rope_store_kvcache_int4(key, key, key, pos.cuda(), rope, *caches, slots.cuda(), interleaved=inter)
+    _same(caches, want)
+
+
+@pytest.mark.parametrize("scaling", [None, "yarn"])
+@pytest.mark.parametrize("layout", ["apart", "odd"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_rotated_keys_beyond_the_range(pkv, cuda_dev, dtype, inter, layout, scaling):
+    """Infinities, NaN and values whose rotation leaves float32: what is beyond 65408 saturates, and the
+    rest of its group is stored under the largest scale.  No sine or cosine here is near 0 but at position 0."""
+    d = 128
+    plants = [{3: INF}, {70: -INF}, {3: INF, 67: INF}, {3: -INF, 67: INF}, {8: INF, 9: -INF}, {9: NAN, 40: INF}, {5: NAN}]
+    if dtype != F16:
+        plants += [{5: 3.3e38, 69: 3.3e38}, {4: 3.3e38, 5: -3.3e38}, {20: 3.0e38, 21: 3.3e38, 84: -3.0e38, 85: 3.3e38},
+                   {j: 3.3e38 * (-1) ** (j // 3) for j in range(d)}]
+    positions = [0, 1, 7, 12345]
+    g = torch.Generator().manual_seed(5)
+    x = (torch.randn(len(plants) * len(positions), 2, d, generator=g) * 20000).clamp(-60000, 60000)
+    for i in range(x.shape[0]):
+        for j, v in plants[i % len(plants)].items():
+            x[i, 0, j] = v
+    pos = torch.tensor(positions, dtype=torch.int32).repeat_interleave(len(plants))
+    rope, (freq, amp) = rope_of(pkv, d, scaling)
+    _store_and_compare(pkv, x.to(dtype), pos, rope, freq, amp, inter, layout)
