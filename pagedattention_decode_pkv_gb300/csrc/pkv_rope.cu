@@ -423,7 +423,9 @@ rope_store_kernel(const __grid_constant__ RopeArgs A) {
                     if (INTER) h1 = h0;
                 }
                 const float t0 = __half2float(h0), t1 = __half2float(h1);
-                if (__any_sync(0xffffffffu, top0 > 7.5f * t0 || top1 > 7.5f * t1)) {  // saturated groups, or too small for a scale
+                // Saturated groups, or too small for a scale, or under a subnormal one, coarse enough that the largest
+                // value is 7.5 of them and would round to 8; under a normal scale it is at most 7 (1 + 2^-8).
+                if (__any_sync(0xffffffffu, top0 > 7.25f * t0 || top1 > 7.25f * t1)) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         y0[k] = fminf(fmaxf(y0[k], -7.f * t0), 7.f * t0);

@@ -55,3 +55,32 @@ def test_rotated_keys_beyond_the_range(pkv, cuda_dev, dtype, inter, layout, scal
     pos = torch.tensor(positions, dtype=torch.int32).repeat_interleave(len(plants))
     rope, (freq, amp) = rope_of(pkv, d, scaling)
     _store_and_compare(pkv, x.to(dtype), pos, rope, freq, amp, inter, layout)
+
+
+@pytest.mark.parametrize("turned", [False, True])
+@pytest.mark.parametrize("layout", ["apart", "odd"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_largest_value_of_seven_and_a_half_steps(pkv, cuda_dev, dtype, inter, layout, turned):
+    """Small scales are multiples k of 2^-24, so that a group's largest value may be 7.5 of them, a tie whose
+    even side, 8, is no code; so may 70080 under the largest scale.  Each in all places of a group, both signs; in
+    float32 their neighbours too.  At position 0, where a turn is exact, and as they stand."""
+    tops = [7.5 * k * 2.0 ** -24 for k in range(1, 8)]
+    if dtype == F32:
+        tops.append(70080.0)
+        tops += [torch.nextafter(torch.tensor(t), torch.tensor(to)).item() for t in tops for to in (0.0, INF)]
+    tops = [t for t in tops if torch.tensor(t).to(dtype).double() == t]
+    assert len(tops) >= 3
+    g = torch.Generator().manual_seed(6)
+    groups = []
+    for t in tops:
+        for sign in (1, -1):
+            for place in range(32):
+                x = t * torch.randint(-7, 8, (32,), generator=g) / 7.5
+                x[place] = sign * t
+                groups.append(x)
+    x = torch.stack(groups).reshape(-1, 1, 128).to(dtype)
+    pos = torch.zeros(x.shape[0], dtype=torch.int32)
+    r = 128 if turned else 0
+    rope, (freq, amp) = rope_of(pkv, r, None)
+    _store_and_compare(pkv, x, pos, rope, freq, amp, inter, layout)
