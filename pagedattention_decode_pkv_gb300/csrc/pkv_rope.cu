@@ -175,12 +175,11 @@ __device__ __forceinline__ uint32_t int4_word(const float (&x)[8], float s, floa
     return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
 }
 
-// Nibble k of w, one of the two codes next to z / s, to the right one.
-__device__ __forceinline__ void int4_settle(uint32_t &w, int k, double z, float s) {
-    const int c = static_cast<int>(w >> int4_shift(k) & 15) - 8;
-    const double r = fma(-static_cast<double>(c), static_cast<double>(s), z), h = 0.5 * s;
-    const int to = c + (r > 0.0 ? 1 : -1);  // (values that saturate stay where they are)
-    if ((fabs(r) > h || (fabs(r) == h && (c & 1))) && to >= -7 && to <= 7) w += static_cast<uint32_t>(to - c) << int4_shift(k);
+// w with the nibble at `shift` as the code of z under s > 0.  (Of a pair that cancels, f32 may have been off by
+// any number of codes.)
+__device__ __noinline__ uint32_t int4_settled(uint32_t w, int shift, double z, float s) {
+    const int c = static_cast<int>(w >> shift & 15) - 8;
+    return w + (static_cast<uint32_t>(int4_code_f64(z, s) - c) << shift);
 }
 
 // Whether x lies within `err` of the border between two codes under s.
@@ -461,8 +460,9 @@ rope_store_kernel(const __grid_constant__ RopeArgs A) {
                         if (__any_sync(0xffffffffu, (na >> ea & 1) || (nb >> eb & 1))) {
                             const double2 z = exact(k);
                             const bool second = INTER && k >= 4;
-                            if (na >> ea & 1) int4_settle(second ? w1 : w0, ea, z.x, second ? t1 : t0);
-                            if (nb >> eb & 1) int4_settle(!INTER || second ? w1 : w0, eb, z.y, !INTER || second ? t1 : t0);
+                            uint32_t &wa = second ? w1 : w0, &wb = !INTER || second ? w1 : w0;
+                            if (na >> ea & 1) wa = int4_settled(wa, int4_shift(ea), z.x, second ? t1 : t0);
+                            if (nb >> eb & 1) wb = int4_settled(wb, int4_shift(eb), z.y, !INTER || second ? t1 : t0);
                         }
                     }
                 }

@@ -84,3 +84,22 @@ def test_largest_value_of_seven_and_a_half_steps(pkv, cuda_dev, dtype, inter, la
     r = 128 if turned else 0
     rope, (freq, amp) = rope_of(pkv, r, None)
     _store_and_compare(pkv, x, pos, rope, freq, amp, inter, layout)
+
+
+@pytest.mark.parametrize("layout", ["apart", "odd"])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_pairs_that_cancel(pkv, cuda_dev, dtype, layout):
+    """A group of small values turned from large ones, which float32 has wrong by many codes: angles of some
+    1e-9 (so far below float32's of a turn), and pairs whose rotation is a remainder of 2^-24 of them."""
+    n, d, half = 64, 128, 64
+    g = torch.Generator().manual_seed(7)
+    size = 10000 + 50000 * torch.rand(n, 1, half, generator=g)
+    big = (size * (1 - 2 * torch.randint(0, 2, size.shape, generator=g))).to(dtype)
+    pos = torch.randint(1, 4, (n,), generator=g, dtype=torch.int32)
+    freq = [(0.5 + i / half) * 1e-9 for i in range(half)]
+    _store_and_compare(pkv, torch.cat([torch.zeros_like(big), big], -1), pos, pkv.pkv_rope_turns(freq), freq, 1.0, False, layout)
+    if dtype == F32:
+        freq = [0.3 + i / half for i in range(half)]
+        t = ref.angles(pos, freq)[:, None]
+        first = big.double() * torch.tan(t)  # first cos - big sin = 0 but for its rounding
+        _store_and_compare(pkv, torch.cat([first.float(), big], -1), pos, pkv.pkv_rope_turns(freq), freq, 1.0, False, layout)
