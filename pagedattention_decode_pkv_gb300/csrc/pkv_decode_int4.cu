@@ -393,7 +393,9 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
             start[gg] = a;
         }
         const float whole_sl = A.scale_log2 * back * (1.f / kI4Unit);
-        const float sl = fabsf(whole_sl) > 3e38f ? copysignf(3e38f, whole_sl) : whole_sl;  // (times a score of 0 is 0)
+        // finite, and without rules not 0 either: times a score of 0, or of -inf (a masked one), it is a number
+        const float top_sl = fabsf(whole_sl) > 3e38f ? copysignf(3e38f, whole_sl) : whole_sl;
+        const float sl = MOD ? top_sl : fmaxf(top_sl, 1.17549435e-38f);
         // from the lanes of head g to those of columns 2 t, 2 t + 1
 #pragma unroll
         for (int gg = 0; gg < NG; ++gg) {

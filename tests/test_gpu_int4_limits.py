@@ -1,10 +1,12 @@
-"""The 4-bit cache at the ends of its inputs' ranges: codes and scales are equal to the
-definition's in binary64, bit for bit, in the vector kernels ("apart") and the scalar one ("odd")."""
+"""The 4-bit cache at the ends of its inputs' ranges.  Stored codes and scales are equal to the
+definition's in binary64, bit for bit, in the vector kernels ("apart") and the scalar one ("odd");
+attention is within the tolerance of its own tests."""
 import pytest
 import torch
 
 import int4_reference as ref
 from test_gpu_int4_cache import _same
+from test_gpu_int4_decode import batch, check as decode_check, reference
 from test_gpu_rope import BF16, F16, F32, rope_of
 
 pytestmark = pytest.mark.gpu
@@ -103,3 +105,22 @@ def test_pairs_that_cancel(pkv, cuda_dev, dtype, layout):
         t = ref.angles(pos, freq)[:, None]
         first = big.double() * torch.tan(t)  # first cos - big sin = 0 but for its rounding
         _store_and_compare(pkv, torch.cat([first.float(), big], -1), pos, pkv.pkv_rope_turns(freq), freq, 1.0, False, layout)
+
+
+@pytest.mark.parametrize("gain", [2.0 ** -119, 2.0 ** -105, 2.0 ** 120])
+def test_decode_of_queries_and_scales_far_from_one(pkv, cuda_dev, gain):
+    """The factor of the scores leaves float32 below: they are all 0, and every key counts alike.  Where it leaves it above,
+    scores of 0 stay 0."""
+    ctx = [200, 33, 1]
+    q, caches, tables = batch(8, 2, 128, 16, ctx, BF16, 8)
+    scale = 1e-12
+    if gain > 1:
+        q, scale = torch.zeros_like(q), 1e20
+        q[..., 5] = gain
+        caches[0][:, :, :, 0:4] = 0x88  # dims 0 .. 7 of K: zeros
+    else:
+        q = (q.float() * gain).to(BF16)
+    lens = torch.tensor(ctx, dtype=torch.int32).cuda()
+    for bound in (200, 5000):
+        out = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, lens, scale, bound)
+        decode_check(out, q, caches, reference(q, caches, tables, ctx, scale), 0.0 if gain > 1 else scale)
