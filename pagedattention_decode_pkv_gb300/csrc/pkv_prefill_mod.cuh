@@ -739,6 +739,13 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::kQFull + t));
         }
+        // The scores' factor f of this row where rq is all of it: finite, so that a score of 0 stays 0.
+        auto by_row = [&](float f) {
+            const float v = f * rq;
+            return fabsf(v) > 3e38f ? copysignf(3e38f, v) : v;
+        };
+        // RAW: not 0 either, since it meets masked scores, which are -inf
+        const float raw_sl = RQ ? fmaxf(by_row(A.sl), 1.17549435e-38f) : A.sl;
         const float nslope = ALIBI && A.slopes && live ? -A.slopes[kh * G + hd] * 1.4426950408889634f : 0.f;
         // this warp's TMEM lanes (32 (warp % 4) ..) in the tile's columns: S / P at 0 and 64, O at 128
         const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 256;
@@ -786,7 +793,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 float top = 0.f;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const uint64_t sa = splat2(BS ? A.sa * f->ks[g0 + g] * rq : RQ ? A.sa * rq : A.sa);
+                    const uint64_t sa = splat2(BS ? A.sa * f->ks[g0 + g] * rq : RQ ? by_row(A.sa) : A.sa);
 #pragma unroll
                     for (int k = 16 * g; k < 16 * g + 16; k += 2) {
                         const uint64_t u = mul2(pack2(x[k], x[k + 1]), sa), u2 = mul2(u, u);
@@ -803,7 +810,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         tmem_ld32(scol + c0, v);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float su = BS ? A.su * f->ks[g0 + (c0 + i) / 16] * rq : RQ ? A.su * rq : A.su;
+                            const float su = BS ? A.su * f->ks[g0 + (c0 + i) / 16] * rq : RQ ? by_row(A.su) : A.su;
                             const float e = __uint_as_float(v[i]) * su;  // 2 log2 e score / cap
                             const float big = fmaf(fast_rcp(1.f + fast_exp2(e)), -2.f * A.capl2, A.capl2);
                             // each score by its own size: a row's bits are its own
@@ -824,7 +831,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const uint64_t on = splat2(-2.f * by);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const uint64_t sl = splat2(CAP ? 1.f : BS ? A.sl * f->ks[g0 + g] * rq : RQ ? A.sl * rq : A.sl);
+                    const uint64_t sl = splat2(CAP ? 1.f : BS ? A.sl * f->ks[g0 + g] * rq : RQ ? by_row(A.sl) : A.sl);
                     uint64_t bias = pack2(by * (c - 16 * g), by * (c - 16 * g - 1));  // two keys on by one addition
 #pragma unroll
                     for (int k = 16 * g; k < 16 * g + 16; k += 2) {
@@ -885,7 +892,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll
                 for (int k = 0; k < kHalfKeys; k += 2) m4[(k >> 1) & 3] = max3f(m4[(k >> 1) & 3], x[k], x[k + 1]);
                 mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                if (RAW) mx *= RQ ? A.sl * rq : A.sl;
+                if (RAW) mx *= raw_sl;
             }
             if (!kFree && mx > m_ref + kModRescale) {  // also the row's first visible key (m_ref = -inf)
                 if (m_ref != -INFINITY) {
@@ -921,7 +928,7 @@ prefill_mod_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             uint32_t pk[32];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const uint64_t mul = splat2(RAW ? (BS ? (scaled ? 1.f : A.sl * f->ks[g0 + g] * rq) : RQ ? A.sl * rq : A.sl) : 1.f);
+                const uint64_t mul = splat2(RAW ? (BS ? (scaled ? 1.f : A.sl * f->ks[g0 + g] * rq) : raw_sl) : 1.f);
                 const uint64_t sv = splat2(BS ? f->vs[g0 + g] : 1.f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {

@@ -7,6 +7,7 @@ import torch
 import int4_reference as ref
 from test_gpu_int4_cache import _same
 from test_gpu_int4_decode import batch, check as decode_check, reference
+from test_gpu_int4_prefill import case as prefill_case, check as prefill_check
 from test_gpu_rope import BF16, F16, F32, rope_of
 
 pytestmark = pytest.mark.gpu
@@ -124,3 +125,19 @@ def test_decode_of_queries_and_scales_far_from_one(pkv, cuda_dev, gain):
     for bound in (200, 5000):
         out = pkv.pkv_paged_attention_decode_int4(q, *caches, tables, lens, scale, bound)
         decode_check(out, q, caches, reference(q, caches, tables, ctx, scale), 0.0 if gain > 1 else scale)
+
+
+@pytest.mark.parametrize("rule", ["plain", "cap", "alibi"])
+@pytest.mark.parametrize("gain", [2.0 ** -119, 2.0 ** -105, 2.0 ** 120])
+@pytest.mark.parametrize("spans", [[(0, 70), (130, 5)], [(0, 1100), (30, 200)]], ids=["fused", "widened"])
+def test_prefill_of_queries_and_scales_far_from_one(pkv, cuda_dev, spans, gain, rule):
+    q, caches, tables, starts, cu, ns = prefill_case(8, 2, 16, spans, BF16, 9)
+    rules = {"plain": {}, "cap": {"softcap": 20.0}, "alibi": {"alibi_slopes": torch.exp2(-torch.arange(1.0, 9.0)).cuda()}}[rule]
+    scale = 1e-12
+    if gain > 1:
+        q, scale = torch.zeros_like(q), 1e20
+        q[..., 5] = gain
+        caches[0][:, :, :, 0:4] = 0x88
+    else:
+        q = (q.float() * gain).to(BF16)
+    prefill_check(pkv, q, caches, tables, starts, cu, ns, spans, rules, scale)
