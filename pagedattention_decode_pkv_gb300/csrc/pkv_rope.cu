@@ -175,11 +175,14 @@ __device__ __forceinline__ uint32_t int4_word(const float (&x)[8], float s, floa
     return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
 }
 
-// w with the nibble at `shift` as the code of z under s > 0.  (Of a pair that cancels, f32 may have been off by
-// any number of codes.)
+// w with the nibble at `shift` as the code of z under s > 0: next to z / s to f32, then by the exact
+// remainder.  (Of a pair that cancels, the f32 rotation may have been off by any number of codes.)
 __device__ __noinline__ uint32_t int4_settled(uint32_t w, int shift, double z, float s) {
-    const int c = static_cast<int>(w >> shift & 15) - 8;
-    return w + (static_cast<uint32_t>(int4_code_f64(z, s) - c) << shift);
+    float c = rintf(fminf(fmaxf(static_cast<float>(z) * __frcp_rn(s), -8.f), 8.f));
+    const double r = fma(-static_cast<double>(c), static_cast<double>(s), z), h = 0.5 * s;
+    if (fabs(r) > h || (fabs(r) == h && (static_cast<int>(c) & 1))) c += r > 0.0 ? 1.f : -1.f;
+    const int to = z == z ? static_cast<int>(fminf(fmaxf(c, -7.f), 7.f)) : 0;
+    return w + (static_cast<uint32_t>(to + 8 - static_cast<int>(w >> shift & 15)) << shift);
 }
 
 // Whether x lies within `err` of the border between two codes under s.
