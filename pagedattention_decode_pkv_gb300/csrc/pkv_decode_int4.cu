@@ -57,7 +57,6 @@ namespace {
 
 constexpr int kI4MaxSeqs = 512;      // sequences of a launch (shared-memory prefix)
 constexpr int kI4MaxWarps = 152 * 16;  // working warps of a launch (sizes the workspace)
-constexpr int kI4MinSteps = 1;       // steps that a working warp takes at least
 constexpr int kI4Heads = 8;          // query heads of a unit
 // Few units (one wave) of short contexts: a CTA each, its warps meeting in shared memory, in one
 // launch without a workspace.  Against slices and the join, 32 heads over 8 KV heads, bf16, on the
@@ -212,9 +211,8 @@ decode_int4_kernel(const __grid_constant__ I4Args A) {
         }
         __syncthreads();
         const int64_t W = pref[B] * HU;
-        int64_t Cw = W / kI4MinSteps;
         const int64_t all = static_cast<int64_t>(gridDim.x) * WARPS;
-        Cw = Cw > all ? all : Cw < 1 ? 1 : Cw;
+        const int64_t Cw = W > all ? all : W < 1 ? 1 : W;  // working warps, a step each at least
         // neighbouring slices go to different SMs, so that a launch of few slices uses them all
         me = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
         if (me < Cw && W > 0) {
