@@ -686,8 +686,9 @@ PKV_API pkv_status pkv_paged_attention_decode_append_int8(void *out, const void 
  *   float16 (both to nearest even), at most 9344, so that scale * code is exact in
  *   float16; code = x / scale rounded to the nearest integer, ties to even, within +-7
  *   (NaN: 0), both from exact values; u = code + 8.  A zero scale stores zeros.  Values
- *   beyond 65408 saturate; groups whose largest magnitude is below 2^-22 become zero, and
- *   below 2^-11 the scale has fewer bits.
+ *   beyond 65408 saturate, infinities too; groups whose largest magnitude is below 7 x 2^-25
+ *   become zero, and below 7 x 2^-17 the scale, a multiple of 2^-24, has fewer bits: values
+ *   there that exceed 7 scales saturate as well.
  *
  * pkv_store_kvcache_int4: "Step 1" into a 4-bit cache: row slot_mapping[i] <- key[i] /
  *   value[i] (dtype any).  key_stride / value_stride: elements from one token to the next
@@ -737,6 +738,8 @@ typedef struct pkv_rope {
  *   PKV_ROPE_YARN    with the turns n_i = original_len f_i / 2 pi and
  *                    k_i = clamp((n_i - beta_slow) / (beta_fast - beta_slow), 0, 1):
  *                    f_i k_i + f_i / factor (1 - k_i), amplitude 0.1 ln(factor) + 1
+ *                    (a ramp over the turns; models whose ramp runs over the pair's index i
+ *                    give their frequencies to pkv_rope_turns)
  * The amplitude of the others is 1.  pkv_rope_turns (host): the table of any other
  * frequencies, inv_freq in radians per position.
  *   turns  host uint64 [rotary_dim / 2] (output), to be copied to the device
@@ -784,7 +787,7 @@ PKV_API pkv_status pkv_rope_store_kvcache_int4(void *q_out, const void *q, int64
  * what is stored; P is rounded to f16, and again times the scale of V (a weight relative to the
  * largest, times its scale, loses bits there below 2^-24 max(1, the largest scale of V)); f32
  * scores and sums.
- *   caches, scales   16-byte aligned, as are q and out
+ *   caches, scales   16-byte aligned, as are q and out; scales not negative
  *   workspace        pkv_paged_attention_decode_int4_workspace_size bytes (0 for few short
  *                    contexts), 256-byte aligned, needed during the call only; calls that may
  *                    overlap need one each
@@ -811,7 +814,9 @@ PKV_API pkv_status pkv_paged_attention_decode_int4(
  * and more, up to 1 GiB) widen the sequences' blocks once into the workspace.
  *   max_total_len  host bound on starts[b] + n_b, or 0 for the tables' width; it bounds the
  *                  workspace.  Where the call widens into it, sequences beyond the bound (rounded
- *                  up to whole blocks) are errors like those beyond their table.
+ *                  up to whole blocks) are errors like those beyond their table.  What is widened is
+ *                  every sequence's whole context, also in front of key_starts and for sequences of
+ *                  one new token: such batches are better split by max_q_len.
  *   workspace      pkv_paged_attention_prefill_int4_workspace_size bytes (may be 0), 256-byte
  *                  aligned, needed during the call only; calls that may overlap need one each
  *   scales         16-byte aligned, not negative

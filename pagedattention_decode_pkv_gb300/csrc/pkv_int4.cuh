@@ -7,12 +7,16 @@
 // u stands for scale * (u - 8), u = 1 .. 15.  A 32-bit word holds eight dims, nibbles from the
 // lowest: 0 2 4 6 1 3 5 7.  Then (w >> 4 j) & 0x000f000f is the pair of dims 2 j, 2 j + 1 in
 // the two halves of a register, and OR-ed with 0x6400 each half is the f16 1024 + u: eight
-// codes widen in nine operations, none of them a conversion.
+// codes widen in nine operations, none of them a conversion.  (The interleaved order and these
+// steps are a published method: Kim, Henry, Fahim and Awadalla, "Who Says Elephants Can't Run:
+// Bringing Large Scale MoE Models into Cloud Scale Production", 2022.)
 //
 // The scale is max|x| / 7 rounded to bf16, then to f16, at most 9344.  Its eight significant
 // bits make scale * code exact in f16 (three bits more), so that attention over the cache, the
 // rows read back and the definition agree to the bit; 7 * 9344 is the largest such value f16
 // holds.  The rounding of the scale costs nothing: codes are rounded under the stored scale.
+// Scales are multiples of 2^-24: below 2^-17 they have fewer bits, and at the first few multiples
+// the largest value may be 7.5 scales and more, which code 7 stands for.
 #pragma once
 
 #include <cuda_bf16.h>
